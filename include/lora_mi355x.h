@@ -60,6 +60,8 @@ typedef enum lora_status {
 typedef enum lora_dtype {
     LORA_F32 = 0,
     LORA_BF16 = 1,
+    LORA_E4M3 = 2,                  /* 8-bit float (1-4-3, no infinities, largest 448):
+                                       elements of a lora_kv_cache only */
     LORA_DTYPE_RANGE_MIN_ = -2147483647 - 1,  /* range markers, as above */
     LORA_DTYPE_RANGE_MAX_ = 2147483647
 } lora_dtype;
@@ -349,6 +351,182 @@ lora_status lora_apply_noalloc(const lora_meta *meta, const void *d_x, int64_t l
                                int32_t r_max, float scale, const float *d_slot_scale,
                                const int32_t *d_slot_rank, void *d_y, int64_t ldy,
                                int add_into_y, lora_mode mode, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention next to the q/k/v delta.  A layer's q/k/v projection leaves one
+ * packed row q | k | v per token (lora_apply adds the adapters' share into it);
+ * the entry points below rotate q and k, append k and v to a paged cache, and
+ * attend.  The keys and values of a request carry its adapter's delta, so
+ * cached pages may be shared by requests of one adapter only.
+ * ------------------------------------------------------------------------- */
+
+/* A paged key/value cache.  Element d of the key at position i of page p for
+ * key head h is k[p * page_stride + h * head_stride + i * pos_stride + d], and
+ * likewise in v: [page][head][position][dim], [page][position][head][dim] and
+ * k and v interleaved in one buffer are all expressed by the strides.
+ *   dtype         LORA_BF16 or LORA_E4M3 (with bf16 queries), LORA_F32 (with
+ *                 fp32 queries)
+ *   k_scale, v_scale  device fp32 [num_heads] or NULL (= 1): with LORA_E4M3 a
+ *                 stored value stands for value * scale[head]; must be NULL
+ *                 for the other types
+ * Supported: head_dim a multiple of 8 (16 with LORA_E4M3), at most 256, page_size in [1, 65536],
+ * num_pages in [1, 2^31 - 1], at most 1024 heads, strides whose byte size is a
+ * multiple of 16.  Offsets are int64. */
+typedef struct lora_kv_cache {
+    void *k, *v;
+    int64_t page_stride, head_stride, pos_stride;   /* elements, k and v alike */
+    int64_t num_pages;
+    int32_t page_size, num_heads, head_dim;
+    int32_t dtype;                  /* a lora_dtype value */
+    const float *k_scale, *v_scale;
+} lora_kv_cache;
+
+/* Rotary positions.  Pair j < rot_dim / 2 of a head is turned by the angle
+ * whose cosine and sine are table[pos][j] and table[pos][rot_dim / 2 + j]:
+ *     a' = a cos - b sin,  b' = b cos + a sin     (fp32, rounded once)
+ * with (a, b) = elements (j, j + rot_dim / 2), or (2j, 2j + 1) if interleaved;
+ * elements from rot_dim on are copied.  With num_axes = 2..4 (time, height,
+ * width of images and video) pair j takes its position from the axis whose
+ * section holds j: the first section[0] pairs from axis 0, the next section[1]
+ * from axis 1, and so on; the sections add up to rot_dim / 2 (num_axes = 1:
+ * section is not read).
+ *   table         device fp32 [num_pos][rot_dim], contiguous, 16-byte aligned
+ * rot_dim is a multiple of 16, at most head_dim. */
+typedef struct lora_rotation {
+    const float *table;
+    int64_t num_pos;
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t num_axes;
+    int32_t section[4];
+    int32_t reserved;               /* must be 0 */
+} lora_rotation;
+
+/* Rotate q and k of every token, write q to d_q and k, v to their place in the
+ * cache, in one pass.
+ *   d_qkv         device [T][ldx] of dtype (LORA_F32 or LORA_BF16): num_q_heads
+ *                 heads of q at column offset[0], cache->num_heads heads of k at
+ *                 offset[1] and of v at offset[2], head_dim columns each
+ *   offset        host int64 [3], multiples of 8
+ *   rot           NULL: no rotation (d_pos is then not read)
+ *   d_pos         device int32 [num_axes][T]
+ *   d_slot        device int64 [T]: page * page_size + position in the page, or
+ *                 -1: the token's k and v are not kept.  Two tokens of a call
+ *                 must not name one slot.
+ *   d_q           device [T][ldq] of dtype, or NULL: q is not written.  It may
+ *                 be the q columns of d_qkv themselves (in place: d_q = d_qkv +
+ *                 offset[0], ldq = ldx) and must not overlap d_qkv otherwise.
+ *   d_num_bad     device int32 or NULL: the number of bad tokens is added to it
+ * A bad token (a slot outside [-1, num_pages * page_size), or with a rotation a
+ * position outside [0, num_pos)) leaves q and the cache as they are.  E4M3
+ * values are value / scale rounded to nearest even, beyond +-448 (infinities
+ * too) +-448; NaN stays NaN.  fp32 values go to an fp32 cache, bf16 ones to a
+ * bf16 or an e4m3 cache (else LORA_ERR_UNSUPPORTED). */
+lora_status lora_cache_append(const void *d_qkv, int64_t ldx, int64_t num_tokens,
+                              lora_dtype dtype, int32_t num_q_heads,
+                              const int64_t *offset, const lora_rotation *rot,
+                              const int32_t *d_pos, const int64_t *d_slot,
+                              const lora_kv_cache *cache, void *d_q, int64_t ldq,
+                              int32_t *d_num_bad, void *stream);
+
+/* One step's batch of sequences, for lora_prepare_attn_meta.  Sequence n has
+ * the query tokens [q_start[n], q_start[n + 1]) and kv_len[n] cached keys, those
+ * of its query tokens included: query token i stands at position
+ * p = kv_len[n] - q_len + i and sees the keys j in [lo, hi) with
+ *     lo = max(0, window > 0 ? p + 1 - window : 0, key_lo ? key_lo[t] : 0)
+ *     hi = min(kv_len[n], key_hi ? key_hi[t] : kv_len[n],
+ *              max(causal ? p + 1 : kv_len[n], prefix_len ? prefix_len[n] : 0))
+ * (key_lo and key_hi, per query token, bound a document; prefix_len, per
+ * sequence, is a prefix that every token of it sees).  A token that sees no
+ * key gets zeros, and -inf as the logarithm of its sum.
+ *   d_q_start     device int32 [num_seqs + 1], non-decreasing, in [0, num_tokens]
+ *   d_kv_len      device int32 [num_seqs]
+ *   d_page_table  device int32 [num_seqs][page_table_stride]: the pages of each
+ *                 sequence's keys in order; it has to stay valid, unchanged,
+ *                 for every call that takes the metadata
+ *   max_q_len     no sequence has more query tokens (else it is bad)
+ *   groups        num_groups runs of consecutive sequences that share leading
+ *                 keys: group g holds the sequences [d_group_start[g],
+ *                 d_group_start[g + 1]) and its first d_group_len[g] keys are
+ *                 the same for all of them.  They are read once for the whole
+ *                 group, through the table of its first sequence.  num_groups
+ *                 = 0: none.
+ * A sequence is bad if its q_start leaves the bounds above, if it has more
+ * query tokens than max_q_len or than keys, or if its keys do not fit
+ * page_table_stride pages; its tokens see no key.  Supported: num_tokens <=
+ * 2^24, num_seqs <= 2^20, num_q_heads <= 1024, page_table_stride * page_size <=
+ * 2^31 - 2^16.  A group is bad, and ignored,
+ * if its bounds are not ascending in [0, num_seqs], its length is negative or
+ * beyond the keys of its first sequence.  Keys in a page whose id lies outside
+ * [0, num_pages) are not seen.  Bad sequences and groups are counted in info. */
+typedef struct lora_attn_batch {
+    const int32_t *d_q_start, *d_kv_len, *d_page_table;
+    int64_t page_table_stride;
+    int64_t num_tokens;
+    int32_t num_seqs, max_q_len;
+    int32_t num_q_heads;            /* a multiple of the cache's num_heads */
+    int32_t causal, window;
+    int32_t num_groups;
+    const int32_t *d_prefix_len;    /* [num_seqs] or NULL */
+    const int32_t *d_key_lo, *d_key_hi;   /* [num_tokens] or NULL */
+    const int32_t *d_group_start, *d_group_len;
+} lora_attn_batch;
+
+/* Attention metadata of one step: which keys every token sees, and the work
+ * list of the attention kernels.  Filled by lora_prepare_attn_meta with
+ * pointers into the caller's workspace; shared, like a lora_meta, by every
+ * layer of the step with this mask and cache geometry, and only read by them.
+ *   limits        int32 [num_tokens][4]: lo, hi, p, sequence of every token
+ *   info          int32 [16]: items of the few-row kernel, items of the
+ *                 tile kernel, bad sequences, bad groups, tokens to join,
+ *                 partial-result units, keys per item (few-row, tile), 0...
+ * The other arrays are work lists whose contents are internal. */
+typedef struct lora_attn_meta {
+    int64_t num_tokens, page_table_stride, max_units;
+    int32_t num_seqs, num_q_heads, num_kv_heads, head_dim, page_size;
+    int32_t dtype;                  /* the cache's */
+    int32_t heads_per_item, head_groups;   /* query heads of one work item; items per key head */
+    int32_t max_tiles, max_few_items, max_tile_items;
+    const int32_t *page_table;
+    int32_t *limits, *info, *tiles, *few_items, *tile_items, *join, *join_tokens;
+} lora_attn_meta;
+
+/* Device workspace of lora_prepare_attn_meta for this batch and cache (sizes
+ * only: no device array is read). */
+lora_status lora_attn_meta_workspace_bytes(const lora_attn_batch *batch,
+                                           const lora_kv_cache *cache, size_t *bytes);
+
+/* Build the attention metadata of a step (two launches).  Of the cache only
+ * num_heads, head_dim, page_size and dtype are read.  d_ws is 16-byte aligned. */
+lora_status lora_prepare_attn_meta(const lora_attn_batch *batch,
+                                   const lora_kv_cache *cache, void *d_ws,
+                                   size_t ws_bytes, lora_attn_meta *out,
+                                   void *stream);
+
+/* Device workspace of lora_attention (partial results of split key ranges);
+ * no initialisation is required. */
+lora_status lora_attention_workspace_bytes(const lora_attn_meta *meta, size_t *bytes);
+
+/* Attention of every query token over the cached keys it sees:
+ *     x[j]      = cap(scale * q . k_j) - slope[h] * |p - j|
+ *     cap(x)    = cap > 0 ? cap * tanh(x / cap) : x
+ *     lse[t][h] = log sum_j exp(x[j]),   out[t][h] = sum_j exp(x[j] - lse) v_j
+ * Query head h reads key head h / (num_q_heads / num_kv_heads).  Scores,
+ * maxima, sums and products are kept in fp32; with a bf16 or e4m3 cache the
+ * weights exp(.) are rounded to bf16 for the product with v, as the matrix
+ * cores take them.
+ *   d_q           device [T][ldq] (bf16, or fp32 with an fp32 cache): head h at
+ *                 column h * head_dim
+ *   d_out         device [T][ldo] of the same type, likewise; not overlapping q
+ *   d_slopes      device fp32 [num_q_heads] or NULL (no bias)
+ *   d_lse         device fp32 [T][num_q_heads] or NULL, contiguous
+ * Tokens outside every sequence are not written.  A non-finite key or value
+ * reaches the tokens that see it and no others.  Calls that run at the same
+ * time need workspaces of their own. */
+lora_status lora_attention(const lora_attn_meta *meta, const void *d_q, int64_t ldq,
+                           const lora_kv_cache *cache, float scale, float cap,
+                           const float *d_slopes, void *d_out, int64_t ldo,
+                           float *d_lse, void *d_ws, size_t ws_bytes, void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *lora_status_string(lora_status status);

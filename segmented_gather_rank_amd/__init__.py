@@ -30,7 +30,7 @@ if not os.path.exists(LIB_PATH):
 _cdll = C.CDLL(LIB_PATH)
 
 LORA_OK, LORA_ERR_INVALID_ARG, LORA_ERR_UNSUPPORTED, LORA_ERR_WORKSPACE, LORA_ERR_HIP = range(5)
-LORA_F32, LORA_BF16 = 0, 1
+LORA_F32, LORA_BF16, LORA_E4M3 = 0, 1, 2
 MODES = {"auto": 0, "bgmv": 1, "sgmv": 2}
 
 
@@ -52,6 +52,37 @@ class lora_meta(C.Structure):
                 ("sorted", C.c_void_p), ("sorted_slot", C.c_void_p), ("seg_slot", C.c_void_p),
                 ("seg_count", C.c_void_p),
                 ("seg_start", C.c_void_p), ("info", C.c_void_p), ("tiles", C.c_void_p)]
+
+
+class lora_kv_cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64), ("head_stride", C.c_int64),
+                ("pos_stride", C.c_int64), ("num_pages", C.c_int64), ("page_size", C.c_int32),
+                ("num_heads", C.c_int32), ("head_dim", C.c_int32), ("dtype", C.c_int32),
+                ("k_scale", C.c_void_p), ("v_scale", C.c_void_p)]
+
+
+class lora_rotation(C.Structure):
+    _fields_ = [("table", C.c_void_p), ("num_pos", C.c_int64), ("rot_dim", C.c_int32), ("interleaved", C.c_int32),
+                ("num_axes", C.c_int32), ("section", C.c_int32 * 4), ("reserved", C.c_int32)]
+
+
+class lora_attn_batch(C.Structure):
+    _fields_ = [("d_q_start", C.c_void_p), ("d_kv_len", C.c_void_p), ("d_page_table", C.c_void_p),
+                ("page_table_stride", C.c_int64), ("num_tokens", C.c_int64), ("num_seqs", C.c_int32),
+                ("max_q_len", C.c_int32), ("num_q_heads", C.c_int32), ("causal", C.c_int32),
+                ("window", C.c_int32), ("num_groups", C.c_int32), ("d_prefix_len", C.c_void_p),
+                ("d_key_lo", C.c_void_p), ("d_key_hi", C.c_void_p), ("d_group_start", C.c_void_p),
+                ("d_group_len", C.c_void_p)]
+
+
+class lora_attn_meta(C.Structure):
+    _fields_ = [("num_tokens", C.c_int64), ("page_table_stride", C.c_int64), ("max_units", C.c_int64),
+                ("num_seqs", C.c_int32), ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32),
+                ("head_dim", C.c_int32), ("page_size", C.c_int32), ("dtype", C.c_int32),
+                ("heads_per_item", C.c_int32), ("head_groups", C.c_int32), ("max_tiles", C.c_int32),
+                ("max_few_items", C.c_int32), ("max_tile_items", C.c_int32), ("page_table", C.c_void_p),
+                ("limits", C.c_void_p), ("info", C.c_void_p), ("tiles", C.c_void_p), ("few_items", C.c_void_p),
+                ("tile_items", C.c_void_p), ("join", C.c_void_p), ("join_tokens", C.c_void_p)]
 
 
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
@@ -76,6 +107,15 @@ _decl = {
     "lora_apply": ([C.POINTER(lora_meta), _p, _i64, _i64, _i32, _i32, C.POINTER(lora_weight),
                     C.POINTER(lora_weight), C.POINTER(_i64), C.POINTER(_i64), _i32, C.c_float, _p,
                     _p, _p, _i64, C.c_int, _i32, _p, _sz, _p], _i32),
+    "lora_cache_append": ([_p, _i64, _i64, _i32, _i32, C.POINTER(_i64), C.POINTER(lora_rotation), _p, _p,
+                           C.POINTER(lora_kv_cache), _p, _i64, _p, _p], _i32),
+    "lora_attn_meta_workspace_bytes": ([C.POINTER(lora_attn_batch), C.POINTER(lora_kv_cache), C.POINTER(_sz)],
+                                       _i32),
+    "lora_prepare_attn_meta": ([C.POINTER(lora_attn_batch), C.POINTER(lora_kv_cache), _p, _sz,
+                                C.POINTER(lora_attn_meta), _p], _i32),
+    "lora_attention_workspace_bytes": ([C.POINTER(lora_attn_meta), C.POINTER(_sz)], _i32),
+    "lora_attention": ([C.POINTER(lora_attn_meta), _p, _i64, C.POINTER(lora_kv_cache), C.c_float, C.c_float, _p,
+                        _p, _i64, _p, _p, _sz, _p], _i32),
 }
 
 
@@ -447,7 +487,213 @@ def lora_apply_noalloc(meta: LoraMeta, x: torch.Tensor, A, B, offsets, y: torch.
     return y
 
 
-__all__ = ["lora_apply_noalloc", "NOALLOC_SCRATCH_BYTES", "lora_abi_version", "lora_status_string", "lora_meta_workspace_bytes", "lora_prepare_meta",
+class KvCache:
+    """A paged key/value cache: k and v indexed [page][head][position][dim],
+    views of any strides with contiguous dims (a [page][position][head][dim]
+    cache is passed as its transpose(1, 2)); float32, bfloat16 or float8_e4m3fn.
+    k_scale and v_scale: float32 [heads], for float8_e4m3fn only."""
+
+    _types = {torch.float32: LORA_F32, torch.bfloat16: LORA_BF16, torch.float8_e4m3fn: LORA_E4M3}
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.stride() != v.stride():
+            raise ValueError("k and v must be [page][head][position][dim] of one shape, dtype and stride")
+        if k.stride(3) != 1:
+            raise ValueError("the dims of a head must be contiguous")
+        if k.dtype not in self._types:
+            raise TypeError(f"unsupported cache dtype {k.dtype}")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is not None and (t.dtype != torch.float32 or t.shape != (k.shape[1],) or not t.is_contiguous()):
+                raise ValueError(f"{name} must be float32 [heads]")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.num_pages, self.num_heads, self.page_size, self.head_dim = k.shape
+        # queries (and appended rows) that go with this cache
+        self.query_dtype = torch.float32 if k.dtype == torch.float32 else torch.bfloat16
+        self.c = lora_kv_cache(_dev(k, "k"), _dev(v, "v"), k.stride(0), k.stride(1), k.stride(2), self.num_pages,
+                               self.page_size, self.num_heads, self.head_dim, self._types[k.dtype],
+                               None if k_scale is None else _dev(k_scale, "k_scale"),
+                               None if v_scale is None else _dev(v_scale, "v_scale"))
+        self.ref = C.byref(self.c)
+
+
+class Rotation:
+    """Rotary positions: table float32 [num_pos][rot_dim], cosines then sines of
+    the rot_dim / 2 pairs; sections: pairs per axis (one entry or none: one axis)."""
+
+    def __init__(self, table: torch.Tensor, sections=None, interleaved: bool = False):
+        if table.dim() != 2 or table.dtype != torch.float32 or not table.is_contiguous():
+            raise ValueError("table must be contiguous float32 [num_pos][rot_dim]")
+        sections = [table.shape[1] // 2] if not sections else [int(n) for n in sections]
+        if len(sections) > 4:
+            raise ValueError("at most 4 axes")
+        self.table, self.num_axes = table, len(sections)
+        self.c = lora_rotation(_dev(table, "table"), table.shape[0], table.shape[1], int(bool(interleaved)),
+                               len(sections), (C.c_int32 * 4)(*sections), 0)
+        self.ref = C.byref(self.c)
+
+
+def lora_cache_append(qkv: torch.Tensor, cache: KvCache, slot: torch.Tensor, q_out: torch.Tensor | None = None,
+                      pos: torch.Tensor | None = None, rotation: Rotation | None = None, num_q_heads: int | None = None,
+                      offsets=None, num_bad: torch.Tensor | None = None, stream=None) -> torch.Tensor | None:
+    """Rotate q and k of the packed rows qkv [T][ldx] and write q to q_out [T][ldq]
+    and k, v to their slots (int64 [T], page * page_size + position, -1: not
+    kept) of the cache.  pos: int32 [T] or [axes][T].  offsets: columns of q, k
+    and v (default: q | k | v without gaps, num_q_heads from q_out's width or
+    from the row's)."""
+    if qkv.dim() != 2 or qkv.stride(1) != 1:
+        raise ValueError("qkv must be [T][ldx] with unit column stride")
+    if slot.dtype != torch.int64 or slot.dim() != 1 or not slot.is_contiguous() or slot.shape[0] != qkv.shape[0]:
+        raise ValueError("slot must be a contiguous int64 vector, one entry per row")
+    T, D, kvh = qkv.shape[0], cache.head_dim, cache.num_heads
+    if num_q_heads is None:
+        num_q_heads = (q_out.shape[1] if q_out is not None else qkv.shape[1] - 2 * kvh * D) // D
+    offs = (C.c_int64 * 3)(*(offsets if offsets is not None
+                             else (0, num_q_heads * D, (num_q_heads + kvh) * D)))
+    if qkv.shape[1] < max(offs[0] + num_q_heads * D, offs[1] + kvh * D, offs[2] + kvh * D):
+        raise ValueError("qkv has fewer columns than its heads need")
+    ldq = 0
+    if q_out is not None:
+        if q_out.dim() != 2 or q_out.stride(1) != 1 or q_out.shape[0] != T or q_out.dtype != qkv.dtype:
+            raise ValueError("q_out must be [T][ldq] of qkv's dtype with unit column stride")
+        if q_out.shape[1] < num_q_heads * D:
+            raise ValueError("q_out has fewer columns than its heads need")
+        ldq = q_out.stride(0) if T > 1 else q_out.shape[1]
+    if rotation is not None:
+        if pos is None or pos.dtype != torch.int32 or not pos.is_contiguous() or pos.numel() != rotation.num_axes * T:
+            raise ValueError("pos must be contiguous int32 [axes][T]")
+    if num_bad is not None and num_bad.dtype != torch.int32:
+        raise ValueError("num_bad must be int32")
+    st = _lib.lora_cache_append(
+        _dev(qkv, "qkv") if T else None, qkv.stride(0) if T > 1 else qkv.shape[1], T, _dtype(qkv), num_q_heads, offs,
+        None if rotation is None else rotation.ref, _dev(pos, "pos") if rotation is not None and T else None,
+        _dev(slot, "slot") if T else None, cache.ref, _dev(q_out, "q_out") if q_out is not None and T else None, ldq,
+        None if num_bad is None else _dev(num_bad, "num_bad"), _stream(stream))
+    _check("lora_cache_append", st)
+    return q_out
+
+
+class AttnMeta:
+    """Attention metadata of one step (see ``lora_attn_meta`` in the C header).
+    ``workspace`` owns the device arrays and ``page_table`` is read by every
+    call; keep this object alive while kernels that use it are in flight."""
+
+    def __init__(self, c: lora_attn_meta, workspace: torch.Tensor, page_table: torch.Tensor):
+        self.c, self.workspace, self.page_table = c, workspace, page_table
+        self.ref = C.byref(c)
+        b = _sz(0)
+        _check("lora_attention_workspace_bytes", _lib.lora_attention_workspace_bytes(self.ref, C.byref(b)))
+        self.attention_bytes = int(b.value)
+
+    def tensors(self) -> dict:
+        """Device int32 views of the documented arrays."""
+        def view(ptr, n):
+            off = ptr - self.workspace.data_ptr()
+            return self.workspace[off:off + 4 * n].view(torch.int32)
+        return dict(info=view(self.c.info, 16), limits=view(self.c.limits, 4 * self.c.num_tokens).view(-1, 4))
+
+
+def _attn_batch(q_start, kv_len, page_table, num_q_heads, num_tokens, max_q_len, causal, window, prefix_len, key_lo,
+                key_hi, group_start, group_len) -> lora_attn_batch:
+    N = kv_len.shape[0]
+    vectors = {"q_start": (q_start, N + 1), "kv_len": (kv_len, N), "prefix_len": (prefix_len, N),
+               "key_lo": (key_lo, num_tokens), "key_hi": (key_hi, num_tokens)}
+    if (group_start is None) != (group_len is None):
+        raise ValueError("group_start and group_len go together")
+    groups = 0 if group_len is None else group_len.shape[0]
+    if groups:
+        vectors.update(group_start=(group_start, groups + 1), group_len=(group_len, groups))
+    ptr = {}
+    for name, (t, n) in vectors.items():
+        if t is None:
+            ptr[name] = None
+            continue
+        if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or t.shape[0] != n:
+            raise ValueError(f"{name} must be a contiguous int32 vector of {n}")
+        ptr[name] = _dev(t, name)
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != N or (
+            page_table.shape[1] and page_table.stride(1) != 1):
+        raise ValueError("page_table must be int32 [sequences][pages] with contiguous rows")
+    if N > 1 and page_table.stride(0) != page_table.shape[1]:
+        raise ValueError("page_table must be contiguous")
+    return lora_attn_batch(ptr["q_start"], ptr["kv_len"], _dev(page_table, "page_table"), page_table.shape[1],
+                           num_tokens, N, num_tokens if max_q_len is None else max_q_len, num_q_heads,
+                           int(bool(causal)), int(window), groups, ptr["prefix_len"], ptr["key_lo"], ptr["key_hi"],
+                           ptr.get("group_start"), ptr.get("group_len"))
+
+
+def lora_prepare_attn_meta(q_start: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, cache: KvCache,
+                           num_q_heads: int, num_tokens: int, max_q_len: int | None = None, causal: bool = True,
+                           window: int = 0, prefix_len: torch.Tensor | None = None,
+                           key_lo: torch.Tensor | None = None, key_hi: torch.Tensor | None = None,
+                           group_start: torch.Tensor | None = None, group_len: torch.Tensor | None = None,
+                           workspace: torch.Tensor | None = None, stream=None) -> AttnMeta:
+    """Attention metadata of a batch: q_start int32 [N + 1], kv_len int32 [N],
+    page_table int32 [N][pages]; the masks and groups of ``lora_attn_batch``.
+    max_q_len: the most query tokens of a sequence (default num_tokens); a batch
+    that states it has few, as in decode, spares a launch."""
+    b = _attn_batch(q_start, kv_len, page_table, num_q_heads, num_tokens, max_q_len, causal, window, prefix_len,
+                    key_lo, key_hi, group_start, group_len)
+    need = _sz(0)
+    _check("lora_attn_meta_workspace_bytes", _lib.lora_attn_meta_workspace_bytes(C.byref(b), cache.ref, C.byref(need)))
+    if workspace is None:
+        workspace = torch.empty(int(need.value), dtype=torch.uint8, device=kv_len.device)
+    m = lora_attn_meta()
+    st = _lib.lora_prepare_attn_meta(C.byref(b), cache.ref, _dev(workspace, "workspace"), workspace.numel(),
+                                     C.byref(m), _stream(stream))
+    _check("lora_prepare_attn_meta", st)
+    return AttnMeta(m, workspace, page_table)
+
+
+def lora_attn_meta_workspace_bytes(q_start, kv_len, page_table, cache: KvCache, num_q_heads: int, num_tokens: int,
+                                   num_groups: int = 0) -> int:
+    """Bytes of lora_prepare_attn_meta's workspace for a batch of these sizes."""
+    b = lora_attn_batch(page_table_stride=page_table.shape[1], num_tokens=num_tokens, num_seqs=kv_len.shape[0],
+                        max_q_len=num_tokens, num_q_heads=num_q_heads, num_groups=num_groups)
+    need = _sz(0)
+    _check("lora_attn_meta_workspace_bytes", _lib.lora_attn_meta_workspace_bytes(C.byref(b), cache.ref, C.byref(need)))
+    return int(need.value)
+
+
+def lora_attention_workspace_bytes(meta: AttnMeta) -> int:
+    return meta.attention_bytes
+
+
+def lora_attention(meta: AttnMeta, q: torch.Tensor, cache: KvCache, out: torch.Tensor | None = None,
+                   scale: float | None = None, cap: float = 0.0, slopes: torch.Tensor | None = None,
+                   lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Attention of q [T][heads][dim] (or [T][heads * dim]) over the cached keys
+    that meta says it sees; returns out, or (out, lse) when lse (float32
+    [T][heads]) is given.  scale: default 1 / sqrt(dim); cap: tanh cap of the
+    scores (0: none); slopes: float32 [heads], bias per unit of distance."""
+    c = meta.c
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    width = c.num_q_heads * c.head_dim
+    for name, t in (("q", q), ("out", out)):
+        rows = t.shape[0] == c.num_tokens and t.dtype == cache.query_dtype and t.stride(-1) == 1
+        if not rows or (t.dim() == 2 and t.shape[1] != width) or t.dim() not in (2, 3) or (
+                t.dim() == 3 and (t.shape[1:] != (c.num_q_heads, c.head_dim) or t.stride(1) != c.head_dim)):
+            raise ValueError(f"{name} must be [T][heads][dim] or [T][heads * dim] of {cache.query_dtype}, heads contiguous")
+    if slopes is not None and (slopes.dtype != torch.float32 or slopes.shape != (c.num_q_heads,) or not slopes.is_contiguous()):
+        raise ValueError("slopes must be float32 [heads]")
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (c.num_tokens, c.num_q_heads) or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [T][heads]")
+    if workspace is None:
+        workspace = torch.empty(meta.attention_bytes, dtype=torch.uint8, device=q.device)
+    st = _lib.lora_attention(
+        meta.ref, _dev(q, "q"), q.stride(0) if c.num_tokens > 1 else width, cache.ref,
+        c.head_dim ** -0.5 if scale is None else scale, cap, None if slopes is None else _dev(slopes, "slopes"),
+        _dev(out, "out"), out.stride(0) if c.num_tokens > 1 else width, None if lse is None else _dev(lse, "lse"),
+        _dev(workspace, "workspace"), workspace.numel(), _stream(stream))
+    _check("lora_attention", st)
+    return out if lse is None else (out, lse)
+
+
+__all__ = ["KvCache", "Rotation", "AttnMeta", "lora_cache_append", "lora_prepare_attn_meta",
+           "lora_attn_meta_workspace_bytes", "lora_attention", "lora_attention_workspace_bytes", "lora_kv_cache",
+           "lora_rotation", "lora_attn_batch", "lora_attn_meta", "LORA_E4M3",
+           "lora_apply_noalloc", "NOALLOC_SCRATCH_BYTES", "lora_abi_version", "lora_status_string", "lora_meta_workspace_bytes", "lora_prepare_meta",
            "lora_moe_meta_workspace_bytes", "lora_prepare_moe_meta",
            "lora_shrink_workspace_bytes", "lora_shrink", "lora_expand", "lora_apply_workspace_bytes",
            "lora_apply_workspace_init", "apply_workspace", "apply_workspace_counters", "apply_workspace_flags",

@@ -1,0 +1,132 @@
+// lora_attn.h -- plan arithmetic and argument blocks of the paged attention
+// kernels and of the cache append.  Internal to the library (not part of the
+// ABI).  Everything marked LORA_HD is plain integer arithmetic that also
+// compiles for the host alone, where the CPU tests check it against the sizes
+// of the buffers it indexes.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIP__)
+#include <hip/hip_runtime.h>
+#define LORA_HD __host__ __device__ __forceinline__
+#else
+#define LORA_HD inline
+#endif
+
+namespace lora {
+
+// Rows (query token x query head) of one work item: the few-row kernel takes up
+// to 16 (one 16-wide matrix tile, the keys split over its waves), the tile
+// kernel up to 128 (32 per wave, the keys shared by the waves).
+constexpr int kFewRows = 16;
+constexpr int kTileQRows = 128;
+// A partial-result unit: 16 rows of one head group.
+constexpr int kUnitRows = 16;
+// Items (of all head groups) that the key ranges of one kernel are cut into at
+// most, beyond one per tile.  Measured at the kernels.
+constexpr int kFewTarget = 2048;
+constexpr int kTileTarget = 1024;
+// Shortest key range worth an item of its own.
+constexpr int kFewMinKeys = 128;
+constexpr int kTileMinKeys = 256;
+
+constexpr int kAttnTileInts = 12;  // see AttnTile
+constexpr int kAttnItemInts = 8;   // see AttnItem
+constexpr int kAttnInfoInts = 16;
+
+LORA_HD int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Query heads of a work item: the query heads of one key head, cut into equal
+// parts of at most 16 so that one token's rows always fit a few-row item.
+LORA_HD int heads_per_item(int per_kv) {
+  for (int parts = 1; parts < per_kv; ++parts)
+    if (per_kv % parts == 0 && per_kv / parts <= kFewRows) return per_kv / parts;
+  return 1;
+}
+
+// Keys per item of one kernel: the tiles' keys together cut into about
+// `target / heads` ranges, of at least `least`, in whole steps of 64.
+LORA_HD int keys_per_item(int64_t total, int heads, int target, int least) {
+  const int64_t parts = target / heads > 0 ? target / heads : 1;
+  int64_t c = ceil_div64(total, parts);
+  if (c < least) c = least;
+  c = (c + 63) & ~(int64_t)63;
+  return c > (1 << 30) ? (1 << 30) : (int)c;
+}
+
+// Capacities of the work lists, from sizes the host knows.
+struct AttnCaps {
+  int64_t tiles;      // tiles of both kernels, groups' included
+  int64_t few_items;  // items of the few-row kernel
+  int64_t tile_items;
+  int64_t units;      // partial-result units
+};
+
+// heads: head groups (items per tile and key range); group: query heads of an
+// item; tile_rows: rows of the larger tile (16 where only the few-row kernel
+// runs).  A sequence of q tokens makes ceil(q / tokens) tiles.  Cutting ranges
+// of keys_per_item keys adds at most target / heads items, and at most that
+// many tiles are cut at all.  With groups every tile may need partial results.
+LORA_HD AttnCaps attn_caps(int64_t tokens, int64_t seqs, int64_t groups, int heads, int group, int tile_rows) {
+  const int64_t per = tile_rows / group;
+  const int64_t own = seqs + tokens / per, shared = groups ? groups + tokens / per : 0;
+  const int64_t few = kFewTarget / heads + 1, big = kTileTarget / heads + 1;
+  AttnCaps c;
+  c.tiles = own + shared;
+  c.few_items = c.tiles + few;
+  c.tile_items = tile_rows > kFewRows ? c.tiles + big : 0;
+  const int64_t wide = tile_rows > kFewRows ? kTileQRows / kUnitRows : 0;
+  if (groups)
+    c.units = 2 * (ceil_div64(tokens * group, kUnitRows) + c.tiles) + few + wide * big;
+  else
+    c.units = 2 * (few + wide * big);
+  return c;
+}
+
+// One tile: rows [tok0 * group, (tok0 + ntok) * group) of every head group.
+struct AttnTile {
+  int32_t tok0, ntok, seq;    // seq: row of the page table
+  int32_t key0, key1;         // keys any of its tokens sees
+  int32_t full0, full1;       // keys all of its tokens see (full0 >= full1: none)
+  int32_t few;                // 1: few-row kernel
+  int32_t shared;             // 1: a group's shared keys; 2: the own keys of a member of a group
+  int32_t splits, unit0, pad;
+};
+
+// One item: a tile's rows on a part of its keys.  unit < 0: the result is final
+// and goes to the output; else to partial-result units unit, unit + 1, ...
+struct AttnItem {
+  int32_t tok0, ntok, seq, key0, key1, full0, full1, unit;
+};
+static_assert(sizeof(AttnTile) == 4 * kAttnTileInts && sizeof(AttnItem) == 4 * kAttnItemInts, "record sizes");
+
+// x / d for 0 <= x < 2^31 and 1 <= d <= 65536.  With m = 2^32 / d rounded up,
+// x * m / 2^32 exceeds x / d by less than x / 2^32 < 1/2, so its integer part is
+// right or one too large, which one comparison mends.
+LORA_HD uint32_t div_magic(uint32_t d) { return (uint32_t)(((1ull << 32) + d - 1) / d); }
+LORA_HD uint32_t div_by(uint32_t x, uint32_t d, uint32_t m) {
+  if (d == 1) return x;
+  uint32_t q = (uint32_t)(((uint64_t)x * m) >> 32);
+  return q - (q * d > x ? 1u : 0u);
+}
+
+// What the attention kernels know of the cache.
+struct CacheView {
+  const char *k, *v;
+  int64_t page_bytes, head_bytes, pos_bytes;
+  uint32_t num_pages, page_size, page_magic;
+  const int32_t *table;
+  int64_t table_stride;
+  const float *k_scale, *v_scale;
+};
+
+// Byte offset of position `key` of a sequence inside a head's plane, given the
+// page id its table holds; ids outside [0, num_pages) give -1.
+LORA_HD int64_t key_offset(const CacheView &c, uint32_t key, int32_t page) {
+  if ((uint32_t)page >= c.num_pages) return -1;
+  const uint32_t at = key - div_by(key, c.page_size, c.page_magic) * c.page_size;
+  return (int64_t)page * c.page_bytes + (int64_t)at * c.pos_bytes;
+}
+
+}  // namespace lora

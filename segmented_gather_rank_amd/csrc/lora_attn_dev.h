@@ -1,0 +1,116 @@
+// lora_attn_dev.h -- device helpers shared by the attention kernels.
+#pragma once
+
+#include "lora_attn_host.h"
+#include "lora_common.h"
+
+namespace lora {
+
+typedef __attribute__((__vector_size__(16 * sizeof(float)))) float f32x16;
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) i16x4 *lds_i16x4_ptr;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Four keys of one column: lane l of a 16-lane group gives the address of row
+// l / 4, columns 4 (l % 4) .. + 3, and receives column l of the group's 4 rows.
+__device__ __forceinline__ u32x2 lds_read_tr(const uint16_t *p) {
+  return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4_ptr)(p)));
+}
+
+// Two e4m3 values (half of a 32-bit word) as a bf16 pair; exact.
+__device__ __forceinline__ u32x4 e4m3x8_to_bf16(uint32_t lo, uint32_t hi) {
+  u32x4 r;
+  r[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, false));
+  r[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, 1.0f, true));
+  r[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, false));
+  r[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, 1.0f, true));
+  return r;
+}
+
+// Whether any of 8 bf16 values is infinite or NaN.
+__device__ __forceinline__ bool any_nonfinite(u32x4 v) {
+  bool bad = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) bad |= (v[i] & 0x7f80u) == 0x7f80u || (v[i] & 0x7f800000u) == 0x7f800000u;
+  return bad;
+}
+
+// A weight of zero does not hide an infinite or NaN value: 0 * inf = NaN would
+// reach the rows that do not see the key.  Where a step has both hidden keys and
+// such values its products with V run three times: with those values as zeros,
+// and with 1 for a seen key against 1 for a +inf (-inf) value, NaN counting as
+// both.  A positive count adds that infinity.
+enum VPart { kVFinite = 0, kVPosInf = 1, kVNegInf = 2 };
+__device__ __forceinline__ u32x4 v_part(u32x4 v, int part) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t x = (v[i] >> (16 * h)) & 0xffffu, mag = x & 0x7fffu;
+      uint32_t y;
+      if (part == kVFinite) y = mag >= 0x7f80u ? 0u : x;
+      else if (part == kVPosInf) y = x == 0x7f80u || mag > 0x7f80u ? 0x3f80u : 0u;
+      else y = x == 0xff80u || mag > 0x7f80u ? 0x3f80u : 0u;
+      w |= y << (16 * h);
+    }
+    r[i] = w;
+  }
+  return r;
+}
+__device__ __forceinline__ float add_counted_infs(float o, float pos, float neg) {
+  if (pos > 0.f) o += __builtin_inff();
+  if (neg > 0.f) o -= __builtin_inff();
+  return o;
+}
+
+// Scores to base-2 logits.  Plain: the factor alone.  General: cap * tanh(x /
+// cap) with tanh(y) = 1 - 2 / (exp(2y) + 1) (absolute error about 1e-7, so the
+// score is off by cap * 1e-7), then the distance bias.
+struct ScoreArgs {
+  float mul;        // scale * k_scale (general), times log2 e (plain)
+  float cap, two_over_cap;  // two_over_cap = 2 log2(e) / cap
+  float slope;      // of this lane's row
+};
+template <bool GENERAL>
+__device__ __forceinline__ float logit2(const ScoreArgs &s, float dot, int distance) {
+  float x = dot * s.mul;
+  if constexpr (GENERAL) {
+    if (s.cap > 0.f) {
+      const float e = exp2_fast(x * s.two_over_cap);
+      x = s.cap - 2.f * s.cap * __builtin_amdgcn_rcpf(e + 1.f);
+    }
+    x = (x - s.slope * fabsf((float)distance)) * kLog2e;
+  }
+  return x;
+}
+template <bool GENERAL>
+__device__ __forceinline__ ScoreArgs score_args(const AttnArgs &a, int kvh, int q_head) {
+  ScoreArgs s;
+  const float ks = a.cache.k_scale ? a.cache.k_scale[kvh] : 1.f;
+  s.mul = a.scale * ks * (GENERAL ? 1.f : kLog2e);
+  s.cap = a.cap;
+  s.two_over_cap = GENERAL && a.cap > 0.f ? 2.f * kLog2e / a.cap : 0.f;
+  s.slope = GENERAL && a.slopes ? a.slopes[q_head] : 0.f;
+  return s;
+}
+
+__device__ __forceinline__ AttnItem load_item(const int32_t *items, int i) {
+  // uniform index: scalar loads
+  const int32_t *p = items + (int64_t)i * kAttnItemInts;
+  return AttnItem{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
+}
+
+// Row `row` (of kUnitRows) of partial-result unit `unit`, head group h.
+__device__ __forceinline__ int64_t part_row(const AttnArgs &a, int64_t unit, int h, int row) {
+  return (unit * a.heads + h) * kUnitRows + row;
+}
+
+}  // namespace lora

@@ -1,0 +1,513 @@
+// lora_attn_few.hip -- attention of up to 16 rows (query token x query head of
+// one key head) over a range of cached keys: decode, short extensions, and every
+// fp32 call.  And the kernel that joins partial results.
+//
+// With the rows of one key head as the columns of a matrix product, the scores
+// of 16 keys are S^T = K Q^T (16 x 16, contracted over the head dimension) and
+// the output is O^T += V^T P^T (dim x 16, contracted over the keys).  A lane's
+// column is then one row from beginning to end: its running maximum and sum, its
+// weights and its part of O stay in that lane, and the scores that a product
+// leaves in a lane (keys 4g .. 4g + 3 of each 16, g the lane's group of 16) are
+// the operand of the next product if V is taken in the same key order, which the
+// transposing LDS read does.  No weight ever leaves its lane.
+//
+// Bound: the keys and values are read once and used by at most 16 rows, 16 / 2
+// operations per byte, so HBM bounds it.  Hence no sharing: each of the 4 waves
+// takes every fourth step of 32 keys with a softmax of its own, K goes from
+// global memory straight into operand registers, V through LDS that only its
+// wave touches (for the transposition), the next step's 16 loads of 16 bytes a
+// lane are in flight while a step is computed, and page ids are fetched two
+// steps ahead.  The waves meet once, at the end.
+#include "lora_attn_dev.h"
+
+namespace lora {
+
+namespace {
+
+constexpr int kStep = 32;  // keys per wave and step
+
+// The waves' maxima, sums and outputs combined; thread tid holds row tid / 16.
+// o_lds: [4] regions of `region` bytes, each float [16][DP + 4].
+template <int DP, typename OUT>
+__device__ __forceinline__ void finish_few(const AttnArgs &a, const AttnItem &it, int h, const char *o_lds,
+                                           int region, const float (*ml)[16][2]) {
+  const int row = threadIdx.x / 16, j = threadIdx.x % 16;
+  if (row >= it.ntok * a.group) return;
+  float m = ml[0][row][0];
+#pragma unroll
+  for (int w = 1; w < 4; ++w) m = fmaxf(m, ml[w][row][0]);
+  const float base = m == kNegInf ? 0.f : m;
+  float f[4], l = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    f[w] = exp2_fast(ml[w][row][0] - base);
+    l += f[w] * ml[w][row][1];
+  }
+  const int t = it.tok0 + row / a.group, qh = h * a.group + row % a.group;
+  const float vs = a.cache.v_scale ? a.cache.v_scale[h / a.kv_parts] : 1.f;
+  const float mul = it.unit >= 0 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));
+  const int64_t pr = it.unit >= 0 ? part_row(a, it.unit, h, row) : 0;
+#pragma unroll
+  for (int q = 0; q < DP / 64; ++q) {
+    const int d = 64 * q + 4 * j;
+    if (d >= a.dim) break;
+    float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const f32x4 v = *reinterpret_cast<const f32x4 *>(o_lds + w * region + (row * (DP + 4) + d) * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += f[w] * v[i];
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul == 0.f ? 0.f : o[i] * mul;
+    if (it.unit >= 0) {
+      gstore16f(a.part + pr * a.dim + d, f32x4{o[0], o[1], o[2], o[3]});
+    } else if constexpr (sizeof(OUT) == 4) {
+      gstore16f(a.out + 4 * (t * a.ldo + (int64_t)qh * a.dim + d), f32x4{o[0], o[1], o[2], o[3]});
+    } else {
+      typedef __attribute__((address_space(1))) u32x2 g_u32x2;
+      *(g_u32x2 *)(a.out + 2 * (t * a.ldo + (int64_t)qh * a.dim + d)) =
+          u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+    }
+  }
+  if (j == 0) {
+    if (it.unit >= 0) {
+      a.part_ml[2 * pr] = m;
+      a.part_ml[2 * pr + 1] = l;
+    } else if (a.lse) {
+      a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+    }
+  }
+}
+
+// DP: head dimension rounded up to 64, 128 or 256 (dimensions past a.dim are
+// zeros).  FP8: e4m3 cache, widened to bf16 (exactly) on the way in.
+template <int DP, bool FP8, bool GENERAL>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_kernel(AttnArgs a) {
+  constexpr int KS = DP / 32;                   // k-steps of a score product
+  constexpr int LDV = DP + 16;                  // V row in LDS: 8 consecutive rows cover all 64 banks
+  constexpr int CPR = FP8 ? DP / 16 : DP / 8;   // 16-byte pieces of a V row
+  constexpr int VROWS = 64 / CPR;               // V rows per load of the wave
+  constexpr int NV = kStep / VROWS;
+  constexpr int KL = FP8 ? KS / 2 : KS;         // 16-byte loads of one key's share of a lane
+  constexpr int REGION = kStep * LDV * 2;
+  static_assert(REGION >= 16 * (DP + 4) * 4, "the waves' outputs reuse the V rows");
+  __shared__ __align__(16) char lds[4 * REGION];
+  __shared__ float ml_lds[4][16][2];
+
+  const int h = blockIdx.x % a.heads, index = blockIdx.x / a.heads;
+  if (index >= a.info[0]) return;
+  const AttnItem it = load_item(a.items, index);
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = lane / 16, c = lane % 16;
+  const int kvh = h / a.kv_parts;
+  const bool row_ok = c < it.ntok * a.group;
+  const int tok = it.tok0 + (row_ok ? c / a.group : 0), qh = h * a.group + (row_ok ? c % a.group : 0);
+
+  // page ids of a step: lane j looks up key j (both halves of the wave alike)
+  const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
+  auto page_of = [&](int step) -> int32_t {
+    const int key = it.key0 + step * kStep + lane % kStep;
+    return key < it.key1 ? table[div_by(key, a.cache.page_size, a.cache.page_magic)] : -1;
+  };
+  const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
+  const int nsteps = (it.key1 - it.key0 + kStep - 1) / kStep;
+
+  int32_t page = page_of(wave);
+  int32_t page_next = page_of(wave + 4);
+
+  // Q: this row's share of the dimensions, in the order the K loads deliver them
+  bf16x8 q[KS];
+  bool k_ok[KL];
+#pragma unroll
+  for (int s = 0; s < KS; ++s) {
+    const int d = FP8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
+    u32x4 w = {0, 0, 0, 0};
+    if (row_ok && d < a.dim) w = gload16(a.q + 2 * (tok * a.ldq + (int64_t)qh * a.dim + d));
+    q[s] = __builtin_bit_cast(bf16x8, w);
+    if (FP8 ? s % 2 == 0 : true) k_ok[FP8 ? s / 2 : s] = d < a.dim;
+  }
+  int lo = 0, hi = 0, pos = 0;
+  if (row_ok) {
+    const int4 v = reinterpret_cast<const int4 *>(a.limits)[tok];
+    lo = v.x, hi = v.y, pos = v.z;
+  }
+  const ScoreArgs sc = score_args<GENERAL>(a, kvh, qh);
+
+  u32x4 kr[2][KL], vr[NV];
+  int64_t off = -1;  // of key (lane % 32), or -1: beyond the range or in a bad page
+  auto issue = [&](int step, int32_t pid) {
+    off = key_offset(a.cache, it.key0 + step * kStep + lane % kStep, pid);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int64_t o = max((int64_t)0, __shfl(off, 16 * t + c));
+#pragma unroll
+      for (int s = 0; s < KL; ++s)
+        kr[t][s] = gload16(k_head + o + (k_ok[s] ? (FP8 ? 64 * s + 16 * g : 2 * (32 * s + 8 * g)) : 0));
+    }
+    const int vc = lane % CPR;
+    const int vcol = 16 * vc < a.dim * (FP8 ? 1 : 2) ? 16 * vc : 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t o = max((int64_t)0, __shfl(off, VROWS * i + lane / CPR));
+      vr[i] = gload16(v_head + o + vcol);
+    }
+  };
+
+  float m = kNegInf, l = 0.f;
+  f32x4 o[DP / 16];
+#pragma unroll
+  for (int d = 0; d < DP / 16; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint16_t *vl = reinterpret_cast<uint16_t *>(lds + wave * REGION);
+
+  if (wave < nsteps) issue(wave, page);
+  for (int step = wave; step < nsteps; step += 4) {
+    const int k0 = it.key0 + step * kStep;
+    // ---- scores
+    f32x4 st[2];
+    const bool ragged_dim = a.dim < DP;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < KL; ++s) {
+        u32x4 w = kr[t][s];
+        if (ragged_dim && !k_ok[s]) w = u32x4{0, 0, 0, 0};
+        if constexpr (FP8) {
+          st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e4m3x8_to_bf16(w[0], w[1])),
+                                                          q[2 * s], st[t], 0, 0, 0);
+          st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e4m3x8_to_bf16(w[2], w[3])),
+                                                          q[2 * s + 1], st[t], 0, 0, 0);
+        } else {
+          st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), q[s], st[t], 0, 0, 0);
+        }
+      }
+    }
+    // ---- V to LDS; rows beyond the range or in a bad page as zeros
+    const bool all_keys = __all(off >= 0);
+    const bool masked = !all_keys || k0 < it.full0 || k0 + kStep > it.full1;
+    bool poison = false;
+    const int64_t off_now = off;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      u32x4 w = vr[i];
+      if (!all_keys && __shfl(off_now, VROWS * i + lane / CPR) < 0) w = u32x4{0, 0, 0, 0};
+      uint16_t *p = vl + (VROWS * i + lane / CPR) * LDV + (lane % CPR) * (FP8 ? 16 : 8);
+      if constexpr (FP8) {
+        const u32x4 w0 = e4m3x8_to_bf16(w[0], w[1]), w1 = e4m3x8_to_bf16(w[2], w[3]);
+        if (masked) poison |= any_nonfinite(w0) || any_nonfinite(w1);
+        *reinterpret_cast<u32x4 *>(p) = w0;
+        *reinterpret_cast<u32x4 *>(p + 8) = w1;
+      } else {
+        if (masked) poison |= any_nonfinite(w);
+        *reinterpret_cast<u32x4 *>(p) = w;
+      }
+    }
+    poison = __any(poison);
+    // which of this lane's keys are in a good page (bit 4 t + i)
+    uint32_t see = 0xff;
+    if (masked) {
+      see = 0;
+      const uint64_t good = __ballot(off_now >= 0);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 16 * t + 4 * g + i, key = k0 + j;
+          if (key >= lo && key < hi && key < it.key1 && ((good >> j) & 1)) see |= 1u << (4 * t + i);
+        }
+    }
+    // ---- the next step's loads
+    if (step + 4 < nsteps) {
+      issue(step + 4, page_next);
+      page_next = page_of(step + 8);
+    }
+    // ---- softmax
+    float top = m;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float x = logit2<GENERAL>(sc, st[t][i], pos - (k0 + 16 * t + 4 * g + i));
+        if (masked && !((see >> (4 * t + i)) & 1)) x = kNegInf;
+        st[t][i] = x;
+        top = fmaxf(top, x);
+      }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float base = top == kNegInf ? 0.f : top;
+    const float fade = exp2_fast(m - base);
+    m = top;
+    l *= fade;
+    u32x4 pw;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        st[t][i] = exp2_fast(st[t][i] - base);
+        l += st[t][i];
+      }
+      pw[2 * t] = pack_bf16x2(st[t][0], st[t][1]);
+      pw[2 * t + 1] = pack_bf16x2(st[t][2], st[t][3]);
+    }
+    const bf16x8 p = __builtin_bit_cast(bf16x8, pw);
+    // ---- O^T = fade O^T + V^T P^T
+    auto v_operand = [&](int d) {
+      const uint16_t *b = vl + (4 * g + c / 4) * LDV + 16 * d + 4 * (c % 4);
+      const u32x2 v0 = lds_read_tr(b), v1 = lds_read_tr(b + 16 * LDV);
+      return u32x4{v0.x, v0.y, v1.x, v1.y};
+    };
+#pragma unroll
+    for (int d = 0; d < DP / 16; ++d) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] *= fade;
+    }
+    if (__builtin_expect(!poison, 1)) {
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d)
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_operand(d)), p, o[d], 0, 0, 0);
+    } else {
+      u32x4 seen;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        seen[i] = ((see >> (2 * i)) & 1 ? 0x3f80u : 0u) | ((see >> (2 * i + 1)) & 1 ? 0x3f800000u : 0u);
+      const bf16x8 sb = __builtin_bit_cast(bf16x8, seen);
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d) {
+        const u32x4 v = v_operand(d);
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_part(v, kVFinite)), p, o[d], 0, 0, 0);
+        const f32x4 pi = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_part(v, kVPosInf)), sb, zero, 0, 0, 0);
+        const f32x4 ni = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_part(v, kVNegInf)), sb, zero, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] = add_counted_infs(o[d][i], pi[i], ni[i]);
+      }
+    }
+  }
+
+  // ---- the waves' results
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    ml_lds[wave][c][0] = m;
+    ml_lds[wave][c][1] = l;
+  }
+  float *ol = reinterpret_cast<float *>(lds + wave * REGION);
+#pragma unroll
+  for (int d = 0; d < DP / 16; ++d) *reinterpret_cast<f32x4 *>(ol + c * (DP + 4) + 16 * d + 4 * g) = o[d];
+  __syncthreads();
+  finish_few<DP, uint16_t>(a, it, h, lds, REGION, ml_lds);
+}
+
+// fp32 queries and cache: the same products with v_mfma_f32_16x16x4_f32 (one
+// value of each operand a lane), 16 keys per wave and step.  Every call with an
+// fp32 cache comes here, in tiles of 16 rows.
+template <int DP, bool GENERAL>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(AttnArgs a) {
+  constexpr int NC = DP / 16;  // 16-byte loads of one key's share of a lane
+  constexpr int REGION = 16 * (DP + 4) * 4;
+  __shared__ __align__(16) char lds[4 * REGION];
+  __shared__ float ml_lds[4][16][2];
+
+  const int h = blockIdx.x % a.heads, index = blockIdx.x / a.heads;
+  if (index >= a.info[0]) return;
+  const AttnItem it = load_item(a.items, index);
+  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = lane / 16, c = lane % 16;
+  const int kvh = h / a.kv_parts;
+  const bool row_ok = c < it.ntok * a.group;
+  const int tok = it.tok0 + (row_ok ? c / a.group : 0), qh = h * a.group + (row_ok ? c % a.group : 0);
+  const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
+  const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
+  const int nsteps = (it.key1 - it.key0 + 15) / 16;
+
+  f32x4 q[NC];
+#pragma unroll
+  for (int s = 0; s < NC; ++s) {
+    const int d = 16 * s + 4 * g;
+    q[s] = row_ok && d < a.dim ? gload16f(a.q + 4 * (tok * a.ldq + (int64_t)qh * a.dim + d)) : f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  int lo = 0, hi = 0, pos = 0;
+  if (row_ok) {
+    const int4 v = reinterpret_cast<const int4 *>(a.limits)[tok];
+    lo = v.x, hi = v.y, pos = v.z;
+  }
+  const ScoreArgs sc = score_args<GENERAL>(a, kvh, qh);
+
+  float m = kNegInf, l = 0.f;
+  f32x4 o[NC];
+#pragma unroll
+  for (int d = 0; d < NC; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int step = wave; step < nsteps; step += 4) {
+    const int k0 = it.key0 + step * 16;
+    const int key_c = k0 + c;
+    const int32_t page = key_c < it.key1 ? table[div_by(key_c, a.cache.page_size, a.cache.page_magic)] : -1;
+    const int64_t off = key_offset(a.cache, key_c, page);
+    const uint64_t good = __ballot(off >= 0);
+    f32x4 kr[NC];
+#pragma unroll
+    for (int s = 0; s < NC; ++s) {
+      const int d = 16 * s + 4 * g;
+      kr[s] = d < a.dim ? gload16f(k_head + max((int64_t)0, off) + 4 * d) : f32x4{0.f, 0.f, 0.f, 0.f};
+    }
+    // V of keys 4g + i: column c of every 16 dimensions
+    float vr[4][NC];
+    bool poison = false;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t ov = __shfl(off, 4 * g + i);
+#pragma unroll
+      for (int d = 0; d < NC; ++d) {
+        vr[i][d] = ov >= 0 && 16 * d + c < a.dim
+                       ? *(const __attribute__((address_space(1))) float *)(v_head + ov + 4 * (16 * d + c))
+                       : 0.f;
+        poison |= !(fabsf(vr[i][d]) < __builtin_inff());
+      }
+    }
+    f32x4 st = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < NC; ++s)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) st = __builtin_amdgcn_mfma_f32_16x16x4f32(kr[s][e], q[s][e], st, 0, 0, 0);
+    float top = m, seen[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * g + i, key = k0 + j;
+      const bool see = key >= lo && key < hi && key < it.key1 && ((good >> j) & 1);
+      seen[i] = see ? 1.f : 0.f;
+      float x = st[i] * sc.mul;
+      if constexpr (GENERAL) {
+        if (sc.cap > 0.f) x = sc.cap * tanhf(x / sc.cap);
+        x = (x - sc.slope * fabsf((float)(pos - key))) * kLog2e;
+      }
+      st[i] = see ? x : kNegInf;
+      top = fmaxf(top, st[i]);
+    }
+    top = fmaxf(top, __shfl_xor(top, 16));
+    top = fmaxf(top, __shfl_xor(top, 32));
+    const float base = top == kNegInf ? 0.f : top;
+    const float fade = exp2_fast(m - base);
+    m = top;
+    l *= fade;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      st[i] = exp2_fast(st[i] - base);
+      l += st[i];
+    }
+    const bool bad = __any(poison);
+#pragma unroll
+    for (int d = 0; d < NC; ++d) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[d][i] *= fade;
+      if (__builtin_expect(!bad, 1)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(vr[i][d], st[i], o[d], 0, 0, 0);
+      } else {
+        f32x4 pi = {0.f, 0.f, 0.f, 0.f}, ni = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float v = vr[i][d], inf = __builtin_inff();
+          const bool nan = v != v;
+          o[d] = __builtin_amdgcn_mfma_f32_16x16x4f32(nan || fabsf(v) == inf ? 0.f : v, st[i], o[d], 0, 0, 0);
+          pi = __builtin_amdgcn_mfma_f32_16x16x4f32(nan || v == inf ? 1.f : 0.f, seen[i], pi, 0, 0, 0);
+          ni = __builtin_amdgcn_mfma_f32_16x16x4f32(nan || v == -inf ? 1.f : 0.f, seen[i], ni, 0, 0, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] = add_counted_infs(o[d][i], pi[i], ni[i]);
+      }
+    }
+  }
+  l += __shfl_xor(l, 16);
+  l += __shfl_xor(l, 32);
+  if (g == 0) {
+    ml_lds[wave][c][0] = m;
+    ml_lds[wave][c][1] = l;
+  }
+  float *ol = reinterpret_cast<float *>(lds + wave * REGION);
+#pragma unroll
+  for (int d = 0; d < NC; ++d) *reinterpret_cast<f32x4 *>(ol + c * (DP + 4) + 16 * d + 4 * g) = o[d];
+  __syncthreads();
+  finish_few<DP, float>(a, it, h, lds, REGION, ml_lds);
+}
+
+// Rows whose result lies in parts: one wave per (token, query head) adds the
+// parts of its group's shared keys and of its own, weighted by their sums, in
+// the order of the keys.
+template <typename OUT>
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  const int lane = threadIdx.x % kWave;
+  const int64_t rows = (int64_t)a.info[4] * a.q_heads;
+  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; r < rows; r += (int64_t)gridDim.x * 4) {
+    const int t = __builtin_amdgcn_readfirstlane(a.join_tokens[r / a.q_heads]);
+    const int qh = __builtin_amdgcn_readfirstlane((int)(r % a.q_heads));
+    const int h = qh / a.group;
+    const int4 own = reinterpret_cast<const int4 *>(a.join)[2 * (int64_t)t];
+    const int4 pre = reinterpret_cast<const int4 *>(a.join)[2 * (int64_t)t + 1];
+    const int n = own.y + pre.y;
+    auto row_of = [&](int p) -> int64_t {
+      const bool shared = p < pre.y;
+      const int4 rec = shared ? pre : own;
+      const int row = rec.w * a.group + qh % a.group;
+      return part_row(a, rec.x + (int64_t)(shared ? p : p - pre.y) * rec.z + row / kUnitRows, h, row % kUnitRows);
+    };
+    // the parts' maxima, 64 at a time
+    float m = kNegInf;
+    for (int p0 = 0; p0 < n; p0 += kWave)
+      if (p0 + lane < n) m = fmaxf(m, a.part_ml[2 * row_of(p0 + lane)]);
+#pragma unroll
+    for (int x = 1; x < kWave; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
+    const float base = m == kNegInf ? 0.f : m;
+    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    const int d = 4 * lane;
+    for (int p = 0; p < n; ++p) {
+      const int64_t pr = row_of(p);
+      const float f = exp2_fast(a.part_ml[2 * pr] - base);
+      l += f * a.part_ml[2 * pr + 1];
+      if (d < a.dim) {
+        const f32x4 v = gload16f(a.part + pr * a.dim + d);
+        // a part without seen keys holds zeros
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += f * v[i];
+      }
+    }
+    const float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = mul == 0.f ? 0.f : o[i] * mul;
+    if (d < a.dim) {
+      const int64_t at = t * a.ldo + (int64_t)qh * a.dim + d;
+      if constexpr (sizeof(OUT) == 4) {
+        gstore16f(a.out + 4 * at, f32x4{o[0], o[1], o[2], o[3]});
+      } else {
+        typedef __attribute__((address_space(1))) u32x2 g_u32x2;
+        *(g_u32x2 *)(a.out + 2 * at) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+      }
+    }
+    if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+  }
+}
+
+template <int DP, bool GENERAL>
+void start_few(const AttnArgs &a, AttnKind kind, dim3 grid, hipStream_t s) {
+  if (kind == kAttnF32) attn_few_f32_kernel<DP, GENERAL><<<grid, dim3(256), 0, s>>>(a);
+  else if (kind == kAttnE4m3) attn_few_kernel<DP, true, GENERAL><<<grid, dim3(256), 0, s>>>(a);
+  else attn_few_kernel<DP, false, GENERAL><<<grid, dim3(256), 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_attn_few(const AttnArgs &a, AttnKind kind, hipStream_t s) {
+  const dim3 grid((unsigned)((int64_t)a.max_items * a.heads));
+  const bool general = a.cap > 0.f || a.slopes;
+  if (a.dim <= 64) general ? start_few<64, true>(a, kind, grid, s) : start_few<64, false>(a, kind, grid, s);
+  else if (a.dim <= 128) general ? start_few<128, true>(a, kind, grid, s) : start_few<128, false>(a, kind, grid, s);
+  else general ? start_few<256, true>(a, kind, grid, s) : start_few<256, false>(a, kind, grid, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_attn_join(const AttnArgs &a, AttnKind kind, hipStream_t s) {
+  const int64_t blocks = (a.tokens * a.q_heads + 3) / 4;
+  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048));
+  if (kind == kAttnF32) attn_join_kernel<float><<<grid, dim3(256), 0, s>>>(a);
+  else attn_join_kernel<uint16_t><<<grid, dim3(256), 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace lora

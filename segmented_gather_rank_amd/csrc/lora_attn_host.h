@@ -1,0 +1,62 @@
+// lora_attn_host.h -- argument blocks and launchers of the attention and append
+// kernels, shared by their translation units.  Internal to the library.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include "lora_attn.h"
+
+namespace lora {
+
+struct AttnPlanArgs {
+  const int32_t *q_start, *kv_len, *prefix_len, *key_lo, *key_hi, *group_start, *group_len;
+  int64_t tokens, table_stride;
+  int32_t seqs, groups, max_q_len, page_size, causal, window;
+  int32_t heads, group, tile_rows;
+  int32_t max_tiles, max_few_items, max_tile_items, max_units;
+  int32_t *limits, *info, *tiles, *few_items, *tile_items, *join, *join_tokens, *seq_base, *group_base;
+};
+hipError_t launch_attn_plan(const AttnPlanArgs &a, hipStream_t s);
+
+struct AttnArgs {
+  CacheView cache;
+  const char *q;
+  char *out;
+  float *lse;                // [T][q_heads] or NULL
+  const float *slopes;       // [q_heads] or NULL
+  const int32_t *limits, *info, *items, *join, *join_tokens;
+  int64_t ldq, ldo, tokens;  // elements
+  float *part;               // partial results: see part_row
+  float *part_ml;
+  float scale, cap;
+  int32_t heads, group, q_heads, kv_parts, dim;  // kv_parts: head groups per key head
+  int32_t max_items;
+};
+
+// Kind of the cache's elements (and with it of q and out).
+enum AttnKind { kAttnBf16 = 0, kAttnE4m3 = 1, kAttnF32 = 2 };
+
+hipError_t launch_attn_few(const AttnArgs &a, AttnKind kind, hipStream_t s);
+hipError_t launch_attn_tile(const AttnArgs &a, AttnKind kind, hipStream_t s);
+hipError_t launch_attn_join(const AttnArgs &a, AttnKind kind, hipStream_t s);
+
+struct AppendArgs {
+  const char *x;
+  char *q, *k, *v;
+  int64_t ldx, ldq, tokens;        // elements
+  int64_t off_q, off_k, off_v;     // columns
+  int64_t page_stride, head_stride, pos_stride;  // elements
+  int64_t num_slots;
+  const int64_t *slot;
+  const int32_t *pos;
+  const float *table;
+  int64_t num_pos;
+  const float *k_scale, *v_scale;
+  int32_t *num_bad;
+  int32_t q_heads, kv_heads, dim, page_size, half, axes, interleaved;
+  int32_t axis_end[4];
+  uint32_t unit_magic[3];          // div_magic of the units per head: turned, copied, v
+};
+hipError_t launch_append(const AppendArgs &a, AttnKind kind, hipStream_t s);
+
+}  // namespace lora
