@@ -23,69 +23,88 @@ namespace lora {
 namespace {
 
 constexpr int kKeys = 64;  // keys per tile
+// The running maximum that the weights refer to is only raised when a score
+// exceeds it by more than 2^kSlack: the weights stay below 2^kSlack and their
+// sum and O are exact up to that factor, while O, half of a wave's registers, is
+// hardly ever rescaled.
+constexpr float kSlack = 8.f;
 
-template <int DP, bool FP8, bool GENERAL>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnArgs a) {
-  constexpr int KS = DP / 16;                  // k-steps of a score product
-  constexpr int DT = DP / 32;                  // 32-row tiles of O^T
-  constexpr int LDK = DP + 8, LDV = DP + 16;   // LDS rows (elements): no bank conflicts
-  constexpr int CPR = FP8 ? DP / 16 : DP / 8;  // 16-byte pieces of a cached row
-  constexpr int ROWS = 256 / CPR;              // rows per load of the workgroup
-  constexpr int NL = kKeys / ROWS;             // loads per thread, K and V each
-  constexpr int BUF = kKeys * (LDK + LDV);
-  __shared__ __align__(16) uint16_t lds[2 * BUF];
-  __shared__ int flag_lds[4];
+template <int DP, bool FP8>
+struct TileShape {
+  static constexpr int KS = DP / 16;                  // k-steps of a score product
+  static constexpr int DT = DP / 32;                  // 32-row tiles of O^T
+  static constexpr int LDK = DP + 8, LDV = DP + 16;   // LDS rows (elements): no bank conflicts
+  static constexpr int CPR = FP8 ? DP / 16 : DP / 8;  // 16-byte pieces of a cached row
+  static constexpr int ROWS = 256 / CPR;              // rows per load of the workgroup
+  static constexpr int NL = kKeys / ROWS;             // loads per thread, K and V each
+  static constexpr int BUF = kKeys * (LDK + LDV);
+};
 
-  const int h = blockIdx.x % a.heads, index = a.info[1] - 1 - (int)(blockIdx.x / a.heads);
-  if (index < 0) return;
-  const AttnItem it = load_item(a.items, index);
+// One item.  CAREFUL = false supposes that every key of the range lies in a page
+// of the cache and that no tile with hidden keys holds an infinite or NaN value;
+// it returns true, with nothing written, when it met either, and the item is
+// then done again with CAREFUL = true, which supposes nothing.  (One loop with
+// both costs the usual case a third of its registers.)
+template <int DP, bool FP8, bool GENERAL, bool CAREFUL>
+__device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, int h, uint16_t *lds, int *flag_lds) {
+  using S = TileShape<DP, FP8>;
   const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, g = lane / 32, c = lane % 32;
   const int kvh = h / a.kv_parts;
-  const int row = 32 * wave + c;
-  const bool row_ok = row < it.ntok * a.group;
+  const int row = 32 * wave + c, rows = it.ntok * a.group;
+  const bool row_ok = row < rows;
   const int tok = it.tok0 + (row_ok ? row / a.group : 0), qh = h * a.group + (row_ok ? row % a.group : 0);
-  const bool wave_ok = 32 * wave < it.ntok * a.group;
+  const bool wave_ok = 32 * wave < rows;
 
   const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
   const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
   const int ntiles = (it.key1 - it.key0 + kKeys - 1) / kKeys;
-  const int piece = tid % CPR, lrow = tid / CPR;
+  const int piece = tid % S::CPR, lrow = tid / S::CPR;
   const bool piece_ok = piece * (FP8 ? 16 : 8) < a.dim;
   const int col = piece_ok ? 16 * piece : 0;
 
-  int32_t page[NL];
-  auto fetch_pages = [&](int tile) {
+  // lane j of every wave looks up key j of a tile
+  auto fetch_page = [&](int tile) -> int32_t {
+    const int key = min(it.key0 + tile * kKeys + lane, it.key1 - 1);
+    return table[div_by(key, a.cache.page_size, a.cache.page_magic)];
+  };
+  u32x4 kr[S::NL], vr[S::NL];
+  uint64_t good = 0;  // keys of the issued tile in a good page
+  bool odd = false;   // met what CAREFUL = false does not handle
+  auto issue = [&](int tile, int32_t page) {
+    // beyond the range the last key is loaded again, and never seen
+    const int key = it.key0 + tile * kKeys + lane;
+    const int64_t off = key_offset(a.cache, min(key, it.key1 - 1), page);
+    if constexpr (CAREFUL) good = __ballot(off >= 0 && key < it.key1);
+    else odd |= off < 0;
+    const int64_t o = max((int64_t)0, off);
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int key = it.key0 + tile * kKeys + ROWS * i + lrow;
-      page[i] = key < it.key1 ? table[div_by(key, a.cache.page_size, a.cache.page_magic)] : -1;
+    for (int i = 0; i < S::NL; ++i) {
+      const int64_t at = __shfl(o, S::ROWS * i + lrow) + col;
+      kr[i] = gload16(k_head + at);
+      vr[i] = gload16(v_head + at);
     }
   };
-  u32x4 kr[NL], vr[NL];
-  uint32_t good = 0;  // bit i: this thread's row i is a key
-  auto issue = [&](int tile) {
-    good = 0;
-#pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const int64_t off = key_offset(a.cache, it.key0 + tile * kKeys + ROWS * i + lrow, page[i]);
-      if (off >= 0) good |= 1u << i;
-      const int64_t o = max((int64_t)0, off) + col;
-      kr[i] = gload16(k_head + o);
-      vr[i] = gload16(v_head + o);
-    }
+  auto is_masked = [&](int tile) {
+    const int k0 = it.key0 + tile * kKeys;
+    return k0 < it.full0 || k0 + kKeys > min(it.full1, it.key1);
   };
-  // Registers to LDS.  Rows that are no keys are written as zeros; in K the
-  // 8 spare elements of a row tell whether it is one.
-  auto stage = [&](int buf, bool masked) -> bool {
-    uint16_t *kl = lds + buf * BUF, *vl = kl + kKeys * LDK;
+  // Registers to LDS.  In K the 8 spare elements of a row tell whether it is a
+  // key (CAREFUL).  Returns whether V holds what a weight of zero does not hide.
+  auto stage = [&](int tile, bool masked) -> bool {
+    uint16_t *kl = lds + (tile & 1) * S::BUF, *vl = kl + kKeys * S::LDK;
     bool poison = false;
 #pragma unroll
-    for (int i = 0; i < NL; ++i) {
-      const bool ok = (good >> i) & 1;
+    for (int i = 0; i < S::NL; ++i) {
+      const int r = S::ROWS * i + lrow;
       u32x4 k = kr[i], v = vr[i];
-      if (!ok || !piece_ok) k = v = u32x4{0, 0, 0, 0};
-      const int r = ROWS * i + lrow;
-      uint16_t *kp = kl + r * LDK + piece * (FP8 ? 16 : 8), *vp = vl + r * LDV + piece * (FP8 ? 16 : 8);
+      if (!piece_ok) k = v = u32x4{0, 0, 0, 0};
+      if constexpr (CAREFUL) {
+        if (!((good >> r) & 1)) k = v = u32x4{0, 0, 0, 0};
+        if (piece == 0) kl[r * S::LDK + DP] = (good >> r) & 1;
+      } else if (masked) {
+        if (it.key0 + tile * kKeys + r >= it.key1) v = u32x4{0, 0, 0, 0};
+      }
+      uint16_t *kp = kl + r * S::LDK + piece * (FP8 ? 16 : 8), *vp = vl + r * S::LDV + piece * (FP8 ? 16 : 8);
       if constexpr (FP8) {
         const u32x4 v0 = e4m3x8_to_bf16(v[0], v[1]), v1 = e4m3x8_to_bf16(v[2], v[3]);
         if (masked) poison |= any_nonfinite(v0) || any_nonfinite(v1);
@@ -98,19 +117,24 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnA
         *reinterpret_cast<u32x4 *>(kp) = k;
         *reinterpret_cast<u32x4 *>(vp) = v;
       }
-      if (piece == 0) kl[r * LDK + DP] = ok ? 1 : 0;
     }
     return poison;
   };
-  auto is_masked = [&](int tile) {
-    const int k0 = it.key0 + tile * kKeys;
-    return k0 < it.full0 || k0 + kKeys > it.full1 || k0 + kKeys > it.key1;
+  // CAREFUL: a tile's word says that its values hold infinities or NaN.  Four
+  // words in turn: one is cleared after the barrier that ends its tile and next
+  // written two barriers later.
+  auto put = [&](int tile) {
+    if constexpr (CAREFUL) {
+      if (stage(tile, true)) atomicOr(&flag_lds[tile & 3], 1);
+    } else {
+      odd |= stage(tile, is_masked(tile));
+    }
   };
 
-  if (ntiles > 0) fetch_pages(0);
-  bf16x8 q[KS];
+  int32_t page = ntiles > 0 ? fetch_page(0) : 0;
+  bf16x8 q[S::KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) {
+  for (int s = 0; s < S::KS; ++s) {
     const int d = 16 * s + 8 * g;
     u32x4 w = {0, 0, 0, 0};
     if (row_ok && d < a.dim) w = gload16(a.q + 2 * (tok * a.ldq + (int64_t)qh * a.dim + d));
@@ -119,46 +143,36 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnA
   int lo = 0, hi = 0, pos = 0;
   if (row_ok) {
     const int4 v = reinterpret_cast<const int4 *>(a.limits)[tok];
-    lo = v.x, hi = v.y, pos = v.z;
+    lo = max(v.x, it.key0), hi = min(v.y, it.key1), pos = v.z;
   }
+  const uint32_t span = (uint32_t)max(hi - lo, 0);
   const ScoreArgs sc = score_args<GENERAL>(a, kvh, qh);
+  const float mul = GENERAL ? 1.f : sc.mul;  // st * mul: base-2 logits
 
-  float m = kNegInf, l = 0.f;
-  f32x16 o[DT];
+  float base = kNegInf, l = 0.f;
+  f32x16 o[S::DT];
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+  for (int d = 0; d < S::DT; ++d)
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.f;
 
-  // A tile's flags: 1, some row of it is no key (a bad page); 2, it holds
-  // infinities or NaN among its values.  Four words in turn: a tile's word is
-  // cleared after the barrier that ends it and next written two barriers later.
-  if (tid < 4) flag_lds[tid] = 0;
+  if (CAREFUL && tid < 4) flag_lds[tid] = 0;
   if (ntiles > 0) {
-    issue(0);
-    if (ntiles > 1) fetch_pages(1);
+    issue(0, page);
+    if (ntiles > 1) page = fetch_page(1);
   }
-  __syncthreads();
-  auto put = [&](int tile) {
-    const bool masked = is_masked(tile) || good != (1u << NL) - 1;
-    const bool poison = stage(tile & 1, masked);
-    int f = 0;
-    if (good != (1u << NL) - 1) f |= 1;
-    if (poison) f |= 2;
-    if (f) atomicOr(&flag_lds[tile & 3], f);
-  };
+  if constexpr (CAREFUL) __syncthreads();
   if (ntiles > 0) put(0);
   __syncthreads();
 
   for (int tile = 0; tile < ntiles; ++tile) {
     const int k0 = it.key0 + tile * kKeys;
     if (tile + 1 < ntiles) {
-      issue(tile + 1);
-      if (tile + 2 < ntiles) fetch_pages(tile + 2);
+      issue(tile + 1, page);
+      if (tile + 2 < ntiles) page = fetch_page(tile + 2);
     }
-    const int flags = flag_lds[tile & 3];
     if (wave_ok) {
-      const uint16_t *kl = lds + (tile & 1) * BUF, *vl = kl + kKeys * LDK;
+      const uint16_t *kl = lds + (tile & 1) * S::BUF, *vl = kl + kKeys * S::LDK;
       // ---- scores of 64 keys
       f32x16 st[2];
 #pragma unroll
@@ -166,74 +180,86 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnA
 #pragma unroll
         for (int i = 0; i < 16; ++i) st[t][i] = 0.f;
 #pragma unroll
-        for (int s = 0; s < KS; ++s) {
-          const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kl + (32 * t + c) * LDK + 16 * s + 8 * g);
+        for (int s = 0; s < S::KS; ++s) {
+          const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kl + (32 * t + c) * S::LDK + 16 * s + 8 * g);
           st[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[s], st[t], 0, 0, 0);
         }
       }
       // ---- softmax; register i of tile t is key 32 t + 8 (i / 4) + 4 g + i % 4
-      const bool masked = is_masked(tile) || (flags & 1);
+      if constexpr (GENERAL) {
+        const int away = pos - (k0 + 4 * g);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) st[t][i] = logit2<true>(sc, st[t][i], away - (32 * t + 8 * (i / 4) + i % 4));
+      }
       uint32_t see = 0xffffffffu;
-      if (masked) {
+      if constexpr (CAREFUL) {
         see = 0;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int j = 32 * t + 8 * (i / 4) + 4 * g + i % 4, key = k0 + j;
-            if (key >= lo && key < hi && kl[j * LDK + DP]) see |= 1u << (16 * t + i);
+            const int j = 32 * t + 8 * (i / 4) + 4 * g + i % 4;
+            if ((uint32_t)(k0 + j - lo) < span && kl[j * S::LDK + DP]) see |= 1u << (16 * t + i);
+            else st[t][i] = kNegInf;
           }
+      } else if (is_masked(tile)) {
+        const int from = k0 + 4 * g - lo;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if ((uint32_t)(from + 32 * t + 8 * (i / 4) + i % 4) >= span) st[t][i] = kNegInf;
       }
-      float top = m;
+      float top = kNegInf;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float x = logit2<GENERAL>(sc, st[t][i], pos - (k0 + 32 * t + 8 * (i / 4) + 4 * g + i % 4));
-          if (masked && !((see >> (16 * t + i)) & 1)) x = kNegInf;
-          st[t][i] = x;
-          top = fmaxf(top, x);
-        }
-      top = fmaxf(top, __shfl_xor(top, 32));
-      const float base = top == kNegInf ? 0.f : top;
-      const float fade = exp2_fast(m - base);
-      m = top;
-      l *= fade;
+        for (int i = 0; i < 16; i += 2) top = fmaxf(top, fmaxf(st[t][i], st[t][i + 1]));
+      top = fmaxf(top, __shfl_xor(top, 32)) * mul;
+      // (a NaN score makes its weight NaN below; it may not steer the branch)
+      if (__any(!(top <= base + kSlack) && top > kNegInf)) {
+        const float next = fmaxf(base, top);
+        const float fade = next > kNegInf ? exp2_fast(base - next) : 1.f;
+        base = next;
+        l *= fade;
+#pragma unroll
+        for (int d = 0; d < S::DT; ++d)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[d][i] *= fade;
+      }
+      const float minus = base == kNegInf ? 0.f : -base;
       u32x4 p[4];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int i = 0; i < 16; i += 2) {
-          const float p0 = exp2_fast(st[t][i] - base), p1 = exp2_fast(st[t][i + 1] - base);
+          const float p0 = exp2_fast(__builtin_fmaf(st[t][i], mul, minus));
+          const float p1 = exp2_fast(__builtin_fmaf(st[t][i + 1], mul, minus));
           l += p0;
           l += p1;
           p[2 * t + i / 8][(i % 8) / 2] = pack_bf16x2(p0, p1);
         }
-      // ---- O^T = fade O^T + V^T P^T; step s: keys 16 s + 8 (e / 4) + 4 g + e % 4
+      // ---- O^T += V^T P^T; step s: keys 16 s + 8 (e / 4) + 4 g + e % 4
       auto v_operand = [&](int d, int s) {
-        const uint16_t *b = vl + (16 * s + 4 * g + (lane % 16) / 4) * LDV + 32 * d + 16 * ((lane / 16) % 2) + 4 * (lane % 4);
-        const u32x2 v0 = lds_read_tr(b), v1 = lds_read_tr(b + 8 * LDV);
+        const uint16_t *b = vl + (16 * s + 4 * g + (lane % 16) / 4) * S::LDV + 32 * d + 16 * ((lane / 16) % 2) + 4 * (lane % 4);
+        const u32x2 v0 = lds_read_tr(b), v1 = lds_read_tr(b + 8 * S::LDV);
         return u32x4{v0.x, v0.y, v1.x, v1.y};
       };
+      const bool poison = CAREFUL && flag_lds[tile & 3];
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[d][i] *= fade;
-      if (__builtin_expect(!(flags & 2), 1)) {
+        for (int d = 0; d < S::DT; ++d) {
+          u32x4 v = v_operand(d, s);
+          if (CAREFUL && poison) v = v_part(v, kVFinite);
+          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, p[s]),
+                                                         o[d], 0, 0, 0);
+        }
+      if (CAREFUL && poison) {
 #pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v_operand(d, s)),
-                                                           __builtin_bit_cast(bf16x8, p[s]), o[d], 0, 0, 0);
-      } else {
-        // infinities or NaN among the values of a tile with hidden keys
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-#pragma unroll
-          for (int s = 0; s < 4; ++s)
-            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v_part(v_operand(d, s), kVFinite)),
-                                                           __builtin_bit_cast(bf16x8, p[s]), o[d], 0, 0, 0);
+        for (int d = 0; d < S::DT; ++d)
 #pragma unroll 1
           for (int part = kVPosInf; part <= kVNegInf; ++part) {
             f32x16 n;
@@ -254,31 +280,33 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnA
 #pragma unroll
             for (int i = 0; i < 16; ++i) o[d][i] = n[i] > 0.f ? o[d][i] + inf : o[d][i];
           }
-        }
       }
     }
     if (tile + 1 < ntiles) {
       // the other buffer was last read before the previous barrier
       put(tile + 1);
       __syncthreads();
-      if (tid == 0) flag_lds[tile & 3] = 0;
+      if (CAREFUL && tid == 0) flag_lds[tile & 3] = 0;
     }
   }
+  if constexpr (!CAREFUL) {
+    if (__syncthreads_or(odd)) return true;
+  }
 
-  if (!row_ok) return;
+  if (!row_ok) return false;
   l += __shfl_xor(l, 32);
   const float vs = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.f;
-  const float mul = it.unit >= 0 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));
+  const float f = it.unit >= 0 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));
   const int64_t pr = it.unit >= 0 ? part_row(a, it.unit + row / kUnitRows, h, row % kUnitRows) : 0;
 #pragma unroll
-  for (int d = 0; d < DT; ++d)
+  for (int d = 0; d < S::DT; ++d)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int at = 32 * d + 8 * i + 4 * g;
       if (at >= a.dim) continue;
       float x[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = mul == 0.f ? 0.f : o[d][4 * i + e] * mul;
+      for (int e = 0; e < 4; ++e) x[e] = f == 0.f ? 0.f : o[d][4 * i + e] * f;
       if (it.unit >= 0) {
         gstore16f(a.part + pr * a.dim + at, f32x4{x[0], x[1], x[2], x[3]});
       } else {
@@ -289,12 +317,25 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnA
     }
   if (g == 0) {
     if (it.unit >= 0) {
-      a.part_ml[2 * pr] = m;
+      a.part_ml[2 * pr] = base;
       a.part_ml[2 * pr + 1] = l;
     } else if (a.lse) {
-      a.lse[(int64_t)tok * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+      a.lse[(int64_t)tok * a.q_heads + qh] = l == 0.f ? kNegInf : (base + __log2f(l)) * kLn2;
     }
   }
+  return false;
+}
+
+template <int DP, bool FP8, bool GENERAL>
+__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnArgs a) {
+  __shared__ __align__(16) uint16_t lds[2 * TileShape<DP, FP8>::BUF];
+  __shared__ int flag_lds[4];
+  // the longest ranges of a causal prompt come last in the list and run first
+  const int h = blockIdx.x % a.heads, index = a.info[1] - 1 - (int)(blockIdx.x / a.heads);
+  if (index < 0) return;
+  const AttnItem it = load_item(a.items, index);
+  if (run_tile<DP, FP8, GENERAL, false>(a, it, h, lds, flag_lds))
+    run_tile<DP, FP8, GENERAL, true>(a, it, h, lds, flag_lds);
 }
 
 template <int DP, bool GENERAL>
@@ -307,7 +348,8 @@ void start_tile(const AttnArgs &a, AttnKind kind, dim3 grid, hipStream_t s) {
 
 hipError_t launch_attn_tile(const AttnArgs &a, AttnKind kind, hipStream_t s) {
   const dim3 grid((unsigned)((int64_t)a.max_items * a.heads));
-  const bool general = a.cap > 0.f || a.slopes;
+  // the plain form supposes a positive factor (hidden scores are -inf before it)
+  const bool general = a.cap > 0.f || a.slopes || !(a.scale > 0.f);
   if (a.dim <= 64) general ? start_tile<64, true>(a, kind, grid, s) : start_tile<64, false>(a, kind, grid, s);
   else if (a.dim <= 128) general ? start_tile<128, true>(a, kind, grid, s) : start_tile<128, false>(a, kind, grid, s);
   else general ? start_tile<256, true>(a, kind, grid, s) : start_tile<256, false>(a, kind, grid, s);
