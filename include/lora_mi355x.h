@@ -477,18 +477,19 @@ typedef struct lora_attn_batch {
  * pointers into the caller's workspace; shared, like a lora_meta, by every
  * layer of the step with this mask and cache geometry, and only read by them.
  *   limits        int32 [num_tokens][4]: lo, hi, p, sequence of every token
- *   info          int32 [16]: items of the few-row kernel, items of the
- *                 tile kernel, bad sequences, bad groups, tokens to join,
- *                 partial-result units, keys per item (few-row, tile), 0...
+ *   info          int32 [16]: slices of the few-row work, items of the tile
+ *                 work, bad sequences, bad groups, tokens to join,
+ *                 partial-result units, keys per slice, most keys per item of
+ *                 the tile work, pieces of the slices, then zeros
  * The other arrays are work lists whose contents are internal. */
 typedef struct lora_attn_meta {
     int64_t num_tokens, page_table_stride, max_units;
     int32_t num_seqs, num_q_heads, num_kv_heads, head_dim, page_size;
     int32_t dtype;                  /* the cache's */
     int32_t heads_per_item, head_groups;   /* query heads of one work item; items per key head */
-    int32_t max_tiles, max_few_items, max_tile_items;
+    int32_t max_tiles, max_slots, max_tile_items;
     const int32_t *page_table;
-    int32_t *limits, *info, *tiles, *few_items, *tile_items, *join, *join_tokens;
+    int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_tokens;
 } lora_attn_meta;
 
 /* Device workspace of lora_prepare_attn_meta for this batch and cache (sizes

@@ -80,8 +80,8 @@ class lora_attn_meta(C.Structure):
                 ("num_seqs", C.c_int32), ("num_q_heads", C.c_int32), ("num_kv_heads", C.c_int32),
                 ("head_dim", C.c_int32), ("page_size", C.c_int32), ("dtype", C.c_int32),
                 ("heads_per_item", C.c_int32), ("head_groups", C.c_int32), ("max_tiles", C.c_int32),
-                ("max_few_items", C.c_int32), ("max_tile_items", C.c_int32), ("page_table", C.c_void_p),
-                ("limits", C.c_void_p), ("info", C.c_void_p), ("tiles", C.c_void_p), ("few_items", C.c_void_p),
+                ("max_slots", C.c_int32), ("max_tile_items", C.c_int32), ("page_table", C.c_void_p),
+                ("limits", C.c_void_p), ("info", C.c_void_p), ("tiles", C.c_void_p), ("few_items", C.c_void_p), ("slots", C.c_void_p),
                 ("tile_items", C.c_void_p), ("join", C.c_void_p), ("join_tokens", C.c_void_p)]
 
 
@@ -162,7 +162,8 @@ def _check(fn: str, st: int) -> None:
 
 def _stream(stream) -> C.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle without building a Stream object (3 us)
+        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     return C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 

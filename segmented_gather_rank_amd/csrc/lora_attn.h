@@ -23,16 +23,24 @@ constexpr int kFewRows = 16;
 constexpr int kTileQRows = 128;
 // A partial-result unit: 16 rows of one head group.
 constexpr int kUnitRows = 16;
-// Items (of all head groups) that the key ranges of one kernel are cut into at
-// most, beyond one per tile.  Measured at the kernels.
-constexpr int kFewTarget = 2048;
-constexpr int kTileTarget = 1024;
-// Shortest key range worth an item of its own.
+// Workgroups that the chip holds of the attention kernels: 256 CUs with two each
+// (registers).  The few-row kernel's keys are laid end to end and cut into one
+// slice per workgroup; a tile's keys are cut only where the tiles alone would
+// leave workgroups without work.
+constexpr int kFewSlots = 256;
+constexpr int kTileSlots = 512;
+// Shortest slice and shortest part of a tile, in keys: one step of every wave;
+// four tiles of 64.
 constexpr int kFewMinKeys = 128;
 constexpr int kTileMinKeys = 256;
+// Workgroups that the tile items of a call are spread over at most.
+constexpr int kMaxTileBlocks = 4096;
+// Granularity of slices and parts.
+constexpr int kCutKeys = 64;
 
 constexpr int kAttnTileInts = 12;  // see AttnTile
 constexpr int kAttnItemInts = 8;   // see AttnItem
+constexpr int kAttnSlotInts = 12;  // see AttnSlot
 constexpr int kAttnInfoInts = 16;
 
 LORA_HD int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -45,42 +53,59 @@ LORA_HD int heads_per_item(int per_kv) {
   return 1;
 }
 
-// Keys per item of one kernel: the tiles' keys together cut into about
-// `target / heads` ranges, of at least `least`, in whole steps of 64.
-LORA_HD int keys_per_item(int64_t total, int heads, int target, int least) {
-  const int64_t parts = target / heads > 0 ? target / heads : 1;
-  int64_t c = ceil_div64(total, parts);
-  if (c < least) c = least;
-  c = (c + 63) & ~(int64_t)63;
+LORA_HD int round_cut(int64_t keys) {
+  const int64_t c = (keys + kCutKeys - 1) & ~(int64_t)(kCutKeys - 1);
   return c > (1 << 30) ? (1 << 30) : (int)c;
+}
+
+// Length of a slice (few-row kernel) or most keys of a part (tile kernel): an
+// equal share of all keys for each of the `slots` workgroups, heads of which
+// work on the same keys, and at least `least`.
+LORA_HD int slots_per_head(int heads, int slots) { return slots / heads > 0 ? slots / heads : 1; }
+LORA_HD int share_of(int64_t total, int heads, int slots, int least) {
+  const int64_t c = ceil_div64(total, slots_per_head(heads, slots));
+  return round_cut(c < least ? least : c);
+}
+
+// Keys that a few-row tile occupies on the line that is cut into slices.
+LORA_HD int line_keys(int keys) { return keys > 0 ? round_cut(keys) : kCutKeys; }
+
+// Parts of a tile-kernel tile: equal parts of at most `share` keys.
+LORA_HD int part_keys(int keys, int share) {
+  if (keys <= share) return keys > 0 ? keys : 1;
+  return round_cut(ceil_div64(keys, ceil_div64(keys, share)));
 }
 
 // Capacities of the work lists, from sizes the host knows.
 struct AttnCaps {
   int64_t tiles;      // tiles of both kernels, groups' included
-  int64_t few_items;  // items of the few-row kernel
+  int64_t few_items;  // pieces of few-row tiles
+  int64_t slots;      // slices of the few-row kernel
   int64_t tile_items;
   int64_t units;      // partial-result units
 };
 
 // heads: head groups (items per tile and key range); group: query heads of an
 // item; tile_rows: rows of the larger tile (16 where only the few-row kernel
-// runs).  A sequence of q tokens makes ceil(q / tokens) tiles.  Cutting ranges
-// of keys_per_item keys adds at most target / heads items, and at most that
-// many tiles are cut at all.  With groups every tile may need partial results.
+// runs).  A sequence of q tokens makes ceil(q / tokens) tiles, a single one
+// where they are few rows.  Every cut between two slices adds one piece; parts
+// of at most share_of keys number at most twice the slots in all tiles that are
+// cut.  With groups every tile may need partial results.
 LORA_HD AttnCaps attn_caps(int64_t tokens, int64_t seqs, int64_t groups, int heads, int group, int tile_rows) {
   const int64_t per = tile_rows / group;
   const int64_t own = seqs + tokens / per, shared = groups ? groups + tokens / per : 0;
-  const int64_t few = kFewTarget / heads + 1, big = kTileTarget / heads + 1;
+  const int64_t few = slots_per_head(heads, kFewSlots) + 1, big = slots_per_head(heads, kTileSlots) + 1;
+  const bool wide = tile_rows > kFewRows;
   AttnCaps c;
   c.tiles = own + shared;
-  c.few_items = c.tiles + few;
-  c.tile_items = tile_rows > kFewRows ? c.tiles + big : 0;
-  const int64_t wide = tile_rows > kFewRows ? kTileQRows / kUnitRows : 0;
+  c.slots = few;
+  c.few_items = (wide ? seqs + groups : c.tiles) + few;
+  c.tile_items = wide ? c.tiles + big : 0;
+  const int64_t ups = wide ? kTileQRows / kUnitRows : 0;
   if (groups)
-    c.units = 2 * (ceil_div64(tokens * group, kUnitRows) + c.tiles) + few + wide * big;
+    c.units = 2 * (ceil_div64(tokens * group, kUnitRows) + c.tiles) + few + ups * big;
   else
-    c.units = 2 * (few + wide * big);
+    c.units = 2 * (few + ups * big);
   return c;
 }
 
@@ -91,14 +116,22 @@ struct AttnTile {
   int32_t full0, full1;       // keys all of its tokens see (full0 >= full1: none)
   int32_t few;                // 1: few-row kernel
   int32_t shared;             // 1: a group's shared keys; 2: the own keys of a member of a group
-  int32_t splits, unit0, pad;
+  int32_t part;               // which of its sequence's (group's) tiles
+  int64_t at;                 // few: start on the line of keys, in cuts
 };
 
-// One item: a tile's rows on a part of its keys.  unit < 0: the result is final
+// One item: a tile's rows on a part of its keys (a piece of a slice, or a part of
+// a tile-kernel tile).  unit < 0: the result is final
 // and goes to the output; else to partial-result units unit, unit + 1, ...
 struct AttnItem {
   int32_t tok0, ntok, seq, key0, key1, full0, full1, unit;
 };
+// One slice of the few-row kernel: its items [first, end), and the first of them.
+struct AttnSlot {
+  int32_t first, end, pad[2];
+  AttnItem item;
+};
+static_assert(sizeof(AttnSlot) == 4 * kAttnSlotInts, "record size");
 static_assert(sizeof(AttnTile) == 4 * kAttnTileInts && sizeof(AttnItem) == 4 * kAttnItemInts, "record sizes");
 
 // x / d for 0 <= x < 2^31 and 1 <= d <= 65536.  With m = 2^32 / d rounded up,

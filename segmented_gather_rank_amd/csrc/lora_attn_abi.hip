@@ -46,7 +46,7 @@ lora_status check_cache(const lora_kv_cache *c) {
 struct AttnSizes {
   int per_kv, group, heads, tile_rows;
   AttnCaps caps;
-  size_t limits, info, tiles, few, big, join, join_tokens, seq_base, group_base, total;
+  size_t limits, info, tiles, few, slots, big, join, join_tokens, total;
 };
 
 lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSizes &s) {
@@ -64,8 +64,8 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   s.heads = b->num_q_heads / s.group;
   s.tile_rows = c->dtype == LORA_F32 ? kFewRows : kTileQRows;
   s.caps = attn_caps(b->num_tokens, b->num_seqs, b->num_groups, s.heads, s.group, s.tile_rows);
-  // the launches' grids and the lists' lengths are 32-bit
-  if (std::max(s.caps.few_items, s.caps.tile_items) * s.heads > 0x7fffffff || s.caps.units > 0x7fffffff)
+  // the lists' lengths are 32-bit
+  if (std::max(s.caps.few_items, s.caps.tile_items) > 0x7fffffff || s.caps.units > 0x7fffffff)
     return LORA_ERR_UNSUPPORTED;
   size_t at = 0;
   auto take = [&](int64_t ints) {
@@ -77,11 +77,10 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   s.limits = take(4 * b->num_tokens);
   s.tiles = take(kAttnTileInts * s.caps.tiles);
   s.few = take(kAttnItemInts * s.caps.few_items);
+  s.slots = take(kAttnSlotInts * s.caps.slots);
   s.big = take(kAttnItemInts * s.caps.tile_items);
   s.join = take(8 * b->num_tokens);
   s.join_tokens = take(b->num_tokens);
-  s.seq_base = take(b->num_seqs + 1);
-  s.group_base = take(b->num_groups + 1);
   s.total = at;
   return LORA_OK;
 }
@@ -236,8 +235,8 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.tile_items = at(s.big);
   a.join = at(s.join);
   a.join_tokens = at(s.join_tokens);
-  a.seq_base = at(s.seq_base);
-  a.group_base = at(s.group_base);
+  a.slots = at(s.slots);
+  a.max_slots = (int32_t)s.caps.slots;
 
   *out = lora_attn_meta{};
   out->num_tokens = a.tokens;
@@ -252,7 +251,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   out->heads_per_item = s.group;
   out->head_groups = s.per_kv / s.group;
   out->max_tiles = a.max_tiles;
-  out->max_few_items = a.max_few_items;
+  out->max_slots = a.max_slots;
   // sequences of at most 16 rows and no groups: nothing for the tile kernel
   out->max_tile_items = !b->num_groups && (int64_t)b->max_q_len * s.group <= kFewRows ? 0 : a.max_tile_items;
   out->page_table = b->d_page_table;
@@ -260,6 +259,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   out->info = a.info;
   out->tiles = a.tiles;
   out->few_items = a.few_items;
+  out->slots = a.slots;
   out->tile_items = a.tile_items;
   out->join = a.join;
   out->join_tokens = a.join_tokens;
@@ -286,7 +286,8 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
   if (m->num_kv_heads != cache->num_heads || m->head_dim != cache->head_dim || m->page_size != cache->page_size ||
       m->dtype != cache->dtype || m->head_groups <= 0 ||
       m->head_groups * m->heads_per_item * m->num_kv_heads != m->num_q_heads || !m->limits || !m->info ||
-      !m->few_items || !m->tile_items || !m->join || !m->join_tokens || m->max_few_items < 0 || m->max_tile_items < 0 ||
+      !m->few_items || !m->slots || !m->tile_items || !m->join || !m->join_tokens || m->max_slots < 1 || m->max_slots > 2048 ||
+      m->max_tile_items < 0 ||
       m->num_tokens < 0)
     return LORA_ERR_INVALID_ARG;
   const int64_t width = (int64_t)m->num_q_heads * m->head_dim;
@@ -334,17 +335,14 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
 
   const AttnKind kind = kind_of(cache->dtype);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t err = hipSuccess;
-  if (m->max_tile_items > 0) {
-    a.items = m->tile_items;
-    a.max_items = m->max_tile_items;
-    err = launch_attn_tile(a, kind, s);
-  }
-  if (err == hipSuccess) {
-    a.items = m->few_items;
-    a.max_items = m->max_few_items;
-    err = launch_attn_few(a, kind, s);
-  }
+  a.few_items = m->few_items;
+  a.slots = m->slots;
+  a.tile_items = m->tile_items;
+  a.few_blocks = (m->max_slots - 1) * a.heads;
+  // more tiles than this are taken in rounds (lora_attn.hip)
+  a.tile_blocks = (int32_t)std::min<int64_t>((int64_t)m->max_tile_items * a.heads, kMaxTileBlocks / a.heads * a.heads);
+  if (m->max_tile_items > 0 && a.tile_blocks == 0) a.tile_blocks = a.heads;
+  hipError_t err = launch_attn(a, kind, s);
   if (err == hipSuccess) err = launch_attn_join(a, kind, s);
   return err == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }

@@ -17,6 +17,45 @@ constexpr float kNegInf = -__builtin_inff();
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// The thread's index, opaque to the optimiser: what a work item derives from it is
+// computed per item instead of being kept in registers across items (and across
+// the variants of the item's code).
+__device__ __forceinline__ int thread_of_item() {
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  return tid;
+}
+
+// Instruction kinds of __builtin_amdgcn_sched_group_barrier.
+constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
+
+// max of three (a NaN among them is passed over), one instruction; fmaxf would
+// first quiet every operand that comes from a matrix product.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+// Maximum and sum over the lanes l and l ^ 32, and over l, l ^ 16, l ^ 32, l ^ 48:
+// swapping a register's halves (rows of 16) with a copy of itself gives one
+// register with each half's value everywhere.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_rows(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return max_halves(fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+}
+__device__ __forceinline__ float sum_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+__device__ __forceinline__ float sum_rows(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return sum_halves(__uint_as_float(r[0]) + __uint_as_float(r[1]));
+}
+
 // Four keys of one column: lane l of a 16-lane group gives the address of row
 // l / 4, columns 4 (l % 4) .. + 3, and receives column l of the group's 4 rows.
 __device__ __forceinline__ u32x2 lds_read_tr(const uint16_t *p) {
@@ -70,6 +109,12 @@ __device__ __forceinline__ float add_counted_infs(float o, float pos, float neg)
   if (neg > 0.f) o -= __builtin_inff();
   return o;
 }
+
+// The running maximum that the weights refer to is only raised when a score
+// exceeds it by more than 2^kSlack: the weights stay below 2^kSlack and their
+// sum and O are exact up to that factor, while O, half of a wave's registers, is
+// hardly ever rescaled.
+constexpr float kSlack = 8.f;
 
 // Scores to base-2 logits.  Plain: the factor alone.  General: cap * tanh(x /
 // cap) with tanh(y) = 1 - 2 / (exp(2y) + 1) (absolute error about 1e-7, so the

@@ -1,6 +1,6 @@
-// lora_attn_few.hip -- attention of up to 16 rows (query token x query head of
+// lora_attn_few.h -- attention of up to 16 rows (query token x query head of
 // one key head) over a range of cached keys: decode, short extensions, and every
-// fp32 call.  And the kernel that joins partial results.
+// fp32 call.  Device code of lora_attn.hip.
 //
 // With the rows of one key head as the columns of a matrix product, the scores
 // of 16 keys are S^T = K Q^T (16 x 16, contracted over the head dimension) and
@@ -18,6 +18,8 @@
 // wave touches (for the transposition), the next step's 16 loads of 16 bytes a
 // lane are in flight while a step is computed, and page ids are fetched two
 // steps ahead.  The waves meet once, at the end.
+#pragma once
+
 #include "lora_attn_dev.h"
 
 namespace lora {
@@ -31,7 +33,7 @@ constexpr int kStep = 32;  // keys per wave and step
 template <int DP, typename OUT>
 __device__ __forceinline__ void finish_few(const AttnArgs &a, const AttnItem &it, int h, const char *o_lds,
                                            int region, const float (*ml)[16][2]) {
-  const int row = threadIdx.x / 16, j = threadIdx.x % 16;
+  const int tid = thread_of_item(), row = tid / 16, j = tid % 16;
   if (row >= it.ntok * a.group) return;
   float m = ml[0][row][0];
 #pragma unroll
@@ -80,98 +82,106 @@ __device__ __forceinline__ void finish_few(const AttnArgs &a, const AttnItem &it
   }
 }
 
-// DP: head dimension rounded up to 64, 128 or 256 (dimensions past a.dim are
-// zeros).  FP8: e4m3 cache, widened to bf16 (exactly) on the way in.
-template <int DP, bool FP8, bool GENERAL>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_kernel(AttnArgs a) {
-  constexpr int KS = DP / 32;                   // k-steps of a score product
-  constexpr int LDV = DP + 16;                  // V row in LDS: 8 consecutive rows cover all 64 banks
-  constexpr int CPR = FP8 ? DP / 16 : DP / 8;   // 16-byte pieces of a V row
-  constexpr int VROWS = 64 / CPR;               // V rows per load of the wave
-  constexpr int NV = kStep / VROWS;
-  constexpr int KL = FP8 ? KS / 2 : KS;         // 16-byte loads of one key's share of a lane
-  constexpr int REGION = kStep * LDV * 2;
+// One item.  DP: head dimension rounded up to 64, 128 or 256 (dimensions past
+// a.dim are zeros).  FP8: e4m3 cache, widened to bf16 (exactly) on the way in.
+// CAREFUL as in run_tile.
+template <int DP, bool FP8>
+struct FewShape {
+  static constexpr int KS = DP / 32;                   // k-steps of a score product
+  static constexpr int LDV = DP + 16;                  // V row in LDS: 8 consecutive rows cover all 64 banks
+  static constexpr int CPR = FP8 ? DP / 16 : DP / 8;   // 16-byte pieces of a V row
+  static constexpr int VROWS = 64 / CPR;               // V rows per load of the wave
+  static constexpr int NV = kStep / VROWS;
+  static constexpr int KL = FP8 ? KS / 2 : KS;         // 16-byte loads of one key's share of a lane
+  static constexpr int REGION = kStep * LDV * 2;       // LDS bytes of a wave
   static_assert(REGION >= 16 * (DP + 4) * 4, "the waves' outputs reuse the V rows");
-  __shared__ __align__(16) char lds[4 * REGION];
-  __shared__ float ml_lds[4][16][2];
+};
 
-  const int h = blockIdx.x % a.heads, index = blockIdx.x / a.heads;
-  if (index >= a.info[0]) return;
-  const AttnItem it = load_item(a.items, index);
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = lane / 16, c = lane % 16;
+template <int DP, bool FP8, bool GENERAL, bool CAREFUL>
+__device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, int h, char *lds, float (*ml_lds)[16][2]) {
+  using S = FewShape<DP, FP8>;
+  const int tid = thread_of_item(), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int g = lane / 16, c = lane % 16;
   const int kvh = h / a.kv_parts;
   const bool row_ok = c < it.ntok * a.group;
   const int tok = it.tok0 + (row_ok ? c / a.group : 0), qh = h * a.group + (row_ok ? c % a.group : 0);
 
-  // page ids of a step: lane j looks up key j (both halves of the wave alike)
+  // lane j looks up key j of a step (both halves of the wave alike); beyond the
+  // range the last key again, never seen
   const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
   auto page_of = [&](int step) -> int32_t {
-    const int key = it.key0 + step * kStep + lane % kStep;
-    return key < it.key1 ? table[div_by(key, a.cache.page_size, a.cache.page_magic)] : -1;
+    const int key = min(it.key0 + step * kStep + lane % kStep, it.key1 - 1);
+    return table[div_by(key, a.cache.page_size, a.cache.page_magic)];
   };
   const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
   const int nsteps = (it.key1 - it.key0 + kStep - 1) / kStep;
 
-  int32_t page = page_of(wave);
-  int32_t page_next = page_of(wave + 4);
+  int32_t page = 0, page_next = 0;
+  if (nsteps > 0) {
+    page = page_of(wave);
+    page_next = page_of(wave + 4);
+  }
 
   // Q: this row's share of the dimensions, in the order the K loads deliver them
-  bf16x8 q[KS];
-  bool k_ok[KL];
+  bf16x8 q[S::KS];
 #pragma unroll
-  for (int s = 0; s < KS; ++s) {
+  for (int s = 0; s < S::KS; ++s) {
     const int d = FP8 ? 64 * (s / 2) + 16 * g + 8 * (s % 2) : 32 * s + 8 * g;
     u32x4 w = {0, 0, 0, 0};
     if (row_ok && d < a.dim) w = gload16(a.q + 2 * (tok * a.ldq + (int64_t)qh * a.dim + d));
     q[s] = __builtin_bit_cast(bf16x8, w);
-    if (FP8 ? s % 2 == 0 : true) k_ok[FP8 ? s / 2 : s] = d < a.dim;
   }
+  auto k_ok = [&](int s) { return (FP8 ? 64 * s + 16 * g : 32 * s + 8 * g) < a.dim; };
   int lo = 0, hi = 0, pos = 0;
   if (row_ok) {
     const int4 v = reinterpret_cast<const int4 *>(a.limits)[tok];
-    lo = v.x, hi = v.y, pos = v.z;
+    lo = max(v.x, it.key0), hi = min(v.y, it.key1), pos = v.z;
   }
+  const uint32_t span = (uint32_t)max(hi - lo, 0);
   const ScoreArgs sc = score_args<GENERAL>(a, kvh, qh);
+  const float mul = GENERAL ? 1.f : sc.mul;  // st * mul: base-2 logits
 
-  u32x4 kr[2][KL], vr[NV];
-  int64_t off = -1;  // of key (lane % 32), or -1: beyond the range or in a bad page
+  u32x4 kr[2][S::KL], vr[S::NV];
+  uint32_t good = 0;  // CAREFUL: keys of the issued step in a good page
+  bool odd = false;   // met what CAREFUL = false does not handle
   auto issue = [&](int step, int32_t pid) {
-    off = key_offset(a.cache, it.key0 + step * kStep + lane % kStep, pid);
+    const int key = it.key0 + step * kStep + lane % kStep;
+    const int64_t off = key_offset(a.cache, min(key, it.key1 - 1), pid);
+    if constexpr (CAREFUL) good = (uint32_t)__ballot(off >= 0 && key < it.key1);
+    else odd |= off < 0;
+    const int64_t at = max((int64_t)0, off);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t o = max((int64_t)0, __shfl(off, 16 * t + c));
+      const int64_t o = __shfl(at, 16 * t + c);
 #pragma unroll
-      for (int s = 0; s < KL; ++s)
-        kr[t][s] = gload16(k_head + o + (k_ok[s] ? (FP8 ? 64 * s + 16 * g : 2 * (32 * s + 8 * g)) : 0));
+      for (int s = 0; s < S::KL; ++s)
+        kr[t][s] = gload16(k_head + o + (k_ok(s) ? (FP8 ? 64 * s + 16 * g : 2 * (32 * s + 8 * g)) : 0));
     }
-    const int vc = lane % CPR;
+    const int vc = lane % S::CPR;
     const int vcol = 16 * vc < a.dim * (FP8 ? 1 : 2) ? 16 * vc : 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t o = max((int64_t)0, __shfl(off, VROWS * i + lane / CPR));
-      vr[i] = gload16(v_head + o + vcol);
-    }
+    for (int i = 0; i < S::NV; ++i) vr[i] = gload16(v_head + __shfl(at, S::VROWS * i + lane / S::CPR) + vcol);
   };
 
-  float m = kNegInf, l = 0.f;
+  float base = kNegInf, l = 0.f;
   f32x4 o[DP / 16];
 #pragma unroll
   for (int d = 0; d < DP / 16; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint16_t *vl = reinterpret_cast<uint16_t *>(lds + wave * REGION);
+  uint16_t *vl = reinterpret_cast<uint16_t *>(lds + wave * S::REGION);
 
   if (wave < nsteps) issue(wave, page);
   for (int step = wave; step < nsteps; step += 4) {
     const int k0 = it.key0 + step * kStep;
+    const bool masked = CAREFUL || k0 < it.full0 || k0 + kStep > min(it.full1, it.key1);
     // ---- scores
     f32x4 st[2];
-    const bool ragged_dim = a.dim < DP;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int s = 0; s < KL; ++s) {
+      for (int s = 0; s < S::KL; ++s) {
         u32x4 w = kr[t][s];
-        if (ragged_dim && !k_ok[s]) w = u32x4{0, 0, 0, 0};
+        if (a.dim < DP && !k_ok(s)) w = u32x4{0, 0, 0, 0};
         if constexpr (FP8) {
           st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e4m3x8_to_bf16(w[0], w[1])),
                                                           q[2 * s], st[t], 0, 0, 0);
@@ -182,16 +192,14 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_kernel(AttnAr
         }
       }
     }
-    // ---- V to LDS; rows beyond the range or in a bad page as zeros
-    const bool all_keys = __all(off >= 0);
-    const bool masked = !all_keys || k0 < it.full0 || k0 + kStep > it.full1;
+    // ---- V to LDS; rows that are no keys as zeros
     bool poison = false;
-    const int64_t off_now = off;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
+    for (int i = 0; i < S::NV; ++i) {
+      const int r = S::VROWS * i + lane / S::CPR;
       u32x4 w = vr[i];
-      if (!all_keys && __shfl(off_now, VROWS * i + lane / CPR) < 0) w = u32x4{0, 0, 0, 0};
-      uint16_t *p = vl + (VROWS * i + lane / CPR) * LDV + (lane % CPR) * (FP8 ? 16 : 8);
+      if (CAREFUL ? !((good >> r) & 1) : masked && k0 + r >= it.key1) w = u32x4{0, 0, 0, 0};
+      uint16_t *p = vl + r * S::LDV + (lane % S::CPR) * (FP8 ? 16 : 8);
       if constexpr (FP8) {
         const u32x4 w0 = e4m3x8_to_bf16(w[0], w[1]), w1 = e4m3x8_to_bf16(w[2], w[3]);
         if (masked) poison |= any_nonfinite(w0) || any_nonfinite(w1);
@@ -202,116 +210,111 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_kernel(AttnAr
         *reinterpret_cast<u32x4 *>(p) = w;
       }
     }
-    poison = __any(poison);
-    // which of this lane's keys are in a good page (bit 4 t + i)
-    uint32_t see = 0xff;
-    if (masked) {
-      see = 0;
-      const uint64_t good = __ballot(off_now >= 0);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int j = 16 * t + 4 * g + i, key = k0 + j;
-          if (key >= lo && key < hi && key < it.key1 && ((good >> j) & 1)) see |= 1u << (4 * t + i);
-        }
-    }
+    if (!CAREFUL) odd |= poison;
+    poison = CAREFUL && __any(poison);
+    const uint32_t good_now = good;
     // ---- the next step's loads
     if (step + 4 < nsteps) {
       issue(step + 4, page_next);
       page_next = page_of(step + 8);
     }
     // ---- softmax
-    float top = m;
+    if constexpr (GENERAL) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float x = logit2<GENERAL>(sc, st[t][i], pos - (k0 + 16 * t + 4 * g + i));
-        if (masked && !((see >> (4 * t + i)) & 1)) x = kNegInf;
-        st[t][i] = x;
-        top = fmaxf(top, x);
-      }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
-    const float base = top == kNegInf ? 0.f : top;
-    const float fade = exp2_fast(m - base);
-    m = top;
-    l *= fade;
+        for (int i = 0; i < 4; ++i) st[t][i] = logit2<true>(sc, st[t][i], pos - (k0 + 16 * t + 4 * g + i));
+    }
+    uint32_t see = 0xff;  // of this lane's keys (bit 4 t + i)
+    if (masked) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = 16 * t + 4 * g + i;
+          const bool hide = (uint32_t)(k0 + j - lo) >= span || (CAREFUL && !((good_now >> j) & 1));
+          if (hide) {
+            st[t][i] = kNegInf;
+            see &= ~(1u << (4 * t + i));
+          }
+        }
+    }
+    float top = max3(st[0][0], st[0][1], st[0][2]);
+    top = max3(top, st[0][3], st[1][0]);
+    top = max3(top, st[1][1], st[1][2]);
+    top = max_rows(fmaxf(top, st[1][3])) * mul;
+    if (__any(!(top <= base + kSlack) && top > kNegInf)) {
+      const float next = fmaxf(base, top);
+      const float fade = next > kNegInf ? exp2_fast(base - next) : 1.f;
+      base = next;
+      l *= fade;
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[d][i] *= fade;
+    }
+    const float minus = base == kNegInf ? 0.f : -base;
     u32x4 pw;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        st[t][i] = exp2_fast(st[t][i] - base);
+        st[t][i] = exp2_fast(__builtin_fmaf(st[t][i], mul, minus));
         l += st[t][i];
       }
       pw[2 * t] = pack_bf16x2(st[t][0], st[t][1]);
       pw[2 * t + 1] = pack_bf16x2(st[t][2], st[t][3]);
     }
     const bf16x8 p = __builtin_bit_cast(bf16x8, pw);
-    // ---- O^T = fade O^T + V^T P^T
-    auto v_operand = [&](int d) {
-      const uint16_t *b = vl + (4 * g + c / 4) * LDV + 16 * d + 4 * (c % 4);
-      const u32x2 v0 = lds_read_tr(b), v1 = lds_read_tr(b + 16 * LDV);
-      return u32x4{v0.x, v0.y, v1.x, v1.y};
-    };
+    // ---- O^T += V^T P^T
 #pragma unroll
     for (int d = 0; d < DP / 16; ++d) {
+      const uint16_t *b = vl + (4 * g + c / 4) * S::LDV + 16 * d + 4 * (c % 4);
+      const u32x2 v0 = lds_read_tr(b), v1 = lds_read_tr(b + 16 * S::LDV);
+      u32x4 v = {v0.x, v0.y, v1.x, v1.y};
+      if (CAREFUL && poison) {
+        u32x4 seen;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[d][i] *= fade;
-    }
-    if (__builtin_expect(!poison, 1)) {
-#pragma unroll
-      for (int d = 0; d < DP / 16; ++d)
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_operand(d)), p, o[d], 0, 0, 0);
-    } else {
-      u32x4 seen;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        seen[i] = ((see >> (2 * i)) & 1 ? 0x3f80u : 0u) | ((see >> (2 * i + 1)) & 1 ? 0x3f800000u : 0u);
-      const bf16x8 sb = __builtin_bit_cast(bf16x8, seen);
-#pragma unroll
-      for (int d = 0; d < DP / 16; ++d) {
-        const u32x4 v = v_operand(d);
+        for (int i = 0; i < 4; ++i)
+          seen[i] = ((see >> (2 * i)) & 1 ? 0x3f80u : 0u) | ((see >> (2 * i + 1)) & 1 ? 0x3f800000u : 0u);
+        const bf16x8 sb = __builtin_bit_cast(bf16x8, seen);
         const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_part(v, kVFinite)), p, o[d], 0, 0, 0);
         const f32x4 pi = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_part(v, kVPosInf)), sb, zero, 0, 0, 0);
         const f32x4 ni = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v_part(v, kVNegInf)), sb, zero, 0, 0, 0);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[d][i] = add_counted_infs(o[d][i], pi[i], ni[i]);
+        v = v_part(v, kVFinite);
       }
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), p, o[d], 0, 0, 0);
     }
   }
 
   // ---- the waves' results
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  if constexpr (!CAREFUL) {
+    if (__syncthreads_or(odd)) return true;
+  }
+  l = sum_rows(l);
   if (g == 0) {
-    ml_lds[wave][c][0] = m;
+    ml_lds[wave][c][0] = base;
     ml_lds[wave][c][1] = l;
   }
-  float *ol = reinterpret_cast<float *>(lds + wave * REGION);
+  float *ol = reinterpret_cast<float *>(lds + wave * S::REGION);
 #pragma unroll
   for (int d = 0; d < DP / 16; ++d) *reinterpret_cast<f32x4 *>(ol + c * (DP + 4) + 16 * d + 4 * g) = o[d];
   __syncthreads();
-  finish_few<DP, uint16_t>(a, it, h, lds, REGION, ml_lds);
+  finish_few<DP, uint16_t>(a, it, h, lds, S::REGION, ml_lds);
+  return false;
 }
 
 // fp32 queries and cache: the same products with v_mfma_f32_16x16x4_f32 (one
 // value of each operand a lane), 16 keys per wave and step.  Every call with an
 // fp32 cache comes here, in tiles of 16 rows.
 template <int DP, bool GENERAL>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(AttnArgs a) {
+__device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &it, int h, char *lds, float (*ml_lds)[16][2]) {
   constexpr int NC = DP / 16;  // 16-byte loads of one key's share of a lane
   constexpr int REGION = 16 * (DP + 4) * 4;
-  __shared__ __align__(16) char lds[4 * REGION];
-  __shared__ float ml_lds[4][16][2];
-
-  const int h = blockIdx.x % a.heads, index = blockIdx.x / a.heads;
-  if (index >= a.info[0]) return;
-  const AttnItem it = load_item(a.items, index);
-  const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, g = lane / 16, c = lane % 16;
+  const int tid = thread_of_item(), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int g = lane / 16, c = lane % 16;
   const int kvh = h / a.kv_parts;
   const bool row_ok = c < it.ntok * a.group;
   const int tok = it.tok0 + (row_ok ? c / a.group : 0), qh = h * a.group + (row_ok ? c % a.group : 0);
@@ -381,8 +384,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(At
       st[i] = see ? x : kNegInf;
       top = fmaxf(top, st[i]);
     }
-    top = fmaxf(top, __shfl_xor(top, 16));
-    top = fmaxf(top, __shfl_xor(top, 32));
+    top = max_rows(top);
     const float base = top == kNegInf ? 0.f : top;
     const float fade = exp2_fast(m - base);
     m = top;
@@ -415,8 +417,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(At
       }
     }
   }
-  l += __shfl_xor(l, 16);
-  l += __shfl_xor(l, 32);
+  l = sum_rows(l);
   if (g == 0) {
     ml_lds[wave][c][0] = m;
     ml_lds[wave][c][1] = l;
@@ -428,86 +429,6 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(At
   finish_few<DP, float>(a, it, h, lds, REGION, ml_lds);
 }
 
-// Rows whose result lies in parts: one wave per (token, query head) adds the
-// parts of its group's shared keys and of its own, weighted by their sums, in
-// the order of the keys.
-template <typename OUT>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int lane = threadIdx.x % kWave;
-  const int64_t rows = (int64_t)a.info[4] * a.q_heads;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; r < rows; r += (int64_t)gridDim.x * 4) {
-    const int t = __builtin_amdgcn_readfirstlane(a.join_tokens[r / a.q_heads]);
-    const int qh = __builtin_amdgcn_readfirstlane((int)(r % a.q_heads));
-    const int h = qh / a.group;
-    const int4 own = reinterpret_cast<const int4 *>(a.join)[2 * (int64_t)t];
-    const int4 pre = reinterpret_cast<const int4 *>(a.join)[2 * (int64_t)t + 1];
-    const int n = own.y + pre.y;
-    auto row_of = [&](int p) -> int64_t {
-      const bool shared = p < pre.y;
-      const int4 rec = shared ? pre : own;
-      const int row = rec.w * a.group + qh % a.group;
-      return part_row(a, rec.x + (int64_t)(shared ? p : p - pre.y) * rec.z + row / kUnitRows, h, row % kUnitRows);
-    };
-    // the parts' maxima, 64 at a time
-    float m = kNegInf;
-    for (int p0 = 0; p0 < n; p0 += kWave)
-      if (p0 + lane < n) m = fmaxf(m, a.part_ml[2 * row_of(p0 + lane)]);
-#pragma unroll
-    for (int x = 1; x < kWave; x *= 2) m = fmaxf(m, __shfl_xor(m, x));
-    const float base = m == kNegInf ? 0.f : m;
-    float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    const int d = 4 * lane;
-    for (int p = 0; p < n; ++p) {
-      const int64_t pr = row_of(p);
-      const float f = exp2_fast(a.part_ml[2 * pr] - base);
-      l += f * a.part_ml[2 * pr + 1];
-      if (d < a.dim) {
-        const f32x4 v = gload16f(a.part + pr * a.dim + d);
-        // a part without seen keys holds zeros
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] += f * v[i];
-      }
-    }
-    const float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = mul == 0.f ? 0.f : o[i] * mul;
-    if (d < a.dim) {
-      const int64_t at = t * a.ldo + (int64_t)qh * a.dim + d;
-      if constexpr (sizeof(OUT) == 4) {
-        gstore16f(a.out + 4 * at, f32x4{o[0], o[1], o[2], o[3]});
-      } else {
-        typedef __attribute__((address_space(1))) u32x2 g_u32x2;
-        *(g_u32x2 *)(a.out + 2 * at) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
-      }
-    }
-    if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
-  }
-}
-
-template <int DP, bool GENERAL>
-void start_few(const AttnArgs &a, AttnKind kind, dim3 grid, hipStream_t s) {
-  if (kind == kAttnF32) attn_few_f32_kernel<DP, GENERAL><<<grid, dim3(256), 0, s>>>(a);
-  else if (kind == kAttnE4m3) attn_few_kernel<DP, true, GENERAL><<<grid, dim3(256), 0, s>>>(a);
-  else attn_few_kernel<DP, false, GENERAL><<<grid, dim3(256), 0, s>>>(a);
-}
-
 }  // namespace
-
-hipError_t launch_attn_few(const AttnArgs &a, AttnKind kind, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.max_items * a.heads));
-  const bool general = a.cap > 0.f || a.slopes;
-  if (a.dim <= 64) general ? start_few<64, true>(a, kind, grid, s) : start_few<64, false>(a, kind, grid, s);
-  else if (a.dim <= 128) general ? start_few<128, true>(a, kind, grid, s) : start_few<128, false>(a, kind, grid, s);
-  else general ? start_few<256, true>(a, kind, grid, s) : start_few<256, false>(a, kind, grid, s);
-  return hipGetLastError();
-}
-
-hipError_t launch_attn_join(const AttnArgs &a, AttnKind kind, hipStream_t s) {
-  const int64_t blocks = (a.tokens * a.q_heads + 3) / 4;
-  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048));
-  if (kind == kAttnF32) attn_join_kernel<float><<<grid, dim3(256), 0, s>>>(a);
-  else attn_join_kernel<uint16_t><<<grid, dim3(256), 0, s>>>(a);
-  return hipGetLastError();
-}
 
 }  // namespace lora

@@ -13,8 +13,8 @@ struct AttnPlanArgs {
   int64_t tokens, table_stride;
   int32_t seqs, groups, max_q_len, page_size, causal, window;
   int32_t heads, group, tile_rows;
-  int32_t max_tiles, max_few_items, max_tile_items, max_units;
-  int32_t *limits, *info, *tiles, *few_items, *tile_items, *join, *join_tokens, *seq_base, *group_base;
+  int32_t max_tiles, max_few_items, max_tile_items, max_units, max_slots;
+  int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_tokens, *seq_base, *group_base;
 };
 hipError_t launch_attn_plan(const AttnPlanArgs &a, hipStream_t s);
 
@@ -24,20 +24,19 @@ struct AttnArgs {
   char *out;
   float *lse;                // [T][q_heads] or NULL
   const float *slopes;       // [q_heads] or NULL
-  const int32_t *limits, *info, *items, *join, *join_tokens;
+  const int32_t *limits, *info, *few_items, *slots, *tile_items, *join, *join_tokens;
   int64_t ldq, ldo, tokens;  // elements
   float *part;               // partial results: see part_row
   float *part_ml;
   float scale, cap;
   int32_t heads, group, q_heads, kv_parts, dim;  // kv_parts: head groups per key head
-  int32_t max_items;
+  int32_t few_blocks, tile_blocks;  // workgroups of the two kinds; tile_blocks = 0: few rows only
 };
 
 // Kind of the cache's elements (and with it of q and out).
 enum AttnKind { kAttnBf16 = 0, kAttnE4m3 = 1, kAttnF32 = 2 };
 
-hipError_t launch_attn_few(const AttnArgs &a, AttnKind kind, hipStream_t s);
-hipError_t launch_attn_tile(const AttnArgs &a, AttnKind kind, hipStream_t s);
+hipError_t launch_attn(const AttnArgs &a, AttnKind kind, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs &a, AttnKind kind, hipStream_t s);
 
 struct AppendArgs {

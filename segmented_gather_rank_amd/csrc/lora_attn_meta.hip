@@ -7,10 +7,11 @@
 //                       document bounds all come down to this one interval, so
 //                       the attention kernels know no mask but it.
 //   attn_plan_kernel    one workgroup: cuts the sequences (and the groups) into
-//                       tiles, sums up their keys, cuts every tile's keys into
-//                       ranges of one common length so that the items are alike
-//                       whatever the lengths, and writes the items and, for
-//                       tokens whose result comes in parts, where the parts lie.
+//                       tiles, lays the keys of the few-row tiles end to end and
+//                       cuts that line into equal slices, cuts the other tiles
+//                       where they are too few to fill the chip, and writes the
+//                       items and, for tokens whose result comes in parts, where
+//                       the parts lie.
 //
 // Both are latency-bound (a few microseconds) and shared by the layers of a step.
 #include "lora_attn.h"
@@ -102,160 +103,184 @@ __device__ int block_scan(int v, int *lds, int &total) {
   return base + inc - v;
 }
 
-// Last entry of base[0 .. n] (non-decreasing) that is <= i, for base[0] <= i.
-__device__ __forceinline__ int last_at_or_before(const int32_t *base, int n, int i) {
-  int lo = 0, hi = n + 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (base[mid] <= i) lo = mid + 1;
-    else hi = mid;
-  }
-  return lo - 1;
-}
-
 __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a) {
   __shared__ int scan_lds[kPlanThreads / kWave];
-  __shared__ unsigned long long sum_lds[2];
+  __shared__ unsigned long long sum_lds;
   __shared__ int bad_lds[2];
   const int tid = threadIdx.x;
-  if (tid < 2) sum_lds[tid] = 0, bad_lds[tid] = 0;
+  if (tid == 0) sum_lds = 0;
+  if (tid < 2) bad_lds[tid] = 0;
   __syncthreads();
 
-  // ---- tiles per sequence, then per group
+  // ---- tiles per sequence, then per group: which one, and which of its tiles
   const int few_tokens = kFewRows / a.group, tile_tokens = a.tile_rows / a.group;
-  int own = 0;
-  for (int n0 = 0; n0 < a.seqs; n0 += kPlanThreads) {
-    const int n = n0 + tid;
-    int count = 0;
-    if (n < a.seqs) {
-      int64_t q0, q1;
-      seq_tokens(a, n, q0, q1);
-      const int len = (int)(q1 - q0);
-      count = len <= few_tokens ? (len > 0) : (len + tile_tokens - 1) / tile_tokens;
-      if (!seq_ok(a, n)) atomicAdd(&bad_lds[0], 1);
-    }
-    int total;
-    const int before = block_scan(count, scan_lds, total);
-    if (n < a.seqs) a.seq_base[n] = min(own + before, a.max_tiles);
-    own = min(own + total, a.max_tiles);
-  }
-  int tiles = own;
-  for (int g0 = 0; g0 < a.groups; g0 += kPlanThreads) {
-    const int g = g0 + tid;
-    int count = 0;
-    if (g < a.groups) {
-      if (!group_ok(a, g)) {
-        atomicAdd(&bad_lds[1], 1);
-      } else if (a.group_len[g] > 0 && a.group_start[g] < a.group_start[g + 1]) {
-        const int64_t q0 = a.q_start[a.group_start[g]], q1 = a.q_start[a.group_start[g + 1]];
-        const int len = q0 >= 0 && q1 >= q0 && q1 <= a.tokens ? (int)(q1 - q0) : 0;
+  AttnTile *tile_list = reinterpret_cast<AttnTile *>(a.tiles);
+  int own = 0, tiles = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    const int count_all = pass ? a.groups : a.seqs;
+    for (int n0 = 0; n0 < count_all; n0 += kPlanThreads) {
+      const int n = n0 + tid;
+      int count = 0;
+      if (n < count_all) {
+        int64_t q0 = 0, q1 = 0;
+        if (pass == 0) {
+          seq_tokens(a, n, q0, q1);
+          if (!seq_ok(a, n)) atomicAdd(&bad_lds[0], 1);
+        } else if (!group_ok(a, n)) {
+          atomicAdd(&bad_lds[1], 1);
+        } else if (a.group_len[n] > 0 && a.group_start[n] < a.group_start[n + 1]) {
+          q0 = a.q_start[a.group_start[n]];
+          q1 = a.q_start[a.group_start[n + 1]];
+          if (q0 < 0 || q1 < q0 || q1 > a.tokens) q0 = q1 = 0;
+        }
+        const int len = (int)(q1 - q0);
         count = len <= few_tokens ? (len > 0) : (len + tile_tokens - 1) / tile_tokens;
       }
-    }
-    int total;
-    const int before = block_scan(count, scan_lds, total);
-    if (g < a.groups) a.group_base[g] = min(tiles + before, a.max_tiles);
-    tiles = min(tiles + total, a.max_tiles);
-  }
-  __syncthreads();  // the bases are written (one workgroup: its own stores)
-  __threadfence_block();
-
-  // ---- the tiles' tokens and keys
-  unsigned long long keys[2] = {0, 0};
-  for (int i = tid; i < tiles; i += kPlanThreads) {
-    AttnTile r;
-    int64_t q0, q1;
-    int first = 0, shared_len = 0;
-    r.shared = 0;
-    if (i < own) {
-      const int n = last_at_or_before(a.seq_base, a.seqs - 1, i);
-      seq_tokens(a, n, q0, q1);
-      first = a.seq_base[n];
-      r.seq = n;
-      const int g = a.groups ? group_of(a, n) : -1;
-      if (g >= 0) {
-        r.shared = 2;
-        shared_len = a.group_len[g];
+      int total;
+      const int before = tiles + block_scan(count, scan_lds, total);
+      for (int i = 0; i < count && before + i < a.max_tiles; ++i) {
+        tile_list[before + i].seq = n;
+        tile_list[before + i].part = i;
       }
-    } else {
-      const int g = last_at_or_before(a.group_base, a.groups - 1, i);
-      first = a.group_base[g];
-      r.seq = a.group_start[g];
-      q0 = a.q_start[r.seq];
-      q1 = a.q_start[a.group_start[g + 1]];
-      r.shared = 1;
-      shared_len = a.group_len[g];
+      tiles = min(tiles + total, a.max_tiles);
     }
-    const int len = (int)(q1 - q0), part = i - first;
-    r.few = len <= few_tokens || a.tile_rows == kFewRows;
-    const int per = r.few ? few_tokens : tile_tokens;
-    r.tok0 = (int)q0 + part * per;
-    r.ntok = max(0, min(per, len - part * per));
-    int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, hi_max = 0;
-    for (int t = 0; t < r.ntok; ++t) {
-      const int4 v = reinterpret_cast<const int4 *>(a.limits)[r.tok0 + t];
-      if (v.y > v.x) {
-        lo_min = min(lo_min, v.x);
-        hi_max = max(hi_max, v.y);
-      }
-      lo_max = max(lo_max, v.x);
-      hi_min = min(hi_min, v.y);
-    }
-    r.key0 = r.shared == 2 ? max(lo_min, shared_len) : lo_min;
-    r.key1 = r.shared == 1 ? min(hi_max, shared_len) : hi_max;
-    if (r.key1 <= r.key0) r.key0 = r.key1 = 0;
-    r.full0 = lo_max;
-    r.full1 = hi_min;
-    r.splits = r.unit0 = r.pad = 0;
-    reinterpret_cast<AttnTile *>(a.tiles)[i] = r;
-    keys[r.few ? 0 : 1] += (unsigned long long)(r.key1 - r.key0);
+    if (pass == 0) own = tiles;
   }
-  for (int c = 0; c < 2; ++c)
-    if (keys[c]) atomicAdd(&sum_lds[c], keys[c]);
-  __threadfence_block();
-  __syncthreads();
-  const int few_keys = keys_per_item((int64_t)sum_lds[0], a.heads, kFewTarget, kFewMinKeys);
-  const int tile_keys = keys_per_item((int64_t)sum_lds[1], a.heads, kTileTarget, kTileMinKeys);
+  __syncthreads();  // the list is written and read by this workgroup alone
 
-  // ---- items, partial-result units, tokens to join
-  int few_items = 0, tile_items = 0, units = 0, joins = 0;
+  // ---- the tiles' tokens and keys; few-row tiles take their place on the line
+  long long line = 0;
+  unsigned long long keys = 0;
   for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
     const int i = i0 + tid;
     AttnTile r;
-    int splits = 0, per = 1, ups = 0;
-    bool parts = false;
+    r.few = 0;
+    int width = 0;
     if (i < tiles) {
-      r = reinterpret_cast<const AttnTile *>(a.tiles)[i];
-      per = r.few ? few_keys : tile_keys;
-      splits = max(1, (r.key1 - r.key0 + per - 1) / per);
-      parts = splits > 1 || r.shared;
+      const int n = tile_list[i].seq, part = tile_list[i].part;
+      int64_t q0, q1;
+      int shared_len = 0;
+      r.shared = 0;
+      r.seq = n;
+      if (i < own) {
+        seq_tokens(a, n, q0, q1);
+        const int g = a.groups ? group_of(a, n) : -1;
+        if (g >= 0) {
+          r.shared = 2;
+          shared_len = a.group_len[g];
+        }
+      } else {
+        r.seq = a.group_start[n];
+        q0 = a.q_start[r.seq];
+        q1 = a.q_start[a.group_start[n + 1]];
+        r.shared = 1;
+        shared_len = a.group_len[n];
+      }
+      const int len = (int)(q1 - q0);
+      r.few = len <= few_tokens || a.tile_rows == kFewRows;
+      const int per = r.few ? few_tokens : tile_tokens;
+      r.tok0 = (int)q0 + part * per;
+      r.ntok = max(0, min(per, len - part * per));
+      int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, hi_max = 0;
+      const int4 *lim = reinterpret_cast<const int4 *>(a.limits) + r.tok0;
+      for (int t0 = 0; t0 < r.ntok; t0 += 8) {
+        int4 v[8];  // past the end the last token again
+#pragma unroll
+        for (int t = 0; t < 8; ++t) v[t] = lim[min(t0 + t, r.ntok - 1)];
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+          if (v[t].y > v[t].x) {
+            lo_min = min(lo_min, v[t].x);
+            hi_max = max(hi_max, v[t].y);
+          }
+          lo_max = max(lo_max, v[t].x);
+          hi_min = min(hi_min, v[t].y);
+        }
+      }
+      r.key0 = r.shared == 2 ? max(lo_min, shared_len) : lo_min;
+      r.key1 = r.shared == 1 ? min(hi_max, shared_len) : hi_max;
+      if (r.key1 <= r.key0) r.key0 = r.key1 = 0;
+      r.full0 = lo_max;
+      r.full1 = hi_min;
+      r.part = part;
+      if (r.few) width = line_keys(r.key1 - r.key0) / kCutKeys;
+      else keys += (unsigned long long)(r.key1 - r.key0);
+    }
+    int total;
+    const int before = block_scan(width, scan_lds, total);
+    if (i < tiles) {
+      r.at = line + before;
+      tile_list[i] = r;
+    }
+    line += total;
+  }
+  if (keys) atomicAdd(&sum_lds, keys);
+  __syncthreads();
+  const int slice = share_of(line * kCutKeys, a.heads, kFewSlots, kFewMinKeys);
+  const int share = share_of((int64_t)sum_lds, a.heads, kTileSlots, kTileMinKeys);
+  const int cuts = slice / kCutKeys;  // of a slice
+  const int slots = (int)min((line + cuts - 1) / cuts, (long long)a.max_slots - 1);
+
+  // ---- items, slices, partial-result units, tokens to join
+  int few_items = 0, tile_items = 0, units = 0, joins = 0;
+  AttnSlot *slot_list = reinterpret_cast<AttnSlot *>(a.slots);
+  for (int i0 = 0; i0 < tiles; i0 += kPlanThreads) {
+    const int i = i0 + tid;
+    AttnTile r;
+    int parts = 0, per = 1, ups = 0;
+    bool join = false;
+    if (i < tiles) {
+      r = tile_list[i];
+      const int n = r.key1 - r.key0;
+      if (r.few) {
+        const int64_t last = r.at + line_keys(n) / kCutKeys - 1;
+        parts = (int)(last / cuts - r.at / cuts) + 1;
+      } else {
+        per = part_keys(n, share);
+        parts = max(1, (n + per - 1) / per);
+      }
+      join = parts > 1 || r.shared;
       ups = (r.ntok * a.group + kUnitRows - 1) / kUnitRows;
     }
     const bool few = i < tiles && r.few;
     int nf, nt, nu, nj;
-    int at_few = few_items + block_scan(few ? splits : 0, scan_lds, nf);
-    int at_tile = tile_items + block_scan(few ? 0 : splits, scan_lds, nt);
-    int unit = units + block_scan(parts ? splits * ups : 0, scan_lds, nu);
-    int join = joins + block_scan(parts && r.shared != 1 ? r.ntok : 0, scan_lds, nj);
+    const int at_few = few_items + block_scan(few ? parts : 0, scan_lds, nf);
+    const int at_tile = tile_items + block_scan(few ? 0 : parts, scan_lds, nt);
+    const int unit = units + block_scan(join ? parts * ups : 0, scan_lds, nu);
+    const int at_join = joins + block_scan(join && r.shared != 1 ? r.ntok : 0, scan_lds, nj);
     if (i < tiles) {
-      // never true for the sizes the capacities are derived from; with a
-      // q_start that is out of order the surplus is dropped
-      const bool fits = (few ? at_few + splits <= a.max_few_items : at_tile + splits <= a.max_tile_items) &&
-                        unit + splits * ups <= a.max_units;
-      AttnItem *items = reinterpret_cast<AttnItem *>(few ? a.few_items : a.tile_items);
-      int at = few ? at_few : at_tile;
-      const int cap = few ? a.max_few_items : a.max_tile_items;
-      for (int s = 0; s < splits && at < cap; ++s, ++at) {
-        const int k0 = r.key0 + s * per;
-        items[at] = AttnItem{r.tok0, fits ? r.ntok : 0, r.seq, k0, min(r.key1, k0 + per), r.full0, r.full1,
-                             parts ? unit + s * ups : -1};
+      // true for every batch in order, by the capacities' derivation; with a
+      // q_start out of order the surplus is dropped
+      const bool fits = (few ? at_few + parts <= a.max_few_items : at_tile + parts <= a.max_tile_items) &&
+                        unit + parts * ups <= a.max_units;
+      AttnItem item{r.tok0, fits ? r.ntok : 0, r.seq, r.key0, r.key1, r.full0, r.full1, -1};
+      for (int s = 0; s < parts; ++s) {
+        const int at = (few ? at_few : at_tile) + s;
+        if (at >= (few ? a.max_few_items : a.max_tile_items)) break;
+        if (join) item.unit = unit + s * ups;
+        if (few) {
+          // the piece of the tile on slice k: the line from `from` on
+          const int64_t k = r.at / cuts + s, from = max(r.at, k * cuts);
+          item.key0 = r.key0 + (int)(from - r.at) * kCutKeys;
+          item.key1 = (int)min((int64_t)r.key1, r.key0 + ((k + 1) * cuts - r.at) * kCutKeys);
+          reinterpret_cast<AttnItem *>(a.few_items)[at] = item;
+          if (from == k * cuts && k < a.max_slots) {
+            slot_list[k].first = at;
+            slot_list[k].item = item;
+            if (k > 0) slot_list[k - 1].end = at;
+          }
+        } else {
+          item.key0 = r.key0 + s * per;
+          item.key1 = min(r.key1, item.key0 + per);
+          reinterpret_cast<AttnItem *>(a.tile_items)[at] = item;
+        }
       }
-      if (parts) {
+      if (join) {
         for (int t = 0; t < r.ntok; ++t) {
           int4 *rec = reinterpret_cast<int4 *>(a.join) + 2 * (int64_t)(r.tok0 + t);
-          rec[r.shared == 1] = int4{unit, fits ? splits : 0, ups, t};
+          rec[r.shared == 1] = int4{unit, fits ? parts : 0, ups, t};
           if (r.shared == 0) rec[1] = int4{0, 0, 0, 0};
-          if (r.shared != 1 && join + t < a.tokens) a.join_tokens[join + t] = r.tok0 + t;
+          if (r.shared != 1 && at_join + t < a.tokens) a.join_tokens[at_join + t] = r.tok0 + t;
         }
       }
     }
@@ -264,17 +289,22 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a)
     units += nu;
     joins += nj;
   }
+  few_items = min(few_items, a.max_few_items);
   if (tid == 0) {
-    a.info[0] = min(few_items, a.max_few_items);
+    if (slots > 0) slot_list[slots - 1].end = few_items;
+    a.info[0] = slots;
     a.info[1] = min(tile_items, a.max_tile_items);
     a.info[2] = bad_lds[0];
     a.info[3] = bad_lds[1];
     a.info[4] = (int)min((int64_t)joins, a.tokens);
     a.info[5] = min(units, a.max_units);
-    a.info[6] = few_keys;
-    a.info[7] = tile_keys;
-    for (int k = 8; k < kAttnInfoInts; ++k) a.info[k] = 0;
+    a.info[6] = slice;
+    a.info[7] = share;
+    a.info[8] = few_items;
+    for (int k = 9; k < kAttnInfoInts; ++k) a.info[k] = 0;
   }
+  // slices without work
+  for (int k = slots + tid; k < a.max_slots; k += kPlanThreads) slot_list[k].first = slot_list[k].end = 0;
 }
 
 }  // namespace

@@ -1,4 +1,4 @@
-// lora_attn_tile.hip -- attention of up to 128 rows (query token x query head of
+// lora_attn_tile.h -- attention of up to 128 rows (query token x query head of
 // one key head) over a range of cached keys: prompts, and the shared keys of a
 // group of sequences.
 //
@@ -16,6 +16,8 @@
 // rows.  Workgroups of one key head follow each other at the distance of the
 // number of head groups, with the usual 8 key heads on one XCD, whose L2 then
 // holds that head's keys.
+#pragma once
+
 #include "lora_attn_dev.h"
 
 namespace lora {
@@ -23,12 +25,6 @@ namespace lora {
 namespace {
 
 constexpr int kKeys = 64;  // keys per tile
-// The running maximum that the weights refer to is only raised when a score
-// exceeds it by more than 2^kSlack: the weights stay below 2^kSlack and their
-// sum and O are exact up to that factor, while O, half of a wave's registers, is
-// hardly ever rescaled.
-constexpr float kSlack = 8.f;
-
 template <int DP, bool FP8>
 struct TileShape {
   static constexpr int KS = DP / 16;                  // k-steps of a score product
@@ -48,7 +44,8 @@ struct TileShape {
 template <int DP, bool FP8, bool GENERAL, bool CAREFUL>
 __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, int h, uint16_t *lds, int *flag_lds) {
   using S = TileShape<DP, FP8>;
-  const int tid = threadIdx.x, lane = tid % kWave, wave = tid / kWave, g = lane / 32, c = lane % 32;
+  const int tid = thread_of_item(), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int g = lane / 32, c = lane % 32;
   const int kvh = h / a.kv_parts;
   const int row = 32 * wave + c, rows = it.ntok * a.group;
   const bool row_ok = row < rows;
@@ -56,11 +53,10 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   const bool wave_ok = 32 * wave < rows;
 
   const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
-  const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
   const int ntiles = (it.key1 - it.key0 + kKeys - 1) / kKeys;
   const int piece = tid % S::CPR, lrow = tid / S::CPR;
   const bool piece_ok = piece * (FP8 ? 16 : 8) < a.dim;
-  const int col = piece_ok ? 16 * piece : 0;
+  const char *k_piece = a.cache.k + kvh * a.cache.head_bytes + (piece_ok ? 16 * piece : 0);
 
   // lane j of every wave looks up key j of a tile
   auto fetch_page = [&](int tile) -> int32_t {
@@ -70,18 +66,25 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   u32x4 kr[S::NL], vr[S::NL];
   uint64_t good = 0;  // keys of the issued tile in a good page
   bool odd = false;   // met what CAREFUL = false does not handle
-  auto issue = [&](int tile, int32_t page) {
+  const char *at[S::NL];   // this thread's pieces of K of the next tile to issue
+  const int64_t k_to_v = a.cache.v - a.cache.k;
+  uint64_t good_next = 0;  // and which of its keys lie in a good page
+  auto locate = [&](int tile, int32_t page) {
     // beyond the range the last key is loaded again, and never seen
     const int key = it.key0 + tile * kKeys + lane;
     const int64_t off = key_offset(a.cache, min(key, it.key1 - 1), page);
-    if constexpr (CAREFUL) good = __ballot(off >= 0 && key < it.key1);
+    if constexpr (CAREFUL) good_next = __ballot(off >= 0 && key < it.key1);
     else odd |= off < 0;
     const int64_t o = max((int64_t)0, off);
 #pragma unroll
+    for (int i = 0; i < S::NL; ++i) at[i] = k_piece + __shfl(o, S::ROWS * i + lrow);
+  };
+  auto issue = [&]() {
+    good = good_next;
+#pragma unroll
     for (int i = 0; i < S::NL; ++i) {
-      const int64_t at = __shfl(o, S::ROWS * i + lrow) + col;
-      kr[i] = gload16(k_head + at);
-      vr[i] = gload16(v_head + at);
+      kr[i] = gload16(at[i]);
+      vr[i] = gload16(at[i] + k_to_v);
     }
   };
   auto is_masked = [&](int tile) {
@@ -90,30 +93,33 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   };
   // Registers to LDS.  In K the 8 spare elements of a row tell whether it is a
   // key (CAREFUL).  Returns whether V holds what a weight of zero does not hide.
-  auto stage = [&](int tile, bool masked) -> bool {
+  auto stage_as = [&](int tile, auto plain_tag) -> bool {
+    constexpr bool PLAIN = decltype(plain_tag)::value;  // all keys seen, all pieces
     uint16_t *kl = lds + (tile & 1) * S::BUF, *vl = kl + kKeys * S::LDK;
     bool poison = false;
 #pragma unroll
     for (int i = 0; i < S::NL; ++i) {
       const int r = S::ROWS * i + lrow;
       u32x4 k = kr[i], v = vr[i];
-      if (!piece_ok) k = v = u32x4{0, 0, 0, 0};
-      if constexpr (CAREFUL) {
-        if (!((good >> r) & 1)) k = v = u32x4{0, 0, 0, 0};
-        if (piece == 0) kl[r * S::LDK + DP] = (good >> r) & 1;
-      } else if (masked) {
-        if (it.key0 + tile * kKeys + r >= it.key1) v = u32x4{0, 0, 0, 0};
+      if constexpr (!PLAIN) {
+        if (!piece_ok) k = v = u32x4{0, 0, 0, 0};
+        if constexpr (CAREFUL) {
+          if (!((good >> r) & 1)) k = v = u32x4{0, 0, 0, 0};
+          if (piece == 0) kl[r * S::LDK + DP] = (good >> r) & 1;
+        } else {
+          if (it.key0 + tile * kKeys + r >= it.key1) v = u32x4{0, 0, 0, 0};
+        }
       }
       uint16_t *kp = kl + r * S::LDK + piece * (FP8 ? 16 : 8), *vp = vl + r * S::LDV + piece * (FP8 ? 16 : 8);
       if constexpr (FP8) {
         const u32x4 v0 = e4m3x8_to_bf16(v[0], v[1]), v1 = e4m3x8_to_bf16(v[2], v[3]);
-        if (masked) poison |= any_nonfinite(v0) || any_nonfinite(v1);
+        if (!PLAIN) poison |= any_nonfinite(v0) || any_nonfinite(v1);
         *reinterpret_cast<u32x4 *>(kp) = e4m3x8_to_bf16(k[0], k[1]);
         *reinterpret_cast<u32x4 *>(kp + 8) = e4m3x8_to_bf16(k[2], k[3]);
         *reinterpret_cast<u32x4 *>(vp) = v0;
         *reinterpret_cast<u32x4 *>(vp + 8) = v1;
       } else {
-        if (masked) poison |= any_nonfinite(v);
+        if (!PLAIN) poison |= any_nonfinite(v);
         *reinterpret_cast<u32x4 *>(kp) = k;
         *reinterpret_cast<u32x4 *>(vp) = v;
       }
@@ -125,9 +131,15 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   // written two barriers later.
   auto put = [&](int tile) {
     if constexpr (CAREFUL) {
-      if (stage(tile, true)) atomicOr(&flag_lds[tile & 3], 1);
+      if (stage_as(tile, std::false_type{})) atomicOr(&flag_lds[tile & 3], 1);
+    } else if (a.dim < DP) {
+      // the spare dimensions are zeros in every tile
+      const bool poison = stage_as(tile, std::false_type{});
+      odd |= poison && is_masked(tile);
+    } else if (is_masked(tile)) {
+      odd |= stage_as(tile, std::false_type{});
     } else {
-      odd |= stage(tile, is_masked(tile));
+      stage_as(tile, std::true_type{});
     }
   };
 
@@ -158,8 +170,12 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
 
   if (CAREFUL && tid < 4) flag_lds[tid] = 0;
   if (ntiles > 0) {
-    issue(0, page);
-    if (ntiles > 1) page = fetch_page(1);
+    locate(0, page);
+    issue();
+    if (ntiles > 1) {
+      locate(1, fetch_page(1));
+      if (ntiles > 2) page = fetch_page(2);
+    }
   }
   if constexpr (CAREFUL) __syncthreads();
   if (ntiles > 0) put(0);
@@ -167,23 +183,36 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
 
   for (int tile = 0; tile < ntiles; ++tile) {
     const int k0 = it.key0 + tile * kKeys;
-    if (tile + 1 < ntiles) {
-      issue(tile + 1, page);
-      if (tile + 2 < ntiles) page = fetch_page(tile + 2);
-    }
+    if (tile + 1 < ntiles) issue();
     if (wave_ok) {
       const uint16_t *kl = lds + (tile & 1) * S::BUF, *vl = kl + kKeys * S::LDK;
       // ---- scores of 64 keys
       f32x16 st[2];
+      {
+        bf16x8 k[2 * S::KS];
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+        for (int s = 0; s < S::KS; ++s)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) st[t][i] = 0.f;
+          for (int t = 0; t < 2; ++t)
+            k[2 * s + t] = *reinterpret_cast<const bf16x8 *>(kl + (32 * t + c) * S::LDK + 16 * s + 8 * g);
 #pragma unroll
-        for (int s = 0; s < S::KS; ++s) {
-          const bf16x8 k = *reinterpret_cast<const bf16x8 *>(kl + (32 * t + c) * S::LDK + 16 * s + 8 * g);
-          st[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k, q[s], st[t], 0, 0, 0);
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) st[t][i] = 0.f;
+#pragma unroll
+        for (int s = 0; s < S::KS; ++s)
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            st[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[2 * s + t], q[s], st[t], 0, 0, 0);
+        // kAhead reads in flight before the first product and between the others
+        constexpr int kAhead = 6;
+        __builtin_amdgcn_sched_group_barrier(kSchedDsRead, kAhead, 0);
+#pragma unroll
+        for (int s = 0; s < 2 * S::KS - kAhead; ++s) {
+          __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+          __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
         }
+        __builtin_amdgcn_sched_group_barrier(kSchedMfma, kAhead, 0);
       }
       // ---- softmax; register i of tile t is key 32 t + 8 (i / 4) + 4 g + i % 4
       if constexpr (GENERAL) {
@@ -212,12 +241,13 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
           for (int i = 0; i < 16; ++i)
             if ((uint32_t)(from + 32 * t + 8 * (i / 4) + i % 4) >= span) st[t][i] = kNegInf;
       }
-      float top = kNegInf;
+      float top0 = kNegInf, top1 = kNegInf;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) top = fmaxf(top, fmaxf(st[t][i], st[t][i + 1]));
-      top = fmaxf(top, __shfl_xor(top, 32)) * mul;
+      for (int i = 0; i < 16; i += 2) {
+        top0 = max3(top0, st[0][i], st[0][i + 1]);
+        top1 = max3(top1, st[1][i], st[1][i + 1]);
+      }
+      const float top = max_halves(fmaxf(top0, top1)) * mul;
       // (a NaN score makes its weight NaN below; it may not steer the branch)
       if (__any(!(top <= base + kSlack) && top > kNegInf)) {
         const float next = fmaxf(base, top);
@@ -230,33 +260,57 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
           for (int i = 0; i < 16; ++i) o[d][i] *= fade;
       }
       const float minus = base == kNegInf ? 0.f : -base;
+      // ---- weights, and O^T += V^T P^T; step s: keys 16 s + 8 (e / 4) + 4 g + e % 4
       u32x4 p[4];
+      float even;  // the first of a pair
+      auto weights = [&](int s, int e0, int e1) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float p0 = exp2_fast(__builtin_fmaf(st[t][i], mul, minus));
-          const float p1 = exp2_fast(__builtin_fmaf(st[t][i + 1], mul, minus));
-          l += p0;
-          l += p1;
-          p[2 * t + i / 8][(i % 8) / 2] = pack_bf16x2(p0, p1);
+        for (int e = e0; e < e1; ++e) {
+          const float x = exp2_fast(__builtin_fmaf(st[s / 2][8 * (s % 2) + e], mul, minus));
+          l += x;
+          if (e % 2 == 0) even = x;
+          else p[s][e / 2] = pack_bf16x2(even, x);
         }
-      // ---- O^T += V^T P^T; step s: keys 16 s + 8 (e / 4) + 4 g + e % 4
+      };
       auto v_operand = [&](int d, int s) {
         const uint16_t *b = vl + (16 * s + 4 * g + (lane % 16) / 4) * S::LDV + 32 * d + 16 * ((lane / 16) % 2) + 4 * (lane % 4);
         const u32x2 v0 = lds_read_tr(b), v1 = lds_read_tr(b + 8 * S::LDV);
         return u32x4{v0.x, v0.y, v1.x, v1.y};
       };
       const bool poison = CAREFUL && flag_lds[tile & 3];
+      if constexpr (CAREFUL) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+        for (int s = 0; s < 4; ++s) {
+          weights(s, 0, 8);
 #pragma unroll
-        for (int d = 0; d < S::DT; ++d) {
-          u32x4 v = v_operand(d, s);
-          if (CAREFUL && poison) v = v_part(v, kVFinite);
-          o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, p[s]),
-                                                         o[d], 0, 0, 0);
+          for (int d = 0; d < S::DT; ++d) {
+            u32x4 v = v_operand(d, s);
+            if (poison) v = v_part(v, kVFinite);
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v), __builtin_bit_cast(bf16x8, p[s]),
+                                                           o[d], 0, 0, 0);
+          }
         }
+      } else {
+        // Each product of step s goes out with its share of what step s + 1 needs:
+        // two reads of V and 8 / DT weights, which run beside it.
+        u32x4 v[2][S::DT];
+#pragma unroll
+        for (int d = 0; d < S::DT; ++d) v[0][d] = v_operand(d, 0);
+        weights(0, 0, 8);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+          for (int d = 0; d < S::DT; ++d) {
+            o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, v[s % 2][d]),
+                                                           __builtin_bit_cast(bf16x8, p[s]), o[d], 0, 0, 0);
+            if (s < 3) {
+              v[(s + 1) % 2][d] = v_operand(d, s + 1);
+              weights(s + 1, 8 * d / S::DT, 8 * (d + 1) / S::DT);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          }
+      }
       if (CAREFUL && poison) {
 #pragma unroll
         for (int d = 0; d < S::DT; ++d)
@@ -283,6 +337,10 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
       }
     }
     if (tile + 1 < ntiles) {
+      if (tile + 2 < ntiles) {
+        locate(tile + 2, page);
+        if (tile + 3 < ntiles) page = fetch_page(tile + 3);
+      }
       // the other buffer was last read before the previous barrier
       put(tile + 1);
       __syncthreads();
@@ -294,7 +352,7 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   }
 
   if (!row_ok) return false;
-  l += __shfl_xor(l, 32);
+  l = sum_halves(l);
   const float vs = a.cache.v_scale ? a.cache.v_scale[kvh] : 1.f;
   const float f = it.unit >= 0 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));
   const int64_t pr = it.unit >= 0 ? part_row(a, it.unit + row / kUnitRows, h, row % kUnitRows) : 0;
@@ -326,34 +384,6 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   return false;
 }
 
-template <int DP, bool FP8, bool GENERAL>
-__global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_tile_kernel(AttnArgs a) {
-  __shared__ __align__(16) uint16_t lds[2 * TileShape<DP, FP8>::BUF];
-  __shared__ int flag_lds[4];
-  // the longest ranges of a causal prompt come last in the list and run first
-  const int h = blockIdx.x % a.heads, index = a.info[1] - 1 - (int)(blockIdx.x / a.heads);
-  if (index < 0) return;
-  const AttnItem it = load_item(a.items, index);
-  if (run_tile<DP, FP8, GENERAL, false>(a, it, h, lds, flag_lds))
-    run_tile<DP, FP8, GENERAL, true>(a, it, h, lds, flag_lds);
-}
-
-template <int DP, bool GENERAL>
-void start_tile(const AttnArgs &a, AttnKind kind, dim3 grid, hipStream_t s) {
-  if (kind == kAttnE4m3) attn_tile_kernel<DP, true, GENERAL><<<grid, dim3(256), 0, s>>>(a);
-  else attn_tile_kernel<DP, false, GENERAL><<<grid, dim3(256), 0, s>>>(a);
-}
-
 }  // namespace
-
-hipError_t launch_attn_tile(const AttnArgs &a, AttnKind kind, hipStream_t s) {
-  const dim3 grid((unsigned)((int64_t)a.max_items * a.heads));
-  // the plain form supposes a positive factor (hidden scores are -inf before it)
-  const bool general = a.cap > 0.f || a.slopes || !(a.scale > 0.f);
-  if (a.dim <= 64) general ? start_tile<64, true>(a, kind, grid, s) : start_tile<64, false>(a, kind, grid, s);
-  else if (a.dim <= 128) general ? start_tile<128, true>(a, kind, grid, s) : start_tile<128, false>(a, kind, grid, s);
-  else general ? start_tile<256, true>(a, kind, grid, s) : start_tile<256, false>(a, kind, grid, s);
-  return hipGetLastError();
-}
 
 }  // namespace lora

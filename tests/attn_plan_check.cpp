@@ -103,15 +103,27 @@ static void capacities() {
       for (int n = seqs * g / groups; n < seqs * (g + 1) / groups; ++n) len += q[n];
       cut(len, upto(50000), true);
     }
-    int64_t total[2] = {0, 0};
-    for (auto &t : tiles) total[!t.few] += t.len;
-    const int c[2] = {keys_per_item(total[0], heads, kFewTarget, kFewMinKeys), keys_per_item(total[1], heads, kTileTarget, kTileMinKeys)};
-    int64_t items[2] = {0, 0}, units = 0;
+    // the few-row tiles' keys on one line, cut into slices; the others in parts
+    int64_t line = 0, total = 0;
+    for (auto &t : tiles) (t.few ? line : total) += t.few ? line_keys((int)t.len) : t.len;
+    const int slice = share_of(line, heads, kFewSlots, kFewMinKeys), share = share_of(total, heads, kTileSlots, kTileMinKeys);
+    CHECK(slice % kCutKeys == 0 && (int64_t)slice * (cap.slots - 1) >= line);
+    int64_t items[2] = {0, 0}, units = 0, at = 0;
     for (auto &t : tiles) {
       CHECK(t.ntok * group <= (t.few ? kFewRows : kTileQRows));
-      const int64_t splits = t.len > c[!t.few] ? ceil_div64(t.len, c[!t.few]) : 1;
-      items[!t.few] += splits;
-      if (t.parts || splits > 1) units += splits * ceil_div64(t.ntok * group, kUnitRows);
+      int64_t parts;
+      if (t.few) {
+        const int64_t last = at + line_keys((int)t.len) - 1;
+        parts = last / slice - at / slice + 1;
+        CHECK(last / slice < cap.slots - 1);
+        at = last + 1;
+      } else {
+        const int per = part_keys((int)t.len, share);
+        CHECK(per >= 1 && per <= share && (per == t.len || per % kCutKeys == 0 || t.len == 0));
+        parts = t.len ? ceil_div64(t.len, per) : 1;
+      }
+      items[!t.few] += parts;
+      if (t.parts || parts > 1) units += parts * ceil_div64(t.ntok * group, kUnitRows);
     }
     CHECK((int64_t)tiles.size() <= cap.tiles);
     CHECK(items[0] <= cap.few_items);
