@@ -454,7 +454,7 @@ lora_status lora_cache_append(const void *d_qkv, int64_t ldx, int64_t num_tokens
  * A sequence is bad if its q_start leaves the bounds above, if it has more
  * query tokens than max_q_len or than keys, or if its keys do not fit
  * page_table_stride pages; its tokens see no key.  Supported: num_tokens <=
- * 2^24, num_seqs <= 2^20, num_q_heads <= 1024, page_table_stride * page_size <=
+ * 2^24, num_tokens * num_q_heads < 2^31, num_seqs <= 2^20, num_q_heads <= 1024, page_table_stride * page_size <=
  * 2^31 - 2^16.  A group is bad, and ignored,
  * if its bounds are not ascending in [0, num_seqs], its length is negative or
  * beyond the keys of its first sequence.  Keys in a page whose id lies outside
@@ -489,7 +489,7 @@ typedef struct lora_attn_meta {
     int32_t heads_per_item, head_groups;   /* query heads of one work item; items per key head */
     int32_t max_tiles, max_slots, max_tile_items;
     const int32_t *page_table;
-    int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_tokens;
+    int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_list;
 } lora_attn_meta;
 
 /* Device workspace of lora_prepare_attn_meta for this batch and cache (sizes

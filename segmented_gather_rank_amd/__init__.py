@@ -82,7 +82,7 @@ class lora_attn_meta(C.Structure):
                 ("heads_per_item", C.c_int32), ("head_groups", C.c_int32), ("max_tiles", C.c_int32),
                 ("max_slots", C.c_int32), ("max_tile_items", C.c_int32), ("page_table", C.c_void_p),
                 ("limits", C.c_void_p), ("info", C.c_void_p), ("tiles", C.c_void_p), ("few_items", C.c_void_p), ("slots", C.c_void_p),
-                ("tile_items", C.c_void_p), ("join", C.c_void_p), ("join_tokens", C.c_void_p)]
+                ("tile_items", C.c_void_p), ("join", C.c_void_p), ("join_list", C.c_void_p)]
 
 
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t

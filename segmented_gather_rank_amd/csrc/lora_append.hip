@@ -72,7 +72,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
   }
   const bool keep = slot >= 0;
   // small caches divide in 32 bits
-  const int64_t page = !keep ? 0 : a.num_slots <= 0x7fffffff ? (int64_t)((uint32_t)slot / (uint32_t)a.page_size) : slot / a.page_size;
+  const int64_t page = !keep ? 0 : a.num_slots <= 0x7fffffff ? (int64_t)a.by_page.quotient((uint32_t)slot) : slot / a.page_size;
   const int64_t place = keep ? page * a.page_stride + (slot - page * a.page_size) * a.pos_stride : 0;
   const char *x = a.x + t * a.ldx * (int64_t)sizeof(X);
   const int both = a.q_heads + a.kv_heads, half = a.half, rot = 2 * half;
@@ -94,7 +94,7 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
 
   for (int u = threadIdx.x; u < n_rot + n_copy + n_v; u += 256) {
     if (u < n_rot) {
-      const int head = (int)div_by(u, rot_per, a.unit_magic[0]), c = u - head * rot_per;
+      const int head = (int)a.units[0].quotient(u), c = u - head * rot_per;
       const int d0 = a.interleaved ? 16 * c : 8 * c, d1 = a.interleaved ? d0 + 8 : d0 + half;
       float p[8], q[8], cs[8], sn[8];
       Vec8<X>::load(x, source(head) + d0, p);
@@ -143,12 +143,12 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs a) {
       put(head, d0, o0);
       put(head, d1, o1);
     } else if (u < n_rot + n_copy) {
-      const int w = u - n_rot, head = (int)div_by(w, copy_per, a.unit_magic[1]), d = rot + 8 * (w - head * copy_per);
+      const int w = u - n_rot, head = (int)a.units[1].quotient(w), d = rot + 8 * (w - head * copy_per);
       float v[8];
       Vec8<X>::load(x, source(head) + d, v);
       put(head, d, v);
     } else if (keep) {
-      const int w = u - n_rot - n_copy, vh = (int)div_by(w, v_per, a.unit_magic[2]), d = 8 * (w - vh * v_per);
+      const int w = u - n_rot - n_copy, vh = (int)a.units[2].quotient(w), d = 8 * (w - vh * v_per);
       float v[8];
       Vec8<X>::load(x, a.off_v + (int64_t)vh * a.dim + d, v);
       Vec8<C>::store(a.v, place + vh * a.head_stride + d, v, a.v_scale ? a.v_scale[vh] : 1.f);

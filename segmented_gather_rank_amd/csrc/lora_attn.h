@@ -23,24 +23,24 @@ constexpr int kFewRows = 16;
 constexpr int kTileQRows = 128;
 // A partial-result unit: 16 rows of one head group.
 constexpr int kUnitRows = 16;
-// Workgroups that the chip holds of the attention kernels: 256 CUs with two each
-// (registers).  The few-row kernel's keys are laid end to end and cut into one
-// slice per workgroup; a tile's keys are cut only where the tiles alone would
-// leave workgroups without work.
-constexpr int kFewSlots = 256;
+// Workers that the work is cut for.  The few-row kernel's keys are laid end to end
+// and cut into one slice per wave; a tile's keys are cut only where the tiles
+// alone would leave workgroups without work (256 CUs with two each).
+constexpr int kFewSlots = 1024;
 constexpr int kTileSlots = 512;
-// Shortest slice and shortest part of a tile, in keys: one step of every wave;
-// four tiles of 64.
-constexpr int kFewMinKeys = 128;
+// Shortest slice and shortest part of a tile, in keys: one step; four tiles.
+constexpr int kFewMinKeys = 32;
 constexpr int kTileMinKeys = 256;
 // Workgroups that the tile items of a call are spread over at most.
 constexpr int kMaxTileBlocks = 4096;
-// Granularity of slices and parts.
-constexpr int kCutKeys = 64;
+// Granularity of slices and of parts: a step of either kernel.
+constexpr int kCutKeys = 32;
+constexpr int kPartKeys = 64;
 
 constexpr int kAttnTileInts = 12;  // see AttnTile
 constexpr int kAttnItemInts = 8;   // see AttnItem
 constexpr int kAttnSlotInts = 12;  // see AttnSlot
+constexpr int kAttnJoinInts = 12;  // a token to join: token, 3 unused, its own parts, its group's parts
 constexpr int kAttnInfoInts = 16;
 
 LORA_HD int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -53,27 +53,27 @@ LORA_HD int heads_per_item(int per_kv) {
   return 1;
 }
 
-LORA_HD int round_cut(int64_t keys) {
-  const int64_t c = (keys + kCutKeys - 1) & ~(int64_t)(kCutKeys - 1);
+LORA_HD int round_to(int64_t keys, int step) {
+  const int64_t c = (keys + step - 1) & ~(int64_t)(step - 1);
   return c > (1 << 30) ? (1 << 30) : (int)c;
 }
 
 // Length of a slice (few-row kernel) or most keys of a part (tile kernel): an
 // equal share of all keys for each of the `slots` workgroups, heads of which
-// work on the same keys, and at least `least`.
+// work on the same keys, and at least `least`, in whole steps.
 LORA_HD int slots_per_head(int heads, int slots) { return slots / heads > 0 ? slots / heads : 1; }
-LORA_HD int share_of(int64_t total, int heads, int slots, int least) {
+LORA_HD int share_of(int64_t total, int heads, int slots, int least, int step) {
   const int64_t c = ceil_div64(total, slots_per_head(heads, slots));
-  return round_cut(c < least ? least : c);
+  return round_to(c < least ? least : c, step);
 }
 
 // Keys that a few-row tile occupies on the line that is cut into slices.
-LORA_HD int line_keys(int keys) { return keys > 0 ? round_cut(keys) : kCutKeys; }
+LORA_HD int line_keys(int keys) { return keys > 0 ? round_to(keys, kCutKeys) : kCutKeys; }
 
 // Parts of a tile-kernel tile: equal parts of at most `share` keys.
 LORA_HD int part_keys(int keys, int share) {
   if (keys <= share) return keys > 0 ? keys : 1;
-  return round_cut(ceil_div64(keys, ceil_div64(keys, share)));
+  return round_to(ceil_div64(keys, ceil_div64(keys, share)), kPartKeys);
 }
 
 // Capacities of the work lists, from sizes the host knows.
@@ -144,11 +144,19 @@ LORA_HD uint32_t div_by(uint32_t x, uint32_t d, uint32_t m) {
   return q - (q * d > x ? 1u : 0u);
 }
 
+// A divisor that the host knows, with its magic number.
+struct Divisor {
+  uint32_t d, m;
+  LORA_HD uint32_t quotient(uint32_t x) const { return div_by(x, d, m); }
+};
+LORA_HD Divisor divisor(uint32_t d) { return Divisor{d, div_magic(d)}; }
+
 // What the attention kernels know of the cache.
 struct CacheView {
   const char *k, *v;
   int64_t page_bytes, head_bytes, pos_bytes;
-  uint32_t num_pages, page_size, page_magic;
+  uint32_t num_pages;
+  Divisor page_size;
   const int32_t *table;
   int64_t table_stride;
   const float *k_scale, *v_scale;
@@ -158,7 +166,7 @@ struct CacheView {
 // page id its table holds; ids outside [0, num_pages) give -1.
 LORA_HD int64_t key_offset(const CacheView &c, uint32_t key, int32_t page) {
   if ((uint32_t)page >= c.num_pages) return -1;
-  const uint32_t at = key - div_by(key, c.page_size, c.page_magic) * c.page_size;
+  const uint32_t at = key - c.page_size.quotient(key) * c.page_size.d;
   return (int64_t)page * c.page_bytes + (int64_t)at * c.pos_bytes;
 }
 

@@ -4,7 +4,7 @@
 // Few-row work is bound by HBM and tile work by the matrix cores, so a batch that
 // has both runs them side by side: the slices' workgroups come first, one per CU,
 // and the tile items' fill the CUs' second places.  Slices are alike by
-// construction, so each has one workgroup.  Tile items are taken longest first,
+// construction, so each has one wave.  Tile items are taken longest first,
 // by as many workgroups as there are items, or in rounds beyond kMaxTileBlocks.
 #include "lora_attn_few.h"
 #include "lora_attn_tile.h"
@@ -13,120 +13,132 @@ namespace lora {
 
 namespace {
 
-template <int DP, bool FP8, bool GENERAL>
-__device__ __forceinline__ void run_slot(const AttnArgs &a, int index, char *lds, float (*ml_lds)[16][2]) {
-  const int h = index % a.heads;
-  const int32_t *p = a.slots + (int64_t)(index / a.heads) * kAttnSlotInts;
+__host__ __device__ inline int few_blocks(const AttnArgs &a) { return (a.few_waves + 3) / 4; }
+
+// A wave's slice: f(item, head group) for each of its items.
+template <typename F>
+__device__ __forceinline__ void run_slice(const AttnArgs &a, F &&f) {
+  const int w = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
+  if (w >= a.few_waves) return;
+  const int slot = a.by_heads.quotient(w), h = w - slot * a.heads;
+  const int32_t *p = a.slots + (int64_t)slot * kAttnSlotInts;
   const int first = p[0], end = p[1];
   AttnItem it{p[4], p[5], p[6], p[7], p[8], p[9], p[10], p[11]};
   for (int i = first; i < end; ++i) {
-    if (i > first) {
-      __syncthreads();  // the last item's results are read
-      it = load_item(a.few_items, i);
-    }
-    if (run_few<DP, FP8, GENERAL, false>(a, it, h, lds, ml_lds)) run_few<DP, FP8, GENERAL, true>(a, it, h, lds, ml_lds);
+    if (i > first) it = load_item(a.few_items, i);
+    f(it, h);
   }
+}
+template <int DP, bool FP8, bool GENERAL>
+__device__ __forceinline__ void run_few_slice(const AttnArgs &a, uint16_t *lds) {
+  uint16_t *v = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * FewShape<DP, FP8>::REGION;
+  run_slice(a, [&](const AttnItem &it, int h) {
+    if (run_few<DP, FP8, GENERAL, false>(a, it, h, v)) run_few<DP, FP8, GENERAL, true>(a, it, h, v);
+  });
 }
 
 // Slices only (decode).
 template <int DP, bool FP8, bool GENERAL>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_kernel(AttnArgs a) {
-  __shared__ __align__(16) char lds[4 * FewShape<DP, FP8>::REGION];
-  __shared__ float ml_lds[4][16][2];
-  run_slot<DP, FP8, GENERAL>(a, blockIdx.x, lds, ml_lds);
+  __shared__ __align__(16) uint16_t lds[4 * FewShape<DP, FP8>::REGION];
+  run_few_slice<DP, FP8, GENERAL>(a, lds);
 }
 
 template <int DP, bool GENERAL>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(AttnArgs a) {
-  __shared__ __align__(16) char lds[4 * 16 * (DP + 4) * 4];
-  __shared__ float ml_lds[4][16][2];
-  const int h = blockIdx.x % a.heads;
-  const int32_t *p = a.slots + (int64_t)(blockIdx.x / a.heads) * kAttnSlotInts;
-  const int first = p[0], end = p[1];
-  for (int i = first; i < end; ++i) {
-    if (i > first) __syncthreads();
-    run_few_f32<DP, GENERAL>(a, load_item(a.few_items, i), h, lds, ml_lds);
-  }
+  run_slice(a, [&](const AttnItem &it, int h) { run_few_f32<DP, GENERAL>(a, it, h); });
 }
 
 template <int DP, bool FP8, bool GENERAL>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_both_kernel(AttnArgs a) {
-  constexpr int kFewLds = 4 * FewShape<DP, FP8>::REGION, kTileLds = 4 * TileShape<DP, FP8>::BUF;
-  __shared__ __align__(16) char lds[kFewLds > kTileLds ? kFewLds : kTileLds];
-  __shared__ float ml_lds[4][16][2];
+  constexpr int kFewLds = 4 * FewShape<DP, FP8>::REGION, kTileLds = 2 * TileShape<DP, FP8>::BUF;
+  __shared__ __align__(16) uint16_t lds[kFewLds > kTileLds ? kFewLds : kTileLds];
   __shared__ int flag_lds[4];
-  const int few_end = (a.few_blocks + 7) / 8 * 8, index = (int)blockIdx.x - few_end;
+  const int few_end = (few_blocks(a) + 7) / 8 * 8, index = (int)blockIdx.x - few_end;
   if (index < 0) {
-    if ((int)blockIdx.x < a.few_blocks) run_slot<DP, FP8, GENERAL>(a, blockIdx.x, lds, ml_lds);
+    run_few_slice<DP, FP8, GENERAL>(a, lds);
     return;
   }
   if (index >= a.tile_blocks) return;
-  const int h = index % a.heads, items = a.info[1];
+  const int first = a.by_heads.quotient(index), h = index - first * a.heads, items = a.info[1];
+  const int step = a.by_heads.quotient(a.tile_blocks);
   // the longest ranges of a causal prompt come last in the list and run first
-  for (int i = index / a.heads; i < items; i += a.tile_blocks / a.heads) {
-    if (i != index / a.heads) __syncthreads();
+  for (int i = first; i < items; i += step) {
+    if (i != first) __syncthreads();
     const AttnItem it = load_item(a.tile_items, items - 1 - i);
-    uint16_t *buf = reinterpret_cast<uint16_t *>(lds);
-    if (run_tile<DP, FP8, GENERAL, false>(a, it, h, buf, flag_lds)) run_tile<DP, FP8, GENERAL, true>(a, it, h, buf, flag_lds);
+    if (run_tile<DP, FP8, GENERAL, false>(a, it, h, lds, flag_lds)) run_tile<DP, FP8, GENERAL, true>(a, it, h, lds, flag_lds);
   }
 }
 
 // Rows whose result lies in parts: one wave per (token, query head) adds the
 // parts of its group's shared keys and of its own, weighted by their sums, in
-// the order of the keys.  Bound by latency (five dependent loads) for a few rows
-// and by L2 for many: lane p looks up part p, then 64 / LANES parts' outputs are
-// read at a time, four rounds in flight.
+// the order of the keys.  Bound by latency (three dependent loads) for few rows
+// and by L2 for many: lane p looks up part p, and the first parts' outputs, 64 /
+// LANES side by side and 8 loads a lane, are on their way while the parts' maxima
+// are reduced.
 template <int LANES, typename OUT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int SIDE = kWave / LANES;  // parts read side by side
+  constexpr int DEEP = 8;              // loads in flight a lane
   const int lane = threadIdx.x % kWave, side = lane / LANES, d = 4 * (lane % LANES);
-  const int64_t rows = (int64_t)a.info[4] * a.q_heads;
-  for (int64_t r = (int64_t)blockIdx.x * 4 + threadIdx.x / kWave; r < rows; r += (int64_t)gridDim.x * 4) {
-    const int t = __builtin_amdgcn_readfirstlane(a.join_tokens[r / a.q_heads]);
-    const int qh = __builtin_amdgcn_readfirstlane((int)(r % a.q_heads));
-    const int h = qh / a.group;
-    const int4 own = reinterpret_cast<const int4 *>(a.join)[2 * (int64_t)t];
-    const int4 pre = reinterpret_cast<const int4 *>(a.join)[2 * (int64_t)t + 1];
+  const uint32_t step = gridDim.x * 4;
+  uint32_t r = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
+  // the first row's record is read before it is known whether there is one
+  auto entry = [&](uint32_t row) {
+    const int64_t j = min((int64_t)a.by_q_heads.quotient(row), a.tokens - 1);
+    return reinterpret_cast<const int4 *>(a.join_list + kAttnJoinInts * j);
+  };
+  const int4 *e = entry(r);
+  int t = e[0].x;
+  int4 own = e[1], pre = e[2];
+  const uint32_t rows = (uint32_t)a.info[4] * a.q_heads;
+  for (; r < rows; r += step) {
+    const int qh = r - a.by_q_heads.quotient(r) * a.q_heads, h = a.by_group.quotient(qh), of_group = qh - h * a.group;
     const int n = own.y + pre.y;
     float m = kNegInf, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
     for (int p0 = 0; p0 < n; p0 += kWave) {
       // lane p: where part p0 + p lies, its maximum and sum
-      const int p = min(p0 + lane, n - 1);
+      const int p = min(p0 + lane, n - 1), count = min(kWave, n - p0);
       const bool shared = p < pre.y;
       const int4 rec = shared ? pre : own;
-      const int row = rec.w * a.group + qh % a.group;
+      const int row = rec.w * a.group + of_group;
       const int64_t pr = part_row(a, rec.x + (int64_t)(shared ? p : p - pre.y) * rec.z + row / kUnitRows, h, row % kUnitRows);
       const float pm = p0 + lane < n ? a.part_ml[2 * pr] : kNegInf, pl = a.part_ml[2 * pr + 1];
+      f32x4 v[DEEP];
+      auto fetch = [&](int q) {
+#pragma unroll
+        for (int u = 0; u < DEEP; ++u)
+          if (q + SIDE * u < count)
+            v[u] = gload16f(a.part + __shfl(pr, min(q + SIDE * u + side, count - 1)) * a.dim + (d < a.dim ? d : 0));
+      };
+      fetch(0);
       float top = fmaxf(m, pm);
 #pragma unroll
-      for (int x = 1; x < kWave; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+      for (int x = 1; x < 16; x *= 2) top = fmaxf(top, __shfl_xor(top, x));
+      top = max_rows(top);
       const float base = top == kNegInf ? 0.f : top;
       const float fade = exp2_fast(m - base);
-      // a part in which no key is seen has -inf and 0; with NaN it stays NaN
+      // a part in which no key is seen has -inf and 0
       const float f = p0 + lane < n ? exp2_fast(pm - base) : 0.f;
       m = top;
       float add = p0 + lane < n ? f * pl : 0.f;
 #pragma unroll
-      for (int x = 1; x < kWave; x *= 2) add += __shfl_xor(add, x);
-      l = l * fade + add;
+      for (int x = 1; x < 16; x *= 2) add += __shfl_xor(add, x);
+      l = l * fade + sum_rows(add);
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] *= fade;
-      const int count = min(kWave, n - p0);
-      for (int q = 0; q < count; q += 4 * SIDE) {
-        f32x4 v[4];
-        float w[4];
+      for (int q = 0; q < count; q += DEEP * SIDE) {
+        if (q) fetch(q);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int from = min(q + SIDE * u + side, count - 1);
-          const int64_t at = __shfl(pr, from);
-          w[u] = __shfl(f, from);
-          if (q + SIDE * u + side >= count) w[u] = 0.f;
-          v[u] = gload16f(a.part + at * a.dim + (d < a.dim ? d : 0));
-        }
+        for (int u = 0; u < DEEP; ++u)
+          if (q + SIDE * u < count) {
+            const int from = q + SIDE * u + side;
+            const float w = __shfl(f, min(from, count - 1));
+            if (from < count) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] += w[u] == 0.f ? 0.f : w[u] * v[u][i];
+              for (int i = 0; i < 4; ++i) o[i] += w == 0.f ? 0.f : w * v[u][i];
+            }
+          }
       }
     }
 #pragma unroll
@@ -146,15 +158,19 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
       }
     }
     if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+    if (r + step < rows) {
+      e = entry(r + step);
+      t = e[0].x, own = e[1], pre = e[2];
+    }
   }
 }
 
 template <int DP, bool FP8, bool GENERAL>
 void start(const AttnArgs &a, hipStream_t s) {
   if (a.tile_blocks == 0) {
-    attn_few_kernel<DP, FP8, GENERAL><<<dim3(a.few_blocks), dim3(256), 0, s>>>(a);
+    attn_few_kernel<DP, FP8, GENERAL><<<dim3(few_blocks(a)), dim3(256), 0, s>>>(a);
   } else {
-    const unsigned grid = 8 * ((a.few_blocks + 7) / 8 + (a.tile_blocks + 7) / 8);
+    const unsigned grid = 8 * ((few_blocks(a) + 7) / 8 + (a.tile_blocks + 7) / 8);
     attn_both_kernel<DP, FP8, GENERAL><<<dim3(grid), dim3(256), 0, s>>>(a);
   }
 }
@@ -164,8 +180,8 @@ void start(const AttnArgs &a, AttnKind kind, hipStream_t s) {
   // the plain form supposes a positive factor (hidden scores are -inf before it)
   const bool general = a.cap > 0.f || a.slopes || !(a.scale > 0.f);
   if (kind == kAttnF32) {
-    if (general) attn_few_f32_kernel<DP, true><<<dim3(a.few_blocks), dim3(256), 0, s>>>(a);
-    else attn_few_f32_kernel<DP, false><<<dim3(a.few_blocks), dim3(256), 0, s>>>(a);
+    if (general) attn_few_f32_kernel<DP, true><<<dim3(few_blocks(a)), dim3(256), 0, s>>>(a);
+    else attn_few_f32_kernel<DP, false><<<dim3(few_blocks(a)), dim3(256), 0, s>>>(a);
   } else if (kind == kAttnE4m3) {
     general ? start<DP, true, true>(a, s) : start<DP, true, false>(a, s);
   } else {

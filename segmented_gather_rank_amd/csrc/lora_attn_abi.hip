@@ -46,7 +46,7 @@ lora_status check_cache(const lora_kv_cache *c) {
 struct AttnSizes {
   int per_kv, group, heads, tile_rows;
   AttnCaps caps;
-  size_t limits, info, tiles, few, slots, big, join, join_tokens, total;
+  size_t limits, info, tiles, few, slots, big, join, join_list, total;
 };
 
 lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSizes &s) {
@@ -57,7 +57,7 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
       b->num_q_heads <= 0 || b->num_q_heads % c->num_heads || b->window < 0)
     return LORA_ERR_INVALID_ARG;
   if (b->num_tokens > (1 << 24) || b->num_seqs > (1 << 20) || b->num_groups > b->num_seqs ||
-      b->num_q_heads > 1024 || b->page_table_stride > 0x7fff0000 / c->page_size)
+      b->num_q_heads > 1024 || b->num_tokens * b->num_q_heads > 0x7fffffff || b->page_table_stride > 0x7fff0000 / c->page_size)
     return LORA_ERR_UNSUPPORTED;
   s.per_kv = b->num_q_heads / c->num_heads;
   s.group = heads_per_item(s.per_kv);
@@ -80,7 +80,7 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   s.slots = take(kAttnSlotInts * s.caps.slots);
   s.big = take(kAttnItemInts * s.caps.tile_items);
   s.join = take(8 * b->num_tokens);
-  s.join_tokens = take(b->num_tokens);
+  s.join_list = take(kAttnJoinInts * b->num_tokens);
   s.total = at;
   return LORA_OK;
 }
@@ -159,10 +159,11 @@ lora_status lora_cache_append(const void *d_qkv, int64_t ldx, int64_t T, lora_dt
   a.kv_heads = cache->num_heads;
   a.dim = cache->head_dim;
   a.page_size = cache->page_size;
-  // units per head of each kind (lora_append.hip), as magic divisors
   const int half = rot ? rot->rot_dim / 2 : 0;
-  const uint32_t per[3] = {(uint32_t)std::max(half / 8, 1), (uint32_t)std::max((a.dim - 2 * half) / 8, 1), (uint32_t)(a.dim / 8)};
-  for (int k = 0; k < 3; ++k) a.unit_magic[k] = div_magic(per[k]);
+  a.units[0] = divisor((uint32_t)std::max(half / 8, 1));
+  a.units[1] = divisor((uint32_t)std::max((a.dim - 2 * half) / 8, 1));
+  a.units[2] = divisor((uint32_t)(a.dim / 8));
+  a.by_page = divisor((uint32_t)a.page_size);
   if (rot) {
     a.pos = d_pos;
     a.table = rot->table;
@@ -234,7 +235,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.few_items = at(s.few);
   a.tile_items = at(s.big);
   a.join = at(s.join);
-  a.join_tokens = at(s.join_tokens);
+  a.join_list = at(s.join_list);
   a.slots = at(s.slots);
   a.max_slots = (int32_t)s.caps.slots;
 
@@ -262,7 +263,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   out->slots = a.slots;
   out->tile_items = a.tile_items;
   out->join = a.join;
-  out->join_tokens = a.join_tokens;
+  out->join_list = a.join_list;
   return launch_attn_plan(a, static_cast<hipStream_t>(stream)) == hipSuccess ? LORA_OK : LORA_ERR_HIP;
 }
 
@@ -286,9 +287,9 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
   if (m->num_kv_heads != cache->num_heads || m->head_dim != cache->head_dim || m->page_size != cache->page_size ||
       m->dtype != cache->dtype || m->head_groups <= 0 ||
       m->head_groups * m->heads_per_item * m->num_kv_heads != m->num_q_heads || !m->limits || !m->info ||
-      !m->few_items || !m->slots || !m->tile_items || !m->join || !m->join_tokens || m->max_slots < 1 || m->max_slots > 2048 ||
+      !m->few_items || !m->slots || !m->tile_items || !m->join || !m->join_list || m->max_slots < 1 || m->max_slots > 4096 ||
       m->max_tile_items < 0 ||
-      m->num_tokens < 0)
+      m->num_tokens < 0 || m->num_tokens > 0x7fffffff / m->num_q_heads)
     return LORA_ERR_INVALID_ARG;
   const int64_t width = (int64_t)m->num_q_heads * m->head_dim;
   if (ldq % 8 || ldq < width || ldo % 8 || ldo < width || !(cap >= 0.f) || !(cap < __builtin_inff())) return LORA_ERR_INVALID_ARG;
@@ -306,8 +307,7 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
   a.cache.head_bytes = cache->head_stride * e;
   a.cache.pos_bytes = cache->pos_stride * e;
   a.cache.num_pages = (uint32_t)cache->num_pages;
-  a.cache.page_size = (uint32_t)cache->page_size;
-  a.cache.page_magic = div_magic((uint32_t)cache->page_size);
+  a.cache.page_size = divisor((uint32_t)cache->page_size);
   a.cache.table = m->page_table;
   a.cache.table_stride = m->page_table_stride;
   a.cache.k_scale = cache->k_scale;
@@ -318,11 +318,11 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
   a.slopes = d_slopes;
   a.limits = m->limits;
   a.info = m->info;
-  a.join = m->join;
-  a.join_tokens = m->join_tokens;
+  a.join_list = m->join_list;
   a.ldq = ldq;
   a.ldo = ldo;
   a.tokens = m->num_tokens;
+  a.max_units = m->max_units;
   a.part_ml = static_cast<float *>(d_ws);
   a.part = reinterpret_cast<float *>(static_cast<char *>(d_ws) + ml);
   a.scale = scale;
@@ -330,7 +330,10 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
   a.group = m->heads_per_item;
   a.heads = m->num_q_heads / m->heads_per_item;
   a.q_heads = m->num_q_heads;
-  a.kv_parts = m->head_groups;
+  a.by_heads = divisor((uint32_t)a.heads);
+  a.by_group = divisor((uint32_t)a.group);
+  a.by_q_heads = divisor((uint32_t)a.q_heads);
+  a.by_kv_parts = divisor((uint32_t)m->head_groups);
   a.dim = m->head_dim;
 
   const AttnKind kind = kind_of(cache->dtype);
@@ -338,7 +341,7 @@ lora_status lora_attention(const lora_attn_meta *m, const void *d_q, int64_t ldq
   a.few_items = m->few_items;
   a.slots = m->slots;
   a.tile_items = m->tile_items;
-  a.few_blocks = (m->max_slots - 1) * a.heads;
+  a.few_waves = (m->max_slots - 1) * a.heads;
   // more tiles than this are taken in rounds (lora_attn.hip)
   a.tile_blocks = (int32_t)std::min<int64_t>((int64_t)m->max_tile_items * a.heads, kMaxTileBlocks / a.heads * a.heads);
   if (m->max_tile_items > 0 && a.tile_blocks == 0) a.tile_blocks = a.heads;

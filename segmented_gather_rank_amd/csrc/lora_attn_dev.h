@@ -153,9 +153,11 @@ __device__ __forceinline__ AttnItem load_item(const int32_t *items, int i) {
   return AttnItem{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
 }
 
-// Row `row` (of kUnitRows) of partial-result unit `unit`, head group h.
+// Row `row` (of kUnitRows) of partial-result unit `unit`, head group h.  A head
+// group's units lie together: the parts of a row are close in memory (one after
+// the other for a decode token), which spares address translations.
 __device__ __forceinline__ int64_t part_row(const AttnArgs &a, int64_t unit, int h, int row) {
-  return (unit * a.heads + h) * kUnitRows + row;
+  return (h * a.max_units + unit) * kUnitRows + row;
 }
 
 }  // namespace lora

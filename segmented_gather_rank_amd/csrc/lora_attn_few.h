@@ -12,12 +12,12 @@
 // transposing LDS read does.  No weight ever leaves its lane.
 //
 // Bound: the keys and values are read once and used by at most 16 rows, 16 / 2
-// operations per byte, so HBM bounds it.  Hence no sharing: each of the 4 waves
-// takes every fourth step of 32 keys with a softmax of its own, K goes from
-// global memory straight into operand registers, V through LDS that only its
-// wave touches (for the transposition), the next step's 16 loads of 16 bytes a
-// lane are in flight while a step is computed, and page ids are fetched two
-// steps ahead.  The waves meet once, at the end.
+// operations per byte, so HBM bounds it.  Hence no sharing: every wave is a
+// worker of its own with a slice of the keys (lora_attn.h), 32 keys a step, and
+// never waits for another.  K goes from global memory straight into operand
+// registers, V through LDS that only its wave touches (for the transposition),
+// the next step's 16 loads of 16 bytes a lane are in flight while a step is
+// computed, and page ids are fetched two steps ahead.
 #pragma once
 
 #include "lora_attn_dev.h"
@@ -28,62 +28,46 @@ namespace {
 
 constexpr int kStep = 32;  // keys per wave and step
 
-// The waves' maxima, sums and outputs combined; thread tid holds row tid / 16.
-// o_lds: [4] regions of `region` bytes, each float [16][DP + 4].
+// A wave's result, final or partial: lane (g, c) holds row c, dimensions
+// 16 d + 4 g .. + 3, and its row's maximum and sum.
 template <int DP, typename OUT>
-__device__ __forceinline__ void finish_few(const AttnArgs &a, const AttnItem &it, int h, const char *o_lds,
-                                           int region, const float (*ml)[16][2]) {
-  const int tid = thread_of_item(), row = tid / 16, j = tid % 16;
+__device__ __forceinline__ void finish_few(const AttnArgs &a, const AttnItem &it, int h, int lane, const f32x4 (&o)[DP / 16],
+                                           float base, float l) {
+  const int g = lane / 16, row = lane % 16;
   if (row >= it.ntok * a.group) return;
-  float m = ml[0][row][0];
-#pragma unroll
-  for (int w = 1; w < 4; ++w) m = fmaxf(m, ml[w][row][0]);
-  const float base = m == kNegInf ? 0.f : m;
-  float f[4], l = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = exp2_fast(ml[w][row][0] - base);
-    l += f[w] * ml[w][row][1];
-  }
-  const int t = it.tok0 + row / a.group, qh = h * a.group + row % a.group;
-  const float vs = a.cache.v_scale ? a.cache.v_scale[h / a.kv_parts] : 1.f;
+  const int nth = a.by_group.quotient(row), t = it.tok0 + nth, qh = h * a.group + row - nth * a.group;
+  const float vs = a.cache.v_scale ? a.cache.v_scale[a.by_kv_parts.quotient(h)] : 1.f;
   const float mul = it.unit >= 0 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));
   const int64_t pr = it.unit >= 0 ? part_row(a, it.unit, h, row) : 0;
 #pragma unroll
-  for (int q = 0; q < DP / 64; ++q) {
-    const int d = 64 * q + 4 * j;
-    if (d >= a.dim) break;
-    float o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int d = 0; d < DP / 16; ++d) {
+    const int at = 16 * d + 4 * g;
+    if (at >= a.dim) break;
+    float x[4];
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const f32x4 v = *reinterpret_cast<const f32x4 *>(o_lds + w * region + (row * (DP + 4) + d) * 4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] += f[w] * v[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = mul == 0.f ? 0.f : o[i] * mul;
+    for (int i = 0; i < 4; ++i) x[i] = mul == 0.f ? 0.f : o[d][i] * mul;
     if (it.unit >= 0) {
-      gstore16f(a.part + pr * a.dim + d, f32x4{o[0], o[1], o[2], o[3]});
+      gstore16f(a.part + pr * a.dim + at, f32x4{x[0], x[1], x[2], x[3]});
     } else if constexpr (sizeof(OUT) == 4) {
-      gstore16f(a.out + 4 * (t * a.ldo + (int64_t)qh * a.dim + d), f32x4{o[0], o[1], o[2], o[3]});
+      gstore16f(a.out + 4 * (t * a.ldo + (int64_t)qh * a.dim + at), f32x4{x[0], x[1], x[2], x[3]});
     } else {
       typedef __attribute__((address_space(1))) u32x2 g_u32x2;
-      *(g_u32x2 *)(a.out + 2 * (t * a.ldo + (int64_t)qh * a.dim + d)) =
-          u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
+      *(g_u32x2 *)(a.out + 2 * (t * a.ldo + (int64_t)qh * a.dim + at)) =
+          u32x2{pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
     }
   }
-  if (j == 0) {
+  if (g == 0) {
     if (it.unit >= 0) {
-      a.part_ml[2 * pr] = m;
+      a.part_ml[2 * pr] = base;
       a.part_ml[2 * pr + 1] = l;
     } else if (a.lse) {
-      a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+      a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (base + __log2f(l)) * kLn2;
     }
   }
 }
 
-// One item.  DP: head dimension rounded up to 64, 128 or 256 (dimensions past
-// a.dim are zeros).  FP8: e4m3 cache, widened to bf16 (exactly) on the way in.
+// One item.  DP: head dimension rounded up to 64, 128 or 256 (the
+// dimensions past a.dim are computed and dropped).  FP8: e4m3 cache, widened to bf16 (exactly) on the way in.
 // CAREFUL as in run_tile.
 template <int DP, bool FP8>
 struct FewShape {
@@ -93,33 +77,32 @@ struct FewShape {
   static constexpr int VROWS = 64 / CPR;               // V rows per load of the wave
   static constexpr int NV = kStep / VROWS;
   static constexpr int KL = FP8 ? KS / 2 : KS;         // 16-byte loads of one key's share of a lane
-  static constexpr int REGION = kStep * LDV * 2;       // LDS bytes of a wave
-  static_assert(REGION >= 16 * (DP + 4) * 4, "the waves' outputs reuse the V rows");
+  static constexpr int REGION = kStep * LDV;           // LDS elements of a wave
 };
 
 template <int DP, bool FP8, bool GENERAL, bool CAREFUL>
-__device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, int h, char *lds, float (*ml_lds)[16][2]) {
+__device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, int h, uint16_t *vl) {
   using S = FewShape<DP, FP8>;
-  const int tid = thread_of_item(), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int g = lane / 16, c = lane % 16;
-  const int kvh = h / a.kv_parts;
+  const int lane = thread_of_item() % kWave, g = lane / 16, c = lane % 16;
+  const int kvh = a.by_kv_parts.quotient(h);
   const bool row_ok = c < it.ntok * a.group;
-  const int tok = it.tok0 + (row_ok ? c / a.group : 0), qh = h * a.group + (row_ok ? c % a.group : 0);
+  const int nth = row_ok ? a.by_group.quotient(c) : 0;
+  const int tok = it.tok0 + nth, qh = h * a.group + (row_ok ? c - nth * a.group : 0);
 
   // lane j looks up key j of a step (both halves of the wave alike); beyond the
   // range the last key again, never seen
   const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
   auto page_of = [&](int step) -> int32_t {
     const int key = min(it.key0 + step * kStep + lane % kStep, it.key1 - 1);
-    return table[div_by(key, a.cache.page_size, a.cache.page_magic)];
+    return table[a.cache.page_size.quotient(key)];
   };
   const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
   const int nsteps = (it.key1 - it.key0 + kStep - 1) / kStep;
 
   int32_t page = 0, page_next = 0;
   if (nsteps > 0) {
-    page = page_of(wave);
-    page_next = page_of(wave + 4);
+    page = page_of(0);
+    page_next = page_of(1);
   }
 
   // Q: this row's share of the dimensions, in the order the K loads deliver them
@@ -131,6 +114,8 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
     if (row_ok && d < a.dim) w = gload16(a.q + 2 * (tok * a.ldq + (int64_t)qh * a.dim + d));
     q[s] = __builtin_bit_cast(bf16x8, w);
   }
+  // past the head dimension the first piece again: Q is zero there, and O^T's
+  // rows there are not stored
   auto k_ok = [&](int s) { return (FP8 ? 64 * s + 16 * g : 32 * s + 8 * g) < a.dim; };
   int lo = 0, hi = 0, pos = 0;
   if (row_ok) {
@@ -167,10 +152,9 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
   f32x4 o[DP / 16];
 #pragma unroll
   for (int d = 0; d < DP / 16; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint16_t *vl = reinterpret_cast<uint16_t *>(lds + wave * S::REGION);
 
-  if (wave < nsteps) issue(wave, page);
-  for (int step = wave; step < nsteps; step += 4) {
+  if (nsteps > 0) issue(0, page);
+  for (int step = 0; step < nsteps; ++step) {
     const int k0 = it.key0 + step * kStep;
     const bool masked = CAREFUL || k0 < it.full0 || k0 + kStep > min(it.full1, it.key1);
     // ---- scores
@@ -180,8 +164,7 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
       st[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < S::KL; ++s) {
-        u32x4 w = kr[t][s];
-        if (a.dim < DP && !k_ok(s)) w = u32x4{0, 0, 0, 0};
+        const u32x4 w = kr[t][s];
         if constexpr (FP8) {
           st[t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, e4m3x8_to_bf16(w[0], w[1])),
                                                           q[2 * s], st[t], 0, 0, 0);
@@ -214,9 +197,9 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
     poison = CAREFUL && __any(poison);
     const uint32_t good_now = good;
     // ---- the next step's loads
-    if (step + 4 < nsteps) {
-      issue(step + 4, page_next);
-      page_next = page_of(step + 8);
+    if (step + 1 < nsteps) {
+      issue(step + 1, page_next);
+      page_next = page_of(step + 2);
     }
     // ---- softmax
     if constexpr (GENERAL) {
@@ -289,20 +272,8 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
     }
   }
 
-  // ---- the waves' results
-  if constexpr (!CAREFUL) {
-    if (__syncthreads_or(odd)) return true;
-  }
-  l = sum_rows(l);
-  if (g == 0) {
-    ml_lds[wave][c][0] = base;
-    ml_lds[wave][c][1] = l;
-  }
-  float *ol = reinterpret_cast<float *>(lds + wave * S::REGION);
-#pragma unroll
-  for (int d = 0; d < DP / 16; ++d) *reinterpret_cast<f32x4 *>(ol + c * (DP + 4) + 16 * d + 4 * g) = o[d];
-  __syncthreads();
-  finish_few<DP, uint16_t>(a, it, h, lds, S::REGION, ml_lds);
+  if (!CAREFUL && __any(odd)) return true;
+  finish_few<DP, uint16_t>(a, it, h, lane, o, base, sum_rows(l));
   return false;
 }
 
@@ -310,14 +281,13 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
 // value of each operand a lane), 16 keys per wave and step.  Every call with an
 // fp32 cache comes here, in tiles of 16 rows.
 template <int DP, bool GENERAL>
-__device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &it, int h, char *lds, float (*ml_lds)[16][2]) {
+__device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &it, int h) {
   constexpr int NC = DP / 16;  // 16-byte loads of one key's share of a lane
-  constexpr int REGION = 16 * (DP + 4) * 4;
-  const int tid = thread_of_item(), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int g = lane / 16, c = lane % 16;
-  const int kvh = h / a.kv_parts;
+  const int lane = thread_of_item() % kWave, g = lane / 16, c = lane % 16;
+  const int kvh = a.by_kv_parts.quotient(h);
   const bool row_ok = c < it.ntok * a.group;
-  const int tok = it.tok0 + (row_ok ? c / a.group : 0), qh = h * a.group + (row_ok ? c % a.group : 0);
+  const int nth = row_ok ? a.by_group.quotient(c) : 0;
+  const int tok = it.tok0 + nth, qh = h * a.group + (row_ok ? c - nth * a.group : 0);
   const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
   const char *k_head = a.cache.k + kvh * a.cache.head_bytes, *v_head = a.cache.v + kvh * a.cache.head_bytes;
   const int nsteps = (it.key1 - it.key0 + 15) / 16;
@@ -339,10 +309,10 @@ __device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &i
   f32x4 o[NC];
 #pragma unroll
   for (int d = 0; d < NC; ++d) o[d] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int step = wave; step < nsteps; step += 4) {
+  for (int step = 0; step < nsteps; ++step) {
     const int k0 = it.key0 + step * 16;
     const int key_c = k0 + c;
-    const int32_t page = key_c < it.key1 ? table[div_by(key_c, a.cache.page_size, a.cache.page_magic)] : -1;
+    const int32_t page = key_c < it.key1 ? table[a.cache.page_size.quotient(key_c)] : -1;
     const int64_t off = key_offset(a.cache, key_c, page);
     const uint64_t good = __ballot(off >= 0);
     f32x4 kr[NC];
@@ -417,16 +387,7 @@ __device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &i
       }
     }
   }
-  l = sum_rows(l);
-  if (g == 0) {
-    ml_lds[wave][c][0] = m;
-    ml_lds[wave][c][1] = l;
-  }
-  float *ol = reinterpret_cast<float *>(lds + wave * REGION);
-#pragma unroll
-  for (int d = 0; d < NC; ++d) *reinterpret_cast<f32x4 *>(ol + c * (DP + 4) + 16 * d + 4 * g) = o[d];
-  __syncthreads();
-  finish_few<DP, float>(a, it, h, lds, REGION, ml_lds);
+  finish_few<DP, float>(a, it, h, lane, o, m, sum_rows(l));
 }
 
 }  // namespace

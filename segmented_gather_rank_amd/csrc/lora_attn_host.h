@@ -14,7 +14,7 @@ struct AttnPlanArgs {
   int32_t seqs, groups, max_q_len, page_size, causal, window;
   int32_t heads, group, tile_rows;
   int32_t max_tiles, max_few_items, max_tile_items, max_units, max_slots;
-  int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_tokens, *seq_base, *group_base;
+  int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_list, *seq_base, *group_base;
 };
 hipError_t launch_attn_plan(const AttnPlanArgs &a, hipStream_t s);
 
@@ -24,13 +24,15 @@ struct AttnArgs {
   char *out;
   float *lse;                // [T][q_heads] or NULL
   const float *slopes;       // [q_heads] or NULL
-  const int32_t *limits, *info, *few_items, *slots, *tile_items, *join, *join_tokens;
+  const int32_t *limits, *info, *few_items, *slots, *tile_items, *join_list;
   int64_t ldq, ldo, tokens;  // elements
+  int64_t max_units;
   float *part;               // partial results: see part_row
   float *part_ml;
   float scale, cap;
-  int32_t heads, group, q_heads, kv_parts, dim;  // kv_parts: head groups per key head
-  int32_t few_blocks, tile_blocks;  // workgroups of the two kinds; tile_blocks = 0: few rows only
+  int32_t heads, group, q_heads, dim;
+  Divisor by_heads, by_group, by_q_heads, by_kv_parts;  // kv_parts: head groups per key head
+  int32_t few_waves, tile_blocks;  // slices times head groups, workgroups of tile items (0: few rows only)
 };
 
 // Kind of the cache's elements (and with it of q and out).
@@ -54,7 +56,8 @@ struct AppendArgs {
   int32_t *num_bad;
   int32_t q_heads, kv_heads, dim, page_size, half, axes, interleaved;
   int32_t axis_end[4];
-  uint32_t unit_magic[3];          // div_magic of the units per head: turned, copied, v
+  Divisor units[3];                // units per head: turned, copied, v
+  Divisor by_page;
 };
 hipError_t launch_append(const AppendArgs &a, AttnKind kind, hipStream_t s);
 

@@ -216,8 +216,8 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a)
   }
   if (keys) atomicAdd(&sum_lds, keys);
   __syncthreads();
-  const int slice = share_of(line * kCutKeys, a.heads, kFewSlots, kFewMinKeys);
-  const int share = share_of((int64_t)sum_lds, a.heads, kTileSlots, kTileMinKeys);
+  const int slice = share_of(line * kCutKeys, a.heads, kFewSlots, kFewMinKeys, kCutKeys);
+  const int share = share_of((int64_t)sum_lds, a.heads, kTileSlots, kTileMinKeys, kPartKeys);
   const int cuts = slice / kCutKeys;  // of a slice
   const int slots = (int)min((line + cuts - 1) / cuts, (long long)a.max_slots - 1);
 
@@ -280,7 +280,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a)
           int4 *rec = reinterpret_cast<int4 *>(a.join) + 2 * (int64_t)(r.tok0 + t);
           rec[r.shared == 1] = int4{unit, fits ? parts : 0, ups, t};
           if (r.shared == 0) rec[1] = int4{0, 0, 0, 0};
-          if (r.shared != 1 && at_join + t < a.tokens) a.join_tokens[at_join + t] = r.tok0 + t;
+          if (r.shared != 1 && at_join + t < a.tokens) a.join_list[kAttnJoinInts * (int64_t)(at_join + t)] = r.tok0 + t;
         }
       }
     }
@@ -302,6 +302,14 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a)
     a.info[7] = share;
     a.info[8] = few_items;
     for (int k = 9; k < kAttnInfoInts; ++k) a.info[k] = 0;
+  }
+  // the list of tokens to join takes their records along
+  __syncthreads();
+  for (int j = tid; j < min((int64_t)joins, a.tokens); j += kPlanThreads) {
+    int4 *e = reinterpret_cast<int4 *>(a.join_list + kAttnJoinInts * (int64_t)j);
+    const int4 *rec = reinterpret_cast<const int4 *>(a.join) + 2 * (int64_t)e[0].x;
+    e[1] = rec[0];
+    e[2] = rec[1];
   }
   // slices without work
   for (int k = slots + tid; k < a.max_slots; k += kPlanThreads) slot_list[k].first = slot_list[k].end = 0;

@@ -46,22 +46,25 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   using S = TileShape<DP, FP8>;
   const int tid = thread_of_item(), lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int g = lane / 32, c = lane % 32;
-  const int kvh = h / a.kv_parts;
+  const int kvh = a.by_kv_parts.quotient(h);
   const int row = 32 * wave + c, rows = it.ntok * a.group;
   const bool row_ok = row < rows;
-  const int tok = it.tok0 + (row_ok ? row / a.group : 0), qh = h * a.group + (row_ok ? row % a.group : 0);
+  const int nth = row_ok ? a.by_group.quotient(row) : 0;
+  const int tok = it.tok0 + nth, qh = h * a.group + (row_ok ? row - nth * a.group : 0);
   const bool wave_ok = 32 * wave < rows;
 
   const int32_t *table = a.cache.table + it.seq * a.cache.table_stride;
   const int ntiles = (it.key1 - it.key0 + kKeys - 1) / kKeys;
   const int piece = tid % S::CPR, lrow = tid / S::CPR;
+  // past the head dimension the first piece again: Q is zero there, and O^T's
+  // rows there are not stored
   const bool piece_ok = piece * (FP8 ? 16 : 8) < a.dim;
   const char *k_piece = a.cache.k + kvh * a.cache.head_bytes + (piece_ok ? 16 * piece : 0);
 
   // lane j of every wave looks up key j of a tile
   auto fetch_page = [&](int tile) -> int32_t {
     const int key = min(it.key0 + tile * kKeys + lane, it.key1 - 1);
-    return table[div_by(key, a.cache.page_size, a.cache.page_magic)];
+    return table[a.cache.page_size.quotient(key)];
   };
   u32x4 kr[S::NL], vr[S::NL];
   uint64_t good = 0;  // keys of the issued tile in a good page
@@ -94,7 +97,7 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   // Registers to LDS.  In K the 8 spare elements of a row tell whether it is a
   // key (CAREFUL).  Returns whether V holds what a weight of zero does not hide.
   auto stage_as = [&](int tile, auto plain_tag) -> bool {
-    constexpr bool PLAIN = decltype(plain_tag)::value;  // all keys seen, all pieces
+    constexpr bool PLAIN = decltype(plain_tag)::value;  // all keys seen
     uint16_t *kl = lds + (tile & 1) * S::BUF, *vl = kl + kKeys * S::LDK;
     bool poison = false;
 #pragma unroll
@@ -102,7 +105,6 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
       const int r = S::ROWS * i + lrow;
       u32x4 k = kr[i], v = vr[i];
       if constexpr (!PLAIN) {
-        if (!piece_ok) k = v = u32x4{0, 0, 0, 0};
         if constexpr (CAREFUL) {
           if (!((good >> r) & 1)) k = v = u32x4{0, 0, 0, 0};
           if (piece == 0) kl[r * S::LDK + DP] = (good >> r) & 1;
@@ -132,10 +134,6 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
   auto put = [&](int tile) {
     if constexpr (CAREFUL) {
       if (stage_as(tile, std::false_type{})) atomicOr(&flag_lds[tile & 3], 1);
-    } else if (a.dim < DP) {
-      // the spare dimensions are zeros in every tile
-      const bool poison = stage_as(tile, std::false_type{});
-      odd |= poison && is_masked(tile);
     } else if (is_masked(tile)) {
       odd |= stage_as(tile, std::false_type{});
     } else {

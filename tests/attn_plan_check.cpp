@@ -48,13 +48,12 @@ static void addresses() {
     c.head_bytes = (tokens ? 1 : page) * dim;
     c.page_bytes = (int64_t)page * heads * dim;
     c.num_pages = (uint32_t)pages;
-    c.page_size = (uint32_t)page;
-    c.page_magic = div_magic((uint32_t)page);
+    c.page_size = divisor((uint32_t)page);
     const int64_t size = pages * c.page_bytes;
     std::vector<int32_t> table(8);
     for (auto &p : table) p = rnd() % 4 ? (int32_t)upto(pages - 1) : (int32_t)rnd();
     for (uint32_t key = 0; key < 8u * page; ++key) {
-      const int32_t id = table[div_by(key, c.page_size, c.page_magic)];
+      const int32_t id = table[c.page_size.quotient(key)];
       const int64_t off = key_offset(c, key, id);
       if (id < 0 || id >= pages) {
         CHECK(off == -1);
@@ -106,7 +105,7 @@ static void capacities() {
     // the few-row tiles' keys on one line, cut into slices; the others in parts
     int64_t line = 0, total = 0;
     for (auto &t : tiles) (t.few ? line : total) += t.few ? line_keys((int)t.len) : t.len;
-    const int slice = share_of(line, heads, kFewSlots, kFewMinKeys), share = share_of(total, heads, kTileSlots, kTileMinKeys);
+    const int slice = share_of(line, heads, kFewSlots, kFewMinKeys, kCutKeys), share = share_of(total, heads, kTileSlots, kTileMinKeys, kPartKeys);
     CHECK(slice % kCutKeys == 0 && (int64_t)slice * (cap.slots - 1) >= line);
     int64_t items[2] = {0, 0}, units = 0, at = 0;
     for (auto &t : tiles) {
@@ -119,7 +118,7 @@ static void capacities() {
         at = last + 1;
       } else {
         const int per = part_keys((int)t.len, share);
-        CHECK(per >= 1 && per <= share && (per == t.len || per % kCutKeys == 0 || t.len == 0));
+        CHECK(per >= 1 && per <= share && (per == t.len || per % kPartKeys == 0 || t.len == 0));
         parts = t.len ? ceil_div64(t.len, per) : 1;
       }
       items[!t.few] += parts;

@@ -143,7 +143,7 @@ def test_workspaces():
 def meta(**kw):
     m = dict(num_tokens=20, page_table_stride=10, max_units=50, num_seqs=5, num_q_heads=4, num_kv_heads=2, head_dim=64,
              page_size=16, dtype=L.LORA_BF16, heads_per_item=2, head_groups=1, max_tiles=5, max_slots=9,
-             max_tile_items=9, page_table=P, limits=P, info=P, tiles=P, few_items=P, slots=P, tile_items=P, join=P, join_tokens=P)
+             max_tile_items=9, page_table=P, limits=P, info=P, tiles=P, few_items=P, slots=P, tile_items=P, join=P, join_list=P)
     m.update(kw)
     return L.lora_attn_meta(**m)
 
