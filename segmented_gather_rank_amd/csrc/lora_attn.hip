@@ -30,8 +30,7 @@ __device__ __forceinline__ void run_slice(const AttnArgs &a, F &&f) {
   }
 }
 template <int DP, bool FP8, bool GENERAL>
-__device__ __forceinline__ void run_few_slice(const AttnArgs &a, uint16_t *lds) {
-  uint16_t *v = lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * FewShape<DP, FP8>::REGION;
+__device__ __forceinline__ void run_few_slice(const AttnArgs &a, uint16_t *v) {
   run_slice(a, [&](const AttnItem &it, int h) {
     if (run_few<DP, FP8, GENERAL, false>(a, it, h, v)) run_few<DP, FP8, GENERAL, true>(a, it, h, v);
   });
@@ -41,7 +40,7 @@ __device__ __forceinline__ void run_few_slice(const AttnArgs &a, uint16_t *lds) 
 template <int DP, bool FP8, bool GENERAL>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_kernel(AttnArgs a) {
   __shared__ __align__(16) uint16_t lds[4 * FewShape<DP, FP8>::REGION];
-  run_few_slice<DP, FP8, GENERAL>(a, lds);
+  run_few_slice<DP, FP8, GENERAL>(a, lds + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave) * FewShape<DP, FP8>::REGION);
 }
 
 template <int DP, bool GENERAL>
@@ -51,12 +50,15 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_few_f32_kernel(At
 
 template <int DP, bool FP8, bool GENERAL>
 __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_both_kernel(AttnArgs a) {
-  constexpr int kFewLds = 4 * FewShape<DP, FP8>::REGION, kTileLds = 2 * TileShape<DP, FP8>::BUF;
-  __shared__ __align__(16) uint16_t lds[kFewLds > kTileLds ? kFewLds : kTileLds];
-  __shared__ int flag_lds[4];
+  constexpr int kK = kKeys * TileShape<DP, FP8>::LDK, kV = kKeys * TileShape<DP, FP8>::LDV;
+  static_assert(FewShape<DP, FP8>::REGION <= kK && kK <= kV, "a few-row wave's V rows fit one of these");
+  __shared__ __align__(16) uint16_t k0[kK], k1[kK], v0[kV], v1[kV];
+  __shared__ int good_lds[kKeys], flag_lds[1];
+  const TileLds lds{k0, k1, v0, v1, good_lds, flag_lds};
   const int few_end = (few_blocks(a) + 7) / 8 * 8, index = (int)blockIdx.x - few_end;
   if (index < 0) {
-    run_few_slice<DP, FP8, GENERAL>(a, lds);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    run_few_slice<DP, FP8, GENERAL>(a, wave == 0 ? k0 : wave == 1 ? k1 : wave == 2 ? v0 : v1);
     return;
   }
   if (index >= a.tile_blocks) return;
@@ -66,7 +68,7 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_both_kernel(AttnA
   for (int i = first; i < items; i += step) {
     if (i != first) __syncthreads();
     const AttnItem it = load_item(a.tile_items, items - 1 - i);
-    if (run_tile<DP, FP8, GENERAL, false>(a, it, h, lds, flag_lds)) run_tile<DP, FP8, GENERAL, true>(a, it, h, lds, flag_lds);
+    if (run_tile<DP, FP8, GENERAL, false>(a, it, h, lds)) run_tile<DP, FP8, GENERAL, true>(a, it, h, lds);
   }
 }
 
