@@ -161,10 +161,14 @@ def _check(fn: str, st: int) -> None:
 
 
 def _stream(stream) -> C.c_void_p:
+    return C.c_void_p(_stream_handle(stream))
+
+
+def _stream_handle(stream) -> int:
     if stream is None:
         # the current stream's handle without building a Stream object (3 us)
-        return C.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
-    return C.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -516,6 +520,15 @@ class KvCache:
                                None if k_scale is None else _dev(k_scale, "k_scale"),
                                None if v_scale is None else _dev(v_scale, "v_scale"))
         self.ref = C.byref(self.c)
+        self._packed = {}
+
+    def packed_offsets(self, num_q_heads: int):
+        """Columns of q, k and v in a row that holds nothing else, and its width."""
+        if num_q_heads not in self._packed:
+            k = num_q_heads * self.head_dim
+            v = k + self.num_heads * self.head_dim
+            self._packed[num_q_heads] = (C.c_int64 * 3)(0, k, v), v + self.num_heads * self.head_dim
+        return self._packed[num_q_heads]
 
 
 class Rotation:
@@ -546,30 +559,35 @@ def lora_cache_append(qkv: torch.Tensor, cache: KvCache, slot: torch.Tensor, q_o
         raise ValueError("qkv must be [T][ldx] with unit column stride")
     if slot.dtype != torch.int64 or slot.dim() != 1 or not slot.is_contiguous() or slot.shape[0] != qkv.shape[0]:
         raise ValueError("slot must be a contiguous int64 vector, one entry per row")
-    T, D, kvh = qkv.shape[0], cache.head_dim, cache.num_heads
+    T, width = qkv.shape
+    D, kvh = cache.head_dim, cache.num_heads
     if num_q_heads is None:
-        num_q_heads = (q_out.shape[1] if q_out is not None else qkv.shape[1] - 2 * kvh * D) // D
-    offs = (C.c_int64 * 3)(*(offsets if offsets is not None
-                             else (0, num_q_heads * D, (num_q_heads + kvh) * D)))
-    if qkv.shape[1] < max(offs[0] + num_q_heads * D, offs[1] + kvh * D, offs[2] + kvh * D):
+        num_q_heads = (q_out.shape[1] if q_out is not None else width - 2 * kvh * D) // D
+    if offsets is None:
+        offs, need = cache.packed_offsets(num_q_heads)
+    else:
+        offs = (C.c_int64 * 3)(*offsets)
+        need = max(offs[0] + num_q_heads * D, offs[1] + kvh * D, offs[2] + kvh * D)
+    if width < need:
         raise ValueError("qkv has fewer columns than its heads need")
-    ldq = 0
+    q_ptr, ldq = None, 0
     if q_out is not None:
         if q_out.dim() != 2 or q_out.stride(1) != 1 or q_out.shape[0] != T or q_out.dtype != qkv.dtype:
             raise ValueError("q_out must be [T][ldq] of qkv's dtype with unit column stride")
         if q_out.shape[1] < num_q_heads * D:
             raise ValueError("q_out has fewer columns than its heads need")
-        ldq = q_out.stride(0) if T > 1 else q_out.shape[1]
+        q_ptr, ldq = _dev(q_out, "q_out") if T else None, q_out.stride(0) if T > 1 else q_out.shape[1]
+    rot = pos_ptr = None
     if rotation is not None:
         if pos is None or pos.dtype != torch.int32 or not pos.is_contiguous() or pos.numel() != rotation.num_axes * T:
             raise ValueError("pos must be contiguous int32 [axes][T]")
+        rot, pos_ptr = rotation.ref, _dev(pos, "pos") if T else None
     if num_bad is not None and num_bad.dtype != torch.int32:
         raise ValueError("num_bad must be int32")
     st = _lib.lora_cache_append(
-        _dev(qkv, "qkv") if T else None, qkv.stride(0) if T > 1 else qkv.shape[1], T, _dtype(qkv), num_q_heads, offs,
-        None if rotation is None else rotation.ref, _dev(pos, "pos") if rotation is not None and T else None,
-        _dev(slot, "slot") if T else None, cache.ref, _dev(q_out, "q_out") if q_out is not None and T else None, ldq,
-        None if num_bad is None else _dev(num_bad, "num_bad"), _stream(stream))
+        _dev(qkv, "qkv") if T else None, qkv.stride(0) if T > 1 else width, T, _dtype(qkv), num_q_heads, offs, rot,
+        pos_ptr, _dev(slot, "slot") if T else None, cache.ref, q_ptr, ldq,
+        None if num_bad is None else _dev(num_bad, "num_bad"), _stream_handle(stream))
     _check("lora_cache_append", st)
     return q_out
 
@@ -686,7 +704,7 @@ def lora_attention(meta: AttnMeta, q: torch.Tensor, cache: KvCache, out: torch.T
         meta.ref, _dev(q, "q"), q.stride(0) if c.num_tokens > 1 else width, cache.ref,
         c.head_dim ** -0.5 if scale is None else scale, cap, None if slopes is None else _dev(slopes, "slopes"),
         _dev(out, "out"), out.stride(0) if c.num_tokens > 1 else width, None if lse is None else _dev(lse, "lse"),
-        _dev(workspace, "workspace"), workspace.numel(), _stream(stream))
+        _dev(workspace, "workspace"), workspace.numel(), _stream_handle(stream))
     _check("lora_attention", st)
     return out if lse is None else (out, lse)
 
