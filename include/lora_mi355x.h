@@ -1,6 +1,9 @@
 /*
  * lora_mi355x.h -- C ABI of the multi-LoRA batched low-rank delta on MI355X
- * (gfx950): slot metadata, shrink, expand, and the fused apply.
+ * (gfx950): slot metadata, shrink, expand, and the fused apply; and of the
+ * attention that its q/k/v rows go on to: cache append, attention metadata,
+ * attention (the last part of this file, with conventions of its own where it
+ * says so).
  *
  * For a batch of T tokens, token t names an adapter slot token_slot[t] in
  * [0, S), or -1 for "no adapter".  The library adds, for every packed output
@@ -367,8 +370,8 @@ lora_status lora_apply_noalloc(const lora_meta *meta, const void *d_x, int64_t l
  *   dtype         LORA_BF16 or LORA_E4M3 (with bf16 queries), LORA_F32 (with
  *                 fp32 queries)
  *   k_scale, v_scale  device fp32 [num_heads] or NULL (= 1): with LORA_E4M3 a
- *                 stored value stands for value * scale[head]; must be NULL
- *                 for the other types
+ *                 stored value stands for value * scale[head], scales positive;
+ *                 must be NULL for the other types
  * Supported: head_dim a multiple of 8 (16 with LORA_E4M3), at most 256, page_size in [1, 65536],
  * num_pages in [1, 2^31 - 1], at most 1024 heads, strides whose byte size is a
  * multiple of 16.  Offsets are int64. */

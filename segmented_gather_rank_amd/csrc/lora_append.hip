@@ -6,6 +6,10 @@
 // once, and its row is cut into units of 8 pairs (two 16-byte pieces of bf16:
 // elements j and j + half of a head, or 16 neighbours when pairs are interleaved)
 // and 8 copied elements, one unit a thread and trip.
+//
+// Measured (32 + 2 x 8 heads of 128, bf16): 17705 tokens 83 us, 5.3 TB/s; 4608
+// tokens 20 us; one token 3.2 us.  With a thread per unit (512 threads, no second
+// trip) the long batch takes 118 us, with 128 threads 90.
 #include "lora_attn_dev.h"
 
 namespace lora {

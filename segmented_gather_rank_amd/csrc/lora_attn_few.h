@@ -18,6 +18,10 @@
 // registers, V through LDS that only its wave touches (for the transposition),
 // the next step's 16 loads of 16 bytes a lane are in flight while a step is
 // computed, and page ids are fetched two steps ahead.
+//
+// Measured (32 / 8 heads of 128): 256 decode sequences of 64 to 6000 keys, bf16
+// pages of 16, 535 us, 5.87 TB/s; 24 of 30 to 65 thousand keys, e4m3, capped, 364
+// us, 5.88 TB/s.  Twice as many waves read no faster (544 us).
 #pragma once
 
 #include "lora_attn_dev.h"

