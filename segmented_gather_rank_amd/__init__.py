@@ -700,6 +700,8 @@ def lora_attention(meta: AttnMeta, q: torch.Tensor, cache: KvCache, out: torch.T
         raise ValueError("lse must be contiguous float32 [T][heads]")
     if workspace is None:
         workspace = torch.empty(meta.attention_bytes, dtype=torch.uint8, device=q.device)
+        if isinstance(stream, torch.cuda.Stream):
+            workspace.record_stream(stream)   # freed here, in use there
     st = _lib.lora_attention(
         meta.ref, _dev(q, "q"), q.stride(0) if c.num_tokens > 1 else width, cache.ref,
         c.head_dim ** -0.5 if scale is None else scale, cap, None if slopes is None else _dev(slopes, "slopes"),

@@ -27,6 +27,10 @@ constexpr int kUnitRows = 16;
 // and cut into one slice per wave; a tile's keys are cut only where the tiles
 // alone would leave workgroups without work (256 CUs with two each).
 constexpr int kFewSlots = 1024;
+// Where a key is at most 128 bytes and nothing else is in the launch: twice as
+// many, since a wave then has less under way.
+constexpr int kFewSlotsSmall = 2048;
+constexpr int kSmallKeyBytes = 128;
 constexpr int kTileSlots = 512;
 // Shortest slice and shortest part of a tile, in keys: one step; four tiles.
 constexpr int kFewMinKeys = 32;
@@ -91,10 +95,10 @@ struct AttnCaps {
 // where they are few rows.  Every cut between two slices adds one piece; parts
 // of at most share_of keys number at most twice the slots in all tiles that are
 // cut.  With groups every tile may need partial results.
-LORA_HD AttnCaps attn_caps(int64_t tokens, int64_t seqs, int64_t groups, int heads, int group, int tile_rows) {
+LORA_HD AttnCaps attn_caps(int64_t tokens, int64_t seqs, int64_t groups, int heads, int group, int tile_rows, int few_slots) {
   const int64_t per = tile_rows / group;
   const int64_t own = seqs + tokens / per, shared = groups ? groups + tokens / per : 0;
-  const int64_t few = slots_per_head(heads, kFewSlots) + 1, big = slots_per_head(heads, kTileSlots) + 1;
+  const int64_t few = slots_per_head(heads, few_slots) + 1, big = slots_per_head(heads, kTileSlots) + 1;
   const bool wide = tile_rows > kFewRows;
   AttnCaps c;
   c.tiles = own + shared;

@@ -11,12 +11,17 @@
 // the slices alone take 287 and the tiles alone 96; 8 and 8 workgroups of the two
 // kinds in turn leave places empty where one kind has no work (a long prompt took
 // 3268 instead of 2630 us), tiles first take 454 us on the mixed batch.
+#include <algorithm>
+
 #include "lora_attn_few.h"
 #include "lora_attn_tile.h"
 
 namespace lora {
 
 namespace {
+
+// Rows up to which the waves of a workgroup share a row's parts in the join.
+constexpr int64_t kJoinShared = 1024;
 
 __host__ __device__ inline int few_blocks(const AttnArgs &a) { return (a.few_waves + 3) / 4; }
 
@@ -77,19 +82,22 @@ __global__ __launch_bounds__(256, DP <= 128 ? 2 : 1) void attn_both_kernel(AttnA
   }
 }
 
-// Rows whose result lies in parts: one wave per (token, query head) adds the
-// parts of its group's shared keys and of its own, weighted by their sums, in
-// the order of the keys.  Bound by latency (three dependent loads) for few rows
-// and by L2 for many: lane p looks up part p, and the first parts' outputs, 64 /
-// LANES side by side and 8 loads a lane, are on their way while the parts' maxima
-// are reduced.
-template <int LANES, typename OUT>
+// Rows whose result lies in parts: for each (token, query head) the parts of its
+// group's shared keys and of its own, weighted by their sums, are added in the
+// order of the keys.  Bound by latency (three dependent loads) for few rows and by
+// L2 for many: lane p looks up part p, and the first parts' outputs, 64 / LANES
+// side by side and 8 loads a lane, are on their way while the parts' maxima are
+// reduced.  WAVES = 1: a wave per row; 4: the workgroup's waves share a row's
+// parts, where rows are too few to fill the chip.
+template <int LANES, int WAVES, typename OUT>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   constexpr int SIDE = kWave / LANES;  // parts read side by side
   constexpr int DEEP = 8;              // loads in flight a lane
+  __shared__ float share[4][LANES * 4 + 2];
   const int lane = threadIdx.x % kWave, side = lane / LANES, d = 4 * (lane % LANES);
-  const uint32_t step = gridDim.x * 4;
-  uint32_t r = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + threadIdx.x / kWave);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const uint32_t step = gridDim.x * (4 / WAVES);
+  uint32_t r = WAVES == 1 ? blockIdx.x * 4 + wave : blockIdx.x;
   // the first row's record is read before it is known whether there is one
   auto entry = [&](uint32_t row) {
     const int64_t j = min((int64_t)a.by_q_heads.quotient(row), a.tokens - 1);
@@ -101,9 +109,11 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const uint32_t rows = (uint32_t)a.info[4] * a.q_heads;
   for (; r < rows; r += step) {
     const int qh = r - a.by_q_heads.quotient(r) * a.q_heads, h = a.by_group.quotient(qh), of_group = qh - h * a.group;
-    const int n = own.y + pre.y;
+    // this wave's parts: begin .. n - 1
+    const int all = own.y + pre.y, per = (all + WAVES - 1) / WAVES;
+    const int begin = WAVES == 1 ? 0 : min(wave * per, all), n = WAVES == 1 ? all : min(begin + per, all);
     float m = kNegInf, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int p0 = 0; p0 < n; p0 += kWave) {
+    for (int p0 = begin; p0 < n; p0 += kWave) {
       // lane p: where part p0 + p lies, its maximum and sum
       const int p = min(p0 + lane, n - 1), count = min(kWave, n - p0);
       const bool shared = p < pre.y;
@@ -152,10 +162,34 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
     for (int x = LANES; x < kWave; x *= 2)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], x);
+    if constexpr (WAVES > 1) {
+      __syncthreads();  // the last row's shares are read
+      if (side == 0) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) share[wave][d + i] = o[i];
+      }
+      if (lane == 0) share[wave][LANES * 4] = m, share[wave][LANES * 4 + 1] = l;
+      __syncthreads();
+      float top = kNegInf;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) top = fmaxf(top, share[w][LANES * 4]);
+      const float base = top == kNegInf ? 0.f : top;
+      m = top, l = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = 0.f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) {
+        const float f = exp2_fast(share[w][LANES * 4] - base);
+        l += f * share[w][LANES * 4 + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] += f == 0.f ? 0.f : f * share[w][d + i];
+      }
+    }
     const float mul = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = mul == 0.f ? 0.f : o[i] * mul;
-    if (side == 0 && d < a.dim) {
+    const bool writes = WAVES == 1 || wave == 0;
+    if (writes && side == 0 && d < a.dim) {
       const int64_t at = t * a.ldo + (int64_t)qh * a.dim + d;
       if constexpr (sizeof(OUT) == 4) {
         gstore16f(a.out + 4 * at, f32x4{o[0], o[1], o[2], o[3]});
@@ -164,7 +198,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
         *(g_u32x2 *)(a.out + 2 * at) = u32x2{pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3])};
       }
     }
-    if (lane == 0 && a.lse) a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
+    if (writes && lane == 0 && a.lse)
+      a.lse[(int64_t)t * a.q_heads + qh] = l == 0.f ? kNegInf : (m + __log2f(l)) * kLn2;
     if (r + step < rows) {
       e = entry(r + step);
       t = e[0].x, own = e[1], pre = e[2];
@@ -196,13 +231,18 @@ void start(const AttnArgs &a, AttnKind kind, hipStream_t s) {
   }
 }
 
+template <int WAVES, typename OUT>
+void start_join(const AttnArgs &a, unsigned grid, hipStream_t s) {
+  if (a.dim <= 64) attn_join_kernel<16, WAVES, OUT><<<dim3(grid), dim3(256), 0, s>>>(a);
+  else if (a.dim <= 128) attn_join_kernel<32, WAVES, OUT><<<dim3(grid), dim3(256), 0, s>>>(a);
+  else attn_join_kernel<64, WAVES, OUT><<<dim3(grid), dim3(256), 0, s>>>(a);
+}
 template <typename OUT>
 void start_join(const AttnArgs &a, hipStream_t s) {
-  const int64_t blocks = (a.tokens * a.q_heads + 3) / 4;
-  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048));
-  if (a.dim <= 64) attn_join_kernel<16, OUT><<<grid, dim3(256), 0, s>>>(a);
-  else if (a.dim <= 128) attn_join_kernel<32, OUT><<<grid, dim3(256), 0, s>>>(a);
-  else attn_join_kernel<64, OUT><<<grid, dim3(256), 0, s>>>(a);
+  // a row per workgroup where they fit the chip together
+  const int64_t rows = a.tokens * a.q_heads;
+  if (rows <= kJoinShared) start_join<4, OUT>(a, (unsigned)rows, s);
+  else start_join<1, OUT>(a, (unsigned)std::min<int64_t>((rows + 3) / 4, 2048), s);
 }
 
 }  // namespace

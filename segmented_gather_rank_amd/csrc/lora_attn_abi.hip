@@ -44,7 +44,8 @@ lora_status check_cache(const lora_kv_cache *c) {
 
 // Sizes that follow from the batch and the cache's geometry.
 struct AttnSizes {
-  int per_kv, group, heads, tile_rows;
+  int per_kv, group, heads, tile_rows, few_slots;
+  bool few_only;  // sequences of at most 16 rows and no groups: nothing for the tile kernel
   AttnCaps caps;
   size_t limits, info, tiles, few, slots, big, join, join_list, total;
 };
@@ -63,7 +64,10 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   s.group = heads_per_item(s.per_kv);
   s.heads = b->num_q_heads / s.group;
   s.tile_rows = c->dtype == LORA_F32 ? kFewRows : kTileQRows;
-  s.caps = attn_caps(b->num_tokens, b->num_seqs, b->num_groups, s.heads, s.group, s.tile_rows);
+  s.few_only = s.tile_rows == kFewRows || (!b->num_groups && (int64_t)b->max_q_len * s.group <= kFewRows);
+  const int64_t key_bytes = c->head_dim * (int64_t)cache_esize(c->dtype);
+  s.few_slots = s.few_only && key_bytes <= kSmallKeyBytes ? kFewSlotsSmall : kFewSlots;
+  s.caps = attn_caps(b->num_tokens, b->num_seqs, b->num_groups, s.heads, s.group, s.tile_rows, s.few_slots);
   // the lists' lengths are 32-bit
   if (std::max(s.caps.few_items, s.caps.tile_items) > 0x7fffffff || s.caps.units > 0x7fffffff)
     return LORA_ERR_UNSUPPORTED;
@@ -225,6 +229,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.heads = s.heads;
   a.group = s.group;
   a.tile_rows = s.tile_rows;
+  a.few_slots = s.few_slots;
   a.max_tiles = (int32_t)s.caps.tiles;
   a.max_few_items = (int32_t)s.caps.few_items;
   a.max_tile_items = (int32_t)s.caps.tile_items;
@@ -253,8 +258,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   out->head_groups = s.per_kv / s.group;
   out->max_tiles = a.max_tiles;
   out->max_slots = a.max_slots;
-  // sequences of at most 16 rows and no groups: nothing for the tile kernel
-  out->max_tile_items = !b->num_groups && (int64_t)b->max_q_len * s.group <= kFewRows ? 0 : a.max_tile_items;
+  out->max_tile_items = s.few_only ? 0 : a.max_tile_items;
   out->page_table = b->d_page_table;
   out->limits = a.limits;
   out->info = a.info;

@@ -309,6 +309,11 @@ __device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &i
   }
   const ScoreArgs sc = score_args<GENERAL>(a, kvh, qh);
 
+  auto page_of = [&](int step) -> int32_t {
+    const int key = it.key0 + step * 16 + c;
+    return key < it.key1 ? table[a.cache.page_size.quotient(key)] : -1;
+  };
+  int32_t page = page_of(0);
   float m = kNegInf, l = 0.f;
   f32x4 o[NC];
 #pragma unroll
@@ -316,8 +321,8 @@ __device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &i
   for (int step = 0; step < nsteps; ++step) {
     const int k0 = it.key0 + step * 16;
     const int key_c = k0 + c;
-    const int32_t page = key_c < it.key1 ? table[a.cache.page_size.quotient(key_c)] : -1;
     const int64_t off = key_offset(a.cache, key_c, page);
+    page = page_of(step + 1);
     const uint64_t good = __ballot(off >= 0);
     f32x4 kr[NC];
 #pragma unroll

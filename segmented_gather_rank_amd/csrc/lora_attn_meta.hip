@@ -218,7 +218,7 @@ __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a)
   }
   if (keys) atomicAdd(&sum_lds, keys);
   __syncthreads();
-  const int slice = share_of(line * kCutKeys, a.heads, kFewSlots, kFewMinKeys, kCutKeys);
+  const int slice = share_of(line * kCutKeys, a.heads, a.few_slots, kFewMinKeys, kCutKeys);
   const int share = share_of((int64_t)sum_lds, a.heads, kTileSlots, kTileMinKeys, kPartKeys);
   const int cuts = slice / kCutKeys;  // of a slice
   const int slots = (int)min((line + cuts - 1) / cuts, (long long)a.max_slots - 1);

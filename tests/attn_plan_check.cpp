@@ -87,7 +87,8 @@ static void capacities() {
       tokens += q[n];
     }
     const int groups = seqs && rnd() % 2 ? 1 + (int)upto(seqs < 5 ? 0 : 3) : 0;
-    const AttnCaps cap = attn_caps(tokens, seqs, groups, heads, group, rows);
+    const int few_slots = rnd() & 1 ? kFewSlots : kFewSlotsSmall;
+    const AttnCaps cap = attn_caps(tokens, seqs, groups, heads, group, rows, few_slots);
     struct Tile { int64_t ntok, len; bool few, parts; };
     std::vector<Tile> tiles;
     const int few = kFewRows / group, per = rows / group;
@@ -105,7 +106,7 @@ static void capacities() {
     // the few-row tiles' keys on one line, cut into slices; the others in parts
     int64_t line = 0, total = 0;
     for (auto &t : tiles) (t.few ? line : total) += t.few ? line_keys((int)t.len) : t.len;
-    const int slice = share_of(line, heads, kFewSlots, kFewMinKeys, kCutKeys), share = share_of(total, heads, kTileSlots, kTileMinKeys, kPartKeys);
+    const int slice = share_of(line, heads, few_slots, kFewMinKeys, kCutKeys), share = share_of(total, heads, kTileSlots, kTileMinKeys, kPartKeys);
     CHECK(slice % kCutKeys == 0 && (int64_t)slice * (cap.slots - 1) >= line);
     int64_t items[2] = {0, 0}, units = 0, at = 0;
     for (auto &t : tiles) {
