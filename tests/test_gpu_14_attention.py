@@ -194,6 +194,26 @@ def test_groups(L, case, cache, heads):
     check(b, o, lse, d_plain)
 
 
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_many_rows_to_join(L, cache):
+    """More rows in parts than the join gives a workgroup each (1024)."""
+    n = 150
+    b = R.Batch([1] * n, [70 + i % 40 for i in range(n)], 8, 2, 128, 16, cache, seed=4, groups=[0, 100, n],
+                group_len=[64, 70])
+    o, lse, meta, _ = run(L, b)
+    assert int(meta.tensors()["info"][4]) == n
+    check(b, o, lse, b.reference())
+
+
+def test_more_tiles_than_workgroups(L):
+    """Tile items that the workgroups take in rounds: over 4096 of them."""
+    n = 140
+    b = R.Batch([17] * n, [17 + i % 50 for i in range(n)], 32, 32, 16, 16, "bf16", seed=4)
+    o, lse, meta, _ = run(L, b)
+    assert int(meta.tensors()["info"][1]) * 32 > 4096
+    check(b, o, lse, b.reference())
+
+
 def test_groups_with_masks(L):
     q, kv = [1, 6, 1, 30, 1], [300, 306, 290, 330, 500]
     r = np.random.default_rng(1)
