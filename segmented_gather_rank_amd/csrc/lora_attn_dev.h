@@ -29,12 +29,13 @@ __device__ __forceinline__ int thread_of_item() {
 // Instruction kinds of __builtin_amdgcn_sched_group_barrier.
 constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 
-// max of three (a NaN among them is passed over), one instruction; fmaxf would
-// first quiet every operand that comes from a matrix product.
+// Maximum of three in one instruction; a NaN among them stays, so that no operand
+// has to be quieted first, as fmaxf would.  Where a score is NaN its row's weights
+// are too, whatever maximum they refer to.  The operands come from matrix products,
+// whose results may be read only some cycles later: the compiler sees to that for
+// operations it knows, not for an inline assembly statement.
 __device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
-  return r;
+  return __builtin_elementwise_maximum(__builtin_elementwise_maximum(a, b), c);
 }
 // Maximum and sum over the lanes l and l ^ 32, and over l, l ^ 16, l ^ 32, l ^ 48:
 // swapping a register's halves (rows of 16) with a copy of itself gives one

@@ -229,7 +229,7 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
     float top = max3(st[0][0], st[0][1], st[0][2]);
     top = max3(top, st[0][3], st[1][0]);
     top = max3(top, st[1][1], st[1][2]);
-    top = max_rows(fmaxf(top, st[1][3])) * mul;
+    top = max_rows(max3(top, top, st[1][3])) * mul;
     if (__any(!(top <= base + kSlack) && top > kNegInf)) {
       const float next = fmaxf(base, top);
       const float fade = next > kNegInf ? exp2_fast(base - next) : 1.f;
