@@ -117,6 +117,22 @@ LORA_HD AttnCaps attn_caps(int64_t tokens, int64_t seqs, int64_t groups, int hea
   return c;
 }
 
+// What follows from the heads, the cache's type and the longest sequence.
+struct AttnShape {
+  int group, heads;  // query heads of an item, items per tile and key range
+  int tile_rows, few_slots;
+  bool few_only;     // sequences of at most 16 rows and no groups: nothing for the tile kernel
+};
+LORA_HD AttnShape attn_shape(int q_heads, int kv_heads, int64_t key_bytes, bool f32, int groups, int max_q_len) {
+  AttnShape s;
+  s.group = heads_per_item(q_heads / kv_heads);
+  s.heads = q_heads / s.group;
+  s.tile_rows = f32 ? kFewRows : kTileQRows;
+  s.few_only = f32 || (!groups && (int64_t)max_q_len * s.group <= kFewRows);
+  s.few_slots = s.few_only && key_bytes <= kSmallKeyBytes ? kFewSlotsSmall : kFewSlots;
+  return s;
+}
+
 // One tile: rows [tok0 * group, (tok0 + ntok) * group) of every head group.
 struct AttnTile {
   int32_t tok0, ntok, seq;    // seq: row of the page table

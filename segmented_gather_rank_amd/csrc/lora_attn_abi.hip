@@ -44,8 +44,7 @@ lora_status check_cache(const lora_kv_cache *c) {
 
 // Sizes that follow from the batch and the cache's geometry.
 struct AttnSizes {
-  int per_kv, group, heads, tile_rows, few_slots;
-  bool few_only;  // sequences of at most 16 rows and no groups: nothing for the tile kernel
+  AttnShape shape;
   AttnCaps caps;
   size_t limits, info, tiles, few, slots, big, join, join_list, total;
 };
@@ -60,14 +59,9 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   if (b->num_tokens > (1 << 24) || b->num_seqs > (1 << 20) || b->num_groups > b->num_seqs ||
       b->num_q_heads > 1024 || b->num_tokens * b->num_q_heads > 0x7fffffff || b->page_table_stride > 0x7fff0000 / c->page_size)
     return LORA_ERR_UNSUPPORTED;
-  s.per_kv = b->num_q_heads / c->num_heads;
-  s.group = heads_per_item(s.per_kv);
-  s.heads = b->num_q_heads / s.group;
-  s.tile_rows = c->dtype == LORA_F32 ? kFewRows : kTileQRows;
-  s.few_only = s.tile_rows == kFewRows || (!b->num_groups && (int64_t)b->max_q_len * s.group <= kFewRows);
-  const int64_t key_bytes = c->head_dim * (int64_t)cache_esize(c->dtype);
-  s.few_slots = s.few_only && key_bytes <= kSmallKeyBytes ? kFewSlotsSmall : kFewSlots;
-  s.caps = attn_caps(b->num_tokens, b->num_seqs, b->num_groups, s.heads, s.group, s.tile_rows, s.few_slots);
+  s.shape = attn_shape(b->num_q_heads, c->num_heads, c->head_dim * (int64_t)cache_esize(c->dtype), c->dtype == LORA_F32,
+                       b->num_groups, b->max_q_len);
+  s.caps = attn_caps(b->num_tokens, b->num_seqs, b->num_groups, s.shape.heads, s.shape.group, s.shape.tile_rows, s.shape.few_slots);
   // the lists' lengths are 32-bit
   if (std::max(s.caps.few_items, s.caps.tile_items) > 0x7fffffff || s.caps.units > 0x7fffffff)
     return LORA_ERR_UNSUPPORTED;
@@ -226,10 +220,10 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.page_size = cache->page_size;
   a.causal = b->causal != 0;
   a.window = b->window;
-  a.heads = s.heads;
-  a.group = s.group;
-  a.tile_rows = s.tile_rows;
-  a.few_slots = s.few_slots;
+  a.heads = s.shape.heads;
+  a.group = s.shape.group;
+  a.tile_rows = s.shape.tile_rows;
+  a.few_slots = s.shape.few_slots;
   a.max_tiles = (int32_t)s.caps.tiles;
   a.max_few_items = (int32_t)s.caps.few_items;
   a.max_tile_items = (int32_t)s.caps.tile_items;
@@ -254,11 +248,11 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   out->head_dim = cache->head_dim;
   out->page_size = cache->page_size;
   out->dtype = cache->dtype;
-  out->heads_per_item = s.group;
-  out->head_groups = s.per_kv / s.group;
+  out->heads_per_item = a.group;
+  out->head_groups = a.heads / cache->num_heads;
   out->max_tiles = a.max_tiles;
   out->max_slots = a.max_slots;
-  out->max_tile_items = s.few_only ? 0 : a.max_tile_items;
+  out->max_tile_items = s.shape.few_only ? 0 : a.max_tile_items;
   out->page_table = b->d_page_table;
   out->limits = a.limits;
   out->info = a.info;

@@ -4,18 +4,10 @@
 
 #include <hip/hip_runtime.h>
 
-#include "lora_attn.h"
+#include "lora_attn_plan.h"
 
 namespace lora {
 
-struct AttnPlanArgs {
-  const int32_t *q_start, *kv_len, *prefix_len, *key_lo, *key_hi, *group_start, *group_len;
-  int64_t tokens, table_stride;
-  int32_t seqs, groups, max_q_len, page_size, causal, window;
-  int32_t heads, group, tile_rows, few_slots;
-  int32_t max_tiles, max_few_items, max_tile_items, max_units, max_slots;
-  int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_list, *seq_base, *group_base;
-};
 hipError_t launch_attn_plan(const AttnPlanArgs &a, hipStream_t s);
 
 struct AttnArgs {
