@@ -460,7 +460,9 @@ lora_status lora_cache_append(const void *d_qkv, int64_t ldx, int64_t num_tokens
  * 2^24, num_tokens * num_q_heads < 2^31, num_seqs <= 2^20, num_q_heads <= 1024, page_table_stride * page_size <=
  * 2^31 - 2^16.  A group is bad, and ignored,
  * if its bounds are not ascending in [0, num_seqs], its length is negative or
- * beyond the keys of its first sequence.  Keys in a page whose id lies outside
+ * beyond the keys of its first sequence; all groups are where any bound of
+ * q_start is out of order or leaves the batch.  The sequences of an ignored group
+ * read all their keys through their own tables.  Keys in a page whose id lies outside
  * [0, num_pages) are not seen.  Bad sequences and groups are counted in info. */
 typedef struct lora_attn_batch {
     const int32_t *d_q_start, *d_kv_len, *d_page_table;

@@ -40,6 +40,7 @@ static_assert(sizeof(AttnJoin) == 4 * kAttnJoinInts, "record size");
 struct TeamShared {
   unsigned long long keys;
   int bad_seqs, bad_groups;
+  int unordered;  // sequences whose bounds are out of order or leave the batch
 };
 
 LORA_HD int min_i(int a, int b) { return a < b ? a : b; }
@@ -47,28 +48,38 @@ LORA_HD int max_i(int a, int b) { return a > b ? a : b; }
 LORA_HD int64_t min_l(int64_t a, int64_t b) { return a < b ? a : b; }
 LORA_HD int64_t max_l(int64_t a, int64_t b) { return a > b ? a : b; }
 
+// Whether the query tokens of sequence n are an interval of the batch.
+LORA_HD bool seq_ordered(const AttnPlanArgs &a, int n) {
+  const int64_t q0 = a.q_start[n], q1 = a.q_start[n + 1];
+  return q0 >= 0 && q1 >= q0 && q1 <= a.tokens;
+}
+
 // Query tokens of sequence n as [q0, q1), empty if the bounds are not in order.
 LORA_HD void seq_tokens(const AttnPlanArgs &a, int n, int64_t &q0, int64_t &q1) {
   q0 = a.q_start[n];
   q1 = a.q_start[n + 1];
-  if (q0 < 0 || q1 < q0 || q1 > a.tokens) q0 = q1 = 0;
+  if (!seq_ordered(a, n)) q0 = q1 = 0;
 }
 
 // Whether sequence n is usable (see lora_attn_batch).
 LORA_HD bool seq_ok(const AttnPlanArgs &a, int n) {
   const int64_t q0 = a.q_start[n], q1 = a.q_start[n + 1], kv = a.kv_len[n];
-  return q0 >= 0 && q1 >= q0 && q1 <= a.tokens && q1 - q0 <= a.max_q_len && kv >= q1 - q0 &&
-         kv <= a.table_stride * a.page_size;
+  return seq_ordered(a, n) && q1 - q0 <= a.max_q_len && kv >= q1 - q0 && kv <= a.table_stride * a.page_size;
 }
 
-LORA_HD bool group_ok(const AttnPlanArgs &a, int g) {
+// Whether group g is served.  One rule for its members and for its tiles, since a
+// member's join reads what the group's tiles leave: its tokens are those between its
+// first sequence's bound and its last one's, which holds its members' only if all
+// bounds ascend.
+LORA_HD bool group_ok(const AttnPlanArgs &a, const TeamShared &common, int g) {
+  if (common.unordered) return false;
   const int s0 = a.group_start[g], s1 = a.group_start[g + 1], len = a.group_len[g];
   if (s0 < 0 || s1 < s0 || s1 > a.seqs || len < 0) return false;
   return s0 == s1 || (seq_ok(a, s0) && len <= a.kv_len[s0]);
 }
 
 // Group of sequence n, or -1: the last group that starts at or before n.
-LORA_HD int group_of(const AttnPlanArgs &a, int n) {
+LORA_HD int group_of(const AttnPlanArgs &a, const TeamShared &common, int n) {
   int lo = 0, hi = a.groups;  // first group that starts after n
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
@@ -76,7 +87,7 @@ LORA_HD int group_of(const AttnPlanArgs &a, int n) {
     else hi = mid;
   }
   const int g = lo - 1;
-  if (g < 0 || n >= a.group_start[g + 1] || !group_ok(a, g) || a.group_len[g] == 0) return -1;
+  if (g < 0 || n >= a.group_start[g + 1] || !group_ok(a, common, g) || a.group_len[g] == 0) return -1;
   return g;
 }
 
@@ -115,7 +126,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
   AttnTile *tile_list = reinterpret_cast<AttnTile *>(a.tiles);
   AttnParts *rec_list = reinterpret_cast<AttnParts *>(a.join);
   AttnJoin *join_list = reinterpret_cast<AttnJoin *>(a.join_list);
-  if (tid == 0) common = TeamShared{0, 0, 0};
+  if (tid == 0) common = TeamShared{0, 0, 0, 0};
   team.sync();
 
   // ---- tiles per sequence, then per group: which one, and which of its tiles
@@ -131,12 +142,12 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
         if (pass == 0) {
           seq_tokens(a, n, q0, q1);
           if (!seq_ok(a, n)) team.add(&common.bad_seqs, 1);
-        } else if (!group_ok(a, n)) {
+          if (!seq_ordered(a, n)) team.add(&common.unordered, 1);
+        } else if (!group_ok(a, common, n)) {
           team.add(&common.bad_groups, 1);
         } else if (a.group_len[n] > 0 && a.group_start[n] < a.group_start[n + 1]) {
           q0 = a.q_start[a.group_start[n]];
           q1 = a.q_start[a.group_start[n + 1]];
-          if (q0 < 0 || q1 < q0 || q1 > a.tokens) q0 = q1 = 0;
         }
         const int len = (int)(q1 - q0);
         count = len <= few_tokens ? (len > 0) : (len + tile_tokens - 1) / tile_tokens;
@@ -150,8 +161,8 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       tiles = min_i(tiles + total, a.max_tiles);
     }
     if (pass == 0) own = tiles;
+    team.sync();  // the counts; the list is written and read by this team alone
   }
-  team.sync();  // the list is written and read by this team alone
 
   // ---- the tiles' tokens and keys; few-row tiles take their place on the line
   long long line = 0;
@@ -169,7 +180,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       r.seq = n;
       if (i < own) {
         seq_tokens(a, n, q0, q1);
-        const int g = a.groups ? group_of(a, n) : -1;
+        const int g = a.groups ? group_of(a, common, n) : -1;
         if (g >= 0) {
           r.shared = 2;
           shared_len = a.group_len[g];

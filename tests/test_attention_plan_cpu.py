@@ -22,3 +22,10 @@ def plan_run(tmp_path_factory):
 def test_plan(plan_run, kind):
     r = subprocess.run([plan_run, kind, "3000"], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("kind", ["bad_ends", "bad_lengths"])
+def test_records_of_bad_batches(plan_run, kind):
+    """No join reads a record or a partial result that nobody wrote."""
+    r = subprocess.run([plan_run, kind, "3000", "records"], capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]

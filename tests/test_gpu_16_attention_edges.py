@@ -1,5 +1,6 @@
 """lora_cache_append and lora_attention where earlier tests do not reach: scores far
-apart on tiles without hidden keys.  Against the float64 form."""
+apart on tiles without hidden keys, groups in batches with bad bounds.  Against the
+float64 form."""
 import numpy as np
 import pytest
 import torch
@@ -35,3 +36,35 @@ def test_large_scores_of_full_tiles(L, D, cache, cap):
     # normal number, times a value
     out_tol = out_tol + max(b.kv_len) * np.finfo(np.float32).tiny * float(b.v_store.float().abs().max())
     check(b, o, lse, (out, rl, out_tol, lse_tol))
+
+
+def poisoned(L, b, d, **kw):
+    """Metadata and attention in memory full of garbage: out, lse, info."""
+    need = L.lora_attn_meta_workspace_bytes(*d.args, d.cache, b.hq, b.T, len(b.group_len or []))
+    meta = d.meta(L, workspace=torch.full((need,), 0x5a, dtype=torch.uint8, device="cuda"), **kw)
+    ws = torch.full((max(16, L.lora_attention_workspace_bytes(meta)),), 255, dtype=torch.uint8, device="cuda")
+    hold = torch.full((b.T + 2, b.hq, b.D), 9.0, dtype=d.q.dtype, device="cuda")
+    lse = torch.full((b.T, b.hq), 5.0, device="cuda")
+    L.lora_attention(meta, d.q, d.cache, hold[1:-1], lse=lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert torch.all(hold[0] == 9) and torch.all(hold[-1] == 9)
+    return hold[1:-1], lse, meta.tensors()["info"].cpu().tolist()
+
+
+def rows_of(b, seqs):
+    return [t for n in seqs for t in range(b.q_start[n], b.q_start[n + 1])]
+
+
+def check_rows(b, out, lse, ref, rows):
+    check(b, out[rows], lse[rows], tuple(r[rows] for r in ref))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("ends,good", [((0, 1, 2, 900), (0, 1)), ((0, 1, 2, -4), (0, 1))])
+def test_group_whose_last_sequence_leaves_the_batch(L, cache, ends, good):
+    b = R.Batch([1, 1, 1], [80, 90, 100], 8, 2, 64, 16, cache, seed=2, groups=[0, 3], group_len=[70])
+    d = Dev(L, b)
+    d.args = (dev(np.array(ends)), d.args[1], d.args[2])
+    out, lse, info = poisoned(L, b, d, max_q_len=3)
+    assert info[2] == 1 and info[3] == 1
+    check_rows(b, out, lse, b.reference(), rows_of(b, good))
