@@ -459,7 +459,8 @@ lora_status lora_cache_append(const void *d_qkv, int64_t ldx, int64_t num_tokens
  * page_table_stride pages; its tokens see no key.  Supported: num_tokens <=
  * 2^24, num_tokens * num_q_heads < 2^31, num_seqs <= 2^20, num_q_heads <= 1024, page_table_stride * page_size <=
  * 2^31 - 2^16.  A group is bad, and ignored,
- * if its bounds are not ascending in [0, num_seqs], its length is negative or
+ * if its bounds are not ascending in [0, num_seqs], if it begins before the end of
+ * an earlier good one, if its length is negative or
  * beyond the keys of its first sequence; all groups are where any bound of
  * q_start is out of order or leaves the batch.  The sequences of an ignored group
  * read all their keys through their own tables.  Keys in a page whose id lies outside

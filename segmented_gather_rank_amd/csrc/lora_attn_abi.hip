@@ -46,7 +46,7 @@ lora_status check_cache(const lora_kv_cache *c) {
 struct AttnSizes {
   AttnShape shape;
   AttnCaps caps;
-  size_t limits, info, tiles, few, slots, big, join, join_list, total;
+  size_t limits, info, tiles, few, slots, big, join, join_list, group_end, total;
 };
 
 lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSizes &s) {
@@ -79,6 +79,7 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   s.big = take(kAttnItemInts * s.caps.tile_items);
   s.join = take(8 * b->num_tokens);
   s.join_list = take(kAttnJoinInts * b->num_tokens);
+  s.group_end = take(b->num_groups);
   s.total = at;
   return LORA_OK;
 }
@@ -235,6 +236,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.tile_items = at(s.big);
   a.join = at(s.join);
   a.join_list = at(s.join_list);
+  a.group_end = at(s.group_end);
   a.slots = at(s.slots);
   a.max_slots = (int32_t)s.caps.slots;
 

@@ -55,6 +55,25 @@ struct BlockTeam {
     total = sum;
     return base + inc - v;
   }
+  __device__ int most_before(int v, int &total) const {
+    const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    int inc = v;
+    for (int x = 1; x < kWave; x *= 2) {
+      const int other = __shfl_up(inc, x);
+      if (lane >= x) inc = max(inc, other);
+    }
+    const int before_lane = __shfl_up(inc, 1);
+    __syncthreads();
+    if (lane == kWave - 1) lds[wave] = inc;
+    __syncthreads();
+    int base = 0, most = 0;
+    for (int w = 0; w < kPlanThreads / kWave; ++w) {
+      if (w == wave) base = most;
+      most = max(most, lds[w]);
+    }
+    total = most;
+    return lane > 0 ? max(base, before_lane) : base;
+  }
 };
 
 __global__ __launch_bounds__(kPlanThreads) void attn_plan_kernel(AttnPlanArgs a) {

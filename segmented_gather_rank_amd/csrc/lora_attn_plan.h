@@ -5,6 +5,7 @@
 //   id(), size()       this thread and how many there are; loops go in steps of size()
 //   sync()             what any thread wrote before, every thread reads after
 //   before(v, total)   sum of v over the threads before this one, and over all
+//   most_before(v, total)   likewise their maximum, of values from 0 on
 //   shared()           a TeamShared that the threads have in common
 //   add(p, v)          atomic add to it
 #pragma once
@@ -20,6 +21,7 @@ struct AttnPlanArgs {
   int32_t heads, group, tile_rows, few_slots;
   int32_t max_tiles, max_few_items, max_tile_items, max_units, max_slots;
   int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_list;
+  int32_t *group_end;  // see group_ok
 };
 
 // What a token sees: keys [lo, hi), its position, its sequence.
@@ -40,7 +42,8 @@ static_assert(sizeof(AttnJoin) == 4 * kAttnJoinInts, "record size");
 struct TeamShared {
   unsigned long long keys;
   int bad_seqs, bad_groups;
-  int unordered;  // sequences whose bounds are out of order or leave the batch
+  int unordered;         // sequences whose bounds are out of order or leave the batch
+  int unordered_groups;  // groups likewise
 };
 
 LORA_HD int min_i(int a, int b) { return a < b ? a : b; }
@@ -67,27 +70,41 @@ LORA_HD bool seq_ok(const AttnPlanArgs &a, int n) {
   return seq_ordered(a, n) && q1 - q0 <= a.max_q_len && kv >= q1 - q0 && kv <= a.table_stride * a.page_size;
 }
 
-// Whether group g is served.  One rule for its members and for its tiles, since a
-// member's join reads what the group's tiles leave: its tokens are those between its
-// first sequence's bound and its last one's, which holds its members' only if all
-// bounds ascend.
-LORA_HD bool group_ok(const AttnPlanArgs &a, const TeamShared &common, int g) {
-  if (common.unordered) return false;
-  const int s0 = a.group_start[g], s1 = a.group_start[g + 1], len = a.group_len[g];
-  if (s0 < 0 || s1 < s0 || s1 > a.seqs || len < 0) return false;
-  return s0 == s1 || (seq_ok(a, s0) && len <= a.kv_len[s0]);
+LORA_HD bool group_ordered(const AttnPlanArgs &a, int g) {
+  const int s0 = a.group_start[g], s1 = a.group_start[g + 1];
+  return s0 >= 0 && s1 >= s0 && s1 <= a.seqs;
 }
 
-// Group of sequence n, or -1: the last group that starts at or before n.
+// Whether group g would be served if it were the only one.  Its tokens are those
+// between its first sequence's bound and its last one's, which holds its members'
+// only if all bounds ascend.
+LORA_HD bool group_alone_ok(const AttnPlanArgs &a, const TeamShared &common, int g) {
+  if (common.unordered || !group_ordered(a, g) || a.group_len[g] < 0) return false;
+  const int s0 = a.group_start[g];
+  return s0 == a.group_start[g + 1] || (seq_ok(a, s0) && a.group_len[g] <= a.kv_len[s0]);
+}
+
+// Whether group g is served.  One rule for its members and for its tiles, since a
+// member's join reads what the group's tiles leave.  Where starts are out of order
+// (beside a bad group), group_end[g] is the furthest end of a group up to g, and a
+// group that starts before it shares sequences with an earlier one: it is bad.
+LORA_HD bool group_ok(const AttnPlanArgs &a, const TeamShared &common, int g) {
+  if (!group_alone_ok(a, common, g)) return false;
+  const int s0 = a.group_start[g];
+  return !common.unordered_groups || g == 0 || s0 == a.group_start[g + 1] || s0 >= a.group_end[g - 1];
+}
+
+// Group of sequence n, or -1: the last group that starts at or before n, or the first
+// whose furthest end lies past n.
 LORA_HD int group_of(const AttnPlanArgs &a, const TeamShared &common, int n) {
-  int lo = 0, hi = a.groups;  // first group that starts after n
+  int lo = 0, hi = a.groups;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (a.group_start[mid] <= n) lo = mid + 1;
+    if (common.unordered_groups ? a.group_end[mid] <= n : a.group_start[mid] <= n) lo = mid + 1;
     else hi = mid;
   }
-  const int g = lo - 1;
-  if (g < 0 || n >= a.group_start[g + 1] || !group_ok(a, common, g) || a.group_len[g] == 0) return -1;
+  const int g = common.unordered_groups ? lo : lo - 1;
+  if (g < 0 || g >= a.groups || n < a.group_start[g] || n >= a.group_start[g + 1] || a.group_len[g] == 0 || !group_ok(a, common, g)) return -1;
   return g;
 }
 
@@ -126,7 +143,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
   AttnTile *tile_list = reinterpret_cast<AttnTile *>(a.tiles);
   AttnParts *rec_list = reinterpret_cast<AttnParts *>(a.join);
   AttnJoin *join_list = reinterpret_cast<AttnJoin *>(a.join_list);
-  if (tid == 0) common = TeamShared{0, 0, 0, 0};
+  if (tid == 0) common = TeamShared{0, 0, 0, 0, 0};
   team.sync();
 
   // ---- tiles per sequence, then per group: which one, and which of its tiles
@@ -143,6 +160,8 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
           seq_tokens(a, n, q0, q1);
           if (!seq_ok(a, n)) team.add(&common.bad_seqs, 1);
           if (!seq_ordered(a, n)) team.add(&common.unordered, 1);
+          // (there are no more groups than sequences)
+          if (n < a.groups && !group_ordered(a, n)) team.add(&common.unordered_groups, 1);
         } else if (!group_ok(a, common, n)) {
           team.add(&common.bad_groups, 1);
         } else if (a.group_len[n] > 0 && a.group_start[n] < a.group_start[n + 1]) {
@@ -162,6 +181,18 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
     }
     if (pass == 0) own = tiles;
     team.sync();  // the counts; the list is written and read by this team alone
+    if (pass == 0 && common.unordered_groups) {
+      int end = 0;
+      for (int g0 = 0; g0 < a.groups; g0 += threads) {
+        const int g = g0 + tid;
+        const int mine = g < a.groups && group_alone_ok(a, common, g) && a.group_start[g] < a.group_start[g + 1] ? a.group_start[g + 1] : 0;
+        int most;
+        const int before = team.most_before(mine, most);
+        if (g < a.groups) a.group_end[g] = max_i(end, max_i(before, mine));
+        end = max_i(end, most);
+      }
+      team.sync();
+    }
   }
 
   // ---- the tiles' tokens and keys; few-row tiles take their place on the line

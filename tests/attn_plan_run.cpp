@@ -46,6 +46,11 @@ struct Solo {
     total = v;
     return 0;
   }
+  template <typename T>
+  T most_before(T v, T &total) const {
+    total = v;
+    return 0;
+  }
 };
 
 struct Batch {
@@ -121,7 +126,7 @@ static void follow(const Batch &b, bool records_only) {
   std::vector<int32_t> limits = ints(4 * b.tokens), info = ints(kAttnInfoInts), tiles = ints(kAttnTileInts * cap.tiles),
                        few = ints(kAttnItemInts * cap.few_items), slots = ints(kAttnSlotInts * cap.slots),
                        big = ints(kAttnItemInts * cap.tile_items), join = ints(8 * b.tokens),
-                       join_list = ints(kAttnJoinInts * b.tokens);
+                       join_list = ints(kAttnJoinInts * b.tokens), group_end = ints(b.groups());
   AttnPlanArgs a = {};
   auto in = [](const std::vector<int32_t> &v) { return v.empty() ? nullptr : v.data(); };
   a.q_start = in(b.q_start), a.kv_len = in(b.kv_len), a.prefix_len = in(b.prefix), a.key_lo = in(b.key_lo);
@@ -133,6 +138,7 @@ static void follow(const Batch &b, bool records_only) {
   a.max_units = (int)cap.units, a.max_slots = (int)cap.slots;
   a.limits = at(limits), a.info = info.data(), a.tiles = at(tiles), a.few_items = at(few), a.slots = at(slots);
   a.tile_items = at(big), a.join = at(join), a.join_list = at(join_list);
+  a.group_end = at(group_end);
   for (int64_t t = 0; t < b.tokens; ++t) reinterpret_cast<AttnLimit *>(a.limits)[t] = limit_of(a, t);
   Solo team;
   attn_plan(a, team);

@@ -68,3 +68,25 @@ def test_group_whose_last_sequence_leaves_the_batch(L, cache, ends, good):
     out, lse, info = poisoned(L, b, d, max_q_len=3)
     assert info[2] == 1 and info[3] == 1
     check_rows(b, out, lse, b.reference(), rows_of(b, good))
+
+
+def test_good_groups_beside_bad_ones(L):
+    """Bounds of groups out of order: the groups beside them are served, their keys
+    read once, over more groups than the plan has threads."""
+    n = 2100
+    starts = list(range(0, n + 1, 2))
+    b = R.Batch([1] * n, [40 + i % 30 for i in range(n)], 2, 1, 16, 16, "bf16", seed=7, groups=starts,
+                group_len=[16 + i % 20 for i in range(len(starts) - 1)])
+    ref = b.reference()
+    for spoiled in ([], [1], [0, 3, 70, 71, 300, 1049], list(range(10, 1045, 7))):
+        got = np.array(starts)
+        got[spoiled] = [10 ** 6 if i % 2 else -3 for i in range(len(spoiled))]
+        b.groups = got
+        d = Dev(L, b)
+        out, lse, info = poisoned(L, b, d)
+        bad = {g for s in spoiled for g in (s - 1, s) if 0 <= g < len(starts) - 1}
+        assert info[2] == 0 and info[3] == len(bad)
+        # every sequence of a good group is joined from the group's keys (others may be
+        # where their keys are cut)
+        assert info[4] >= n - 2 * len(bad)
+        check(b, out, lse, ref)
