@@ -665,13 +665,18 @@ def lora_prepare_attn_meta(q_start: torch.Tensor, kv_len: torch.Tensor, page_tab
 
 
 def lora_attn_meta_workspace_bytes(q_start, kv_len, page_table, cache: KvCache, num_q_heads: int, num_tokens: int,
-                                   num_groups: int = 0) -> int:
-    """Bytes of lora_prepare_attn_meta's workspace for a batch of these sizes."""
-    b = lora_attn_batch(page_table_stride=page_table.shape[1], num_tokens=num_tokens, num_seqs=kv_len.shape[0],
-                        max_q_len=num_tokens, num_q_heads=num_q_heads, num_groups=num_groups)
-    need = _sz(0)
-    _check("lora_attn_meta_workspace_bytes", _lib.lora_attn_meta_workspace_bytes(C.byref(b), cache.ref, C.byref(need)))
-    return int(need.value)
+                                   num_groups: int = 0, max_q_len: int | None = None) -> int:
+    """Bytes of lora_prepare_attn_meta's workspace for a batch of these sizes;
+    max_q_len as given there, or None: enough for any."""
+    most = 0
+    for q_len in (0, num_tokens) if max_q_len is None else (max_q_len,):
+        b = lora_attn_batch(page_table_stride=page_table.shape[1], num_tokens=num_tokens, num_seqs=kv_len.shape[0],
+                            max_q_len=q_len, num_q_heads=num_q_heads, num_groups=num_groups)
+        need = _sz(0)
+        _check("lora_attn_meta_workspace_bytes",
+               _lib.lora_attn_meta_workspace_bytes(C.byref(b), cache.ref, C.byref(need)))
+        most = max(most, int(need.value))
+    return most
 
 
 def lora_attention_workspace_bytes(meta: AttnMeta) -> int:
