@@ -57,13 +57,6 @@ LORA_HD bool seq_ordered(const AttnPlanArgs &a, int n) {
   return q0 >= 0 && q1 >= q0 && q1 <= a.tokens;
 }
 
-// Query tokens of sequence n as [q0, q1), empty if the bounds are not in order.
-LORA_HD void seq_tokens(const AttnPlanArgs &a, int n, int64_t &q0, int64_t &q1) {
-  q0 = a.q_start[n];
-  q1 = a.q_start[n + 1];
-  if (!seq_ordered(a, n)) q0 = q1 = 0;
-}
-
 // Whether sequence n is usable (see lora_attn_batch).
 LORA_HD bool seq_ok(const AttnPlanArgs &a, int n) {
   const int64_t q0 = a.q_start[n], q1 = a.q_start[n + 1], kv = a.kv_len[n];
@@ -157,8 +150,8 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       if (n < count_all) {
         int64_t q0 = 0, q1 = 0;
         if (pass == 0) {
-          seq_tokens(a, n, q0, q1);
-          if (!seq_ok(a, n)) team.add(&common.bad_seqs, 1);
+          if (seq_ok(a, n)) q0 = a.q_start[n], q1 = a.q_start[n + 1];
+          else team.add(&common.bad_seqs, 1);
           if (!seq_ordered(a, n)) team.add(&common.unordered, 1);
           // (there are no more groups than sequences)
           if (n < a.groups && !group_ordered(a, n)) team.add(&common.unordered_groups, 1);
@@ -210,7 +203,8 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       r.shared = 0;
       r.seq = n;
       if (i < own) {
-        seq_tokens(a, n, q0, q1);
+        q0 = a.q_start[n];
+        q1 = a.q_start[n + 1];
         const int g = a.groups ? group_of(a, common, n) : -1;
         if (g >= 0) {
           r.shared = 2;
@@ -336,6 +330,22 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
     tile_items += nt;
     units += nu;
     joins += nj;
+  }
+  // the tokens of bad sequences are in no tile: the join of no parts gives them their
+  // zeros
+  if (common.bad_seqs) {
+    team.sync();
+    for (int64_t t0 = 0; t0 < a.tokens; t0 += threads) {
+      const int64_t t = t0 + tid;
+      const bool bad = t < a.tokens && limits[t].seq >= 0 && !seq_ok(a, limits[t].seq);
+      int total;
+      const int at = joins + team.before((int)bad, total);
+      if (bad && at < a.tokens) {
+        rec_list[2 * t] = rec_list[2 * t + 1] = AttnParts{0, 0, 0, 0};
+        join_list[at].token = (int)t;
+      }
+      joins += total;
+    }
   }
   few_items = min_i(few_items, a.max_few_items);
   joins = (int)min_l(joins, a.tokens);

@@ -90,3 +90,36 @@ def test_good_groups_beside_bad_ones(L):
         # where their keys are cut)
         assert info[4] >= n - 2 * len(bad)
         check(b, out, lse, ref)
+
+
+@pytest.mark.parametrize("cache,hq,hkv", [("bf16", 8, 2), ("e4m3", 32, 8), ("f32", 8, 2), ("bf16", 6, 6)])
+@pytest.mark.parametrize("most", [1, 2, 5, 100])
+@pytest.mark.parametrize("grouped", [False, True])
+def test_rows_of_bad_sequences(L, cache, hq, hkv, most, grouped):
+    """More query tokens than stated, more keys than the table holds, fewer than
+    queries, a negative count: zeros and -inf for those tokens, the others as ever."""
+    q, kv = [1, 20, 1, 1, 2, 40, 1, 3], [50, 60, 70, 33, 45, 90, 1, 64]
+    groups = dict(groups=[2, 4, 8], group_len=[33, 1]) if grouped else {}
+    b = R.Batch(q, kv, hq, hkv, 64, 16, cache, seed=3, **groups)
+    d = Dev(L, b)
+    kv_dev = np.array(kv)
+    kv_dev[2], kv_dev[5], kv_dev[6] = 10 ** 6, 39, -1
+    d.args = (d.args[0], dev(kv_dev), d.args[2])
+    bad = tuple(n for n in range(len(q)) if n in (2, 5, 6) or q[n] > most)
+    out, lse, info = poisoned(L, b, d, max_q_len=most)
+    assert info[2] == len(bad)
+    check(b, out, lse, b.reference(bad_seqs=bad))
+
+
+@pytest.mark.parametrize("most", [1, 30])
+def test_rows_of_a_sequence_that_leaves_the_batch(L, most):
+    """Its tokens inside the batch get zeros, those of no sequence are not written."""
+    b = R.Batch([1, 1, 1, 25], [50, 60, 70, 40], 8, 2, 64, 16, "bf16", seed=3)
+    d = Dev(L, b)
+    for ends, bad, outside in (([0, 1, 2, 3, 900], [3], []), ([1, 2, 3, 3, 3], [], [0] + list(range(3, 28)))):
+        d.args = (dev(np.array(ends)), d.args[1], d.args[2])
+        out, lse, info = poisoned(L, b, d, max_q_len=most)
+        assert info[2] == len(bad)
+        if bad:
+            check(b, out, lse, b.reference(bad_seqs=(3,)))
+        assert torch.all(out[outside] == 9) and torch.all(lse[outside] == 5)
