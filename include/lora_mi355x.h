@@ -454,9 +454,11 @@ lora_status lora_cache_append(const void *d_qkv, int64_t ldx, int64_t num_tokens
  *                 the same for all of them.  They are read once for the whole
  *                 group, through the table of its first sequence.  num_groups
  *                 = 0: none.
- * A sequence is bad if its q_start leaves the bounds above, if it has more
+ * A sequence is bad if its q_start leaves the bounds above, if it begins before the
+ * end of an earlier good one, if it has more
  * query tokens than max_q_len or than keys, or if its keys do not fit
- * page_table_stride pages; its tokens see no key.  Supported: num_tokens <=
+ * page_table_stride pages; its tokens see no key.  Tokens that a good sequence holds
+ * too are that one's.  Supported: num_tokens <=
  * 2^24, num_tokens * num_q_heads < 2^31, num_seqs <= 2^20, num_q_heads <= 1024, page_table_stride * page_size <=
  * 2^31 - 2^16.  A group is bad, and ignored,
  * if its bounds are not ascending in [0, num_seqs], if it begins before the end of
@@ -482,7 +484,8 @@ typedef struct lora_attn_batch {
  * list of the attention kernels.  Filled by lora_prepare_attn_meta with
  * pointers into the caller's workspace; shared, like a lora_meta, by every
  * layer of the step with this mask and cache geometry, and only read by them.
- *   limits        int32 [num_tokens][4]: lo, hi, p, sequence of every token
+ *   limits        int32 [num_tokens][4]: lo, hi, p, sequence of every token (-1: in
+ *                 none; -2: q_start is out of order, and only bad ones hold it)
  *   info          int32 [16]: slices of the few-row work, items of the tile
  *                 work, bad sequences, bad groups, tokens to join,
  *                 partial-result units, keys per slice, most keys per item of

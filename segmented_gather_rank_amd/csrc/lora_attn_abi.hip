@@ -46,7 +46,7 @@ lora_status check_cache(const lora_kv_cache *c) {
 struct AttnSizes {
   AttnShape shape;
   AttnCaps caps;
-  size_t limits, info, tiles, few, slots, big, join, join_list, group_end, total;
+  size_t limits, info, tiles, few, slots, big, join, join_list, seq_end, group_end, total;
 };
 
 lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSizes &s) {
@@ -79,6 +79,7 @@ lora_status attn_sizes(const lora_attn_batch *b, const lora_kv_cache *c, AttnSiz
   s.big = take(kAttnItemInts * s.caps.tile_items);
   s.join = take(8 * b->num_tokens);
   s.join_list = take(kAttnJoinInts * b->num_tokens);
+  s.seq_end = take(b->num_seqs);
   s.group_end = take(b->num_groups);
   s.total = at;
   return LORA_OK;
@@ -225,10 +226,6 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.group = s.shape.group;
   a.tile_rows = s.shape.tile_rows;
   a.few_slots = s.shape.few_slots;
-  a.max_tiles = (int32_t)s.caps.tiles;
-  a.max_few_items = (int32_t)s.caps.few_items;
-  a.max_tile_items = (int32_t)s.caps.tile_items;
-  a.max_units = (int32_t)s.caps.units;
   a.limits = at(s.limits);
   a.info = at(s.info);
   a.tiles = at(s.tiles);
@@ -236,6 +233,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.tile_items = at(s.big);
   a.join = at(s.join);
   a.join_list = at(s.join_list);
+  a.seq_end = at(s.seq_end);
   a.group_end = at(s.group_end);
   a.slots = at(s.slots);
   a.max_slots = (int32_t)s.caps.slots;
@@ -252,9 +250,9 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   out->dtype = cache->dtype;
   out->heads_per_item = a.group;
   out->head_groups = a.heads / cache->num_heads;
-  out->max_tiles = a.max_tiles;
+  out->max_tiles = (int32_t)s.caps.tiles;
   out->max_slots = a.max_slots;
-  out->max_tile_items = s.shape.few_only ? 0 : a.max_tile_items;
+  out->max_tile_items = s.shape.few_only ? 0 : (int32_t)s.caps.tile_items;
   out->page_table = b->d_page_table;
   out->limits = a.limits;
   out->info = a.info;

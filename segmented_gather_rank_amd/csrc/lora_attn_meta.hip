@@ -39,6 +39,11 @@ struct BlockTeam {
   __device__ __forceinline__ int size() const { return kPlanThreads; }
   __device__ __forceinline__ void sync() const { __syncthreads(); }
   __device__ __forceinline__ TeamShared &shared() const { return *common; }
+  __device__ __forceinline__ bool any(bool x) const { return __syncthreads_or(x); }
+  // (atomics pass by the CU's cache, and so does this)
+  __device__ __forceinline__ int read(const int *p) const {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
   template <typename T>
   __device__ __forceinline__ void add(T *p, T v) const { atomicAdd(p, v); }
   __device__ int before(int v, int &total) const {

@@ -6,8 +6,10 @@
 //   sync()             what any thread wrote before, every thread reads after
 //   before(v, total)   sum of v over the threads before this one, and over all
 //   most_before(v, total)   likewise their maximum, of values from 0 on
+//   any(x)             whether x holds for any thread
 //   shared()           a TeamShared that the threads have in common
-//   add(p, v)          atomic add to it
+//   add(p, v)          atomic add, to it or to memory
+//   read(p)            what such adds to memory came to, after sync()
 #pragma once
 
 #include "lora_attn.h"
@@ -19,9 +21,9 @@ struct AttnPlanArgs {
   int64_t tokens, table_stride;
   int32_t seqs, groups, max_q_len, page_size, causal, window;
   int32_t heads, group, tile_rows, few_slots;
-  int32_t max_tiles, max_few_items, max_tile_items, max_units, max_slots;
+  int32_t max_slots;
   int32_t *limits, *info, *tiles, *few_items, *slots, *tile_items, *join, *join_list;
-  int32_t *group_end;  // see group_ok
+  int32_t *seq_end, *group_end;  // see seq_ok, group_ok
 };
 
 // What a token sees: keys [lo, hi), its position, its sequence.
@@ -42,8 +44,11 @@ static_assert(sizeof(AttnJoin) == 4 * kAttnJoinInts, "record size");
 struct TeamShared {
   unsigned long long keys;
   int bad_seqs, bad_groups;
-  int unordered;         // sequences whose bounds are out of order or leave the batch
-  int unordered_groups;  // groups likewise
+};
+
+// Whether bounds are out of order or leave their range anywhere, the same in all threads.
+struct AttnOrder {
+  bool seqs, groups;
 };
 
 LORA_HD int min_i(int a, int b) { return a < b ? a : b; }
@@ -57,10 +62,18 @@ LORA_HD bool seq_ordered(const AttnPlanArgs &a, int n) {
   return q0 >= 0 && q1 >= q0 && q1 <= a.tokens;
 }
 
-// Whether sequence n is usable (see lora_attn_batch).
-LORA_HD bool seq_ok(const AttnPlanArgs &a, int n) {
+// Whether sequence n would be usable if it were the only one (see lora_attn_batch).
+LORA_HD bool seq_alone_ok(const AttnPlanArgs &a, int n) {
   const int64_t q0 = a.q_start[n], q1 = a.q_start[n + 1], kv = a.kv_len[n];
   return seq_ordered(a, n) && q1 - q0 <= a.max_q_len && kv >= q1 - q0 && kv <= a.table_stride * a.page_size;
+}
+
+// Whether sequence n is usable.  Where bounds are out of order, seq_end[n] is the
+// furthest end of a sequence up to n, and one that starts before it shares tokens with
+// an earlier one: it is bad, so that no token has two sequences.
+LORA_HD bool seq_ok(const AttnPlanArgs &a, AttnOrder broken, int n) {
+  if (!seq_alone_ok(a, n)) return false;
+  return !broken.seqs || n == 0 || a.q_start[n] == a.q_start[n + 1] || a.q_start[n] >= a.seq_end[n - 1];
 }
 
 LORA_HD bool group_ordered(const AttnPlanArgs &a, int g) {
@@ -71,37 +84,53 @@ LORA_HD bool group_ordered(const AttnPlanArgs &a, int g) {
 // Whether group g would be served if it were the only one.  Its tokens are those
 // between its first sequence's bound and its last one's, which holds its members'
 // only if all bounds ascend.
-LORA_HD bool group_alone_ok(const AttnPlanArgs &a, const TeamShared &common, int g) {
-  if (common.unordered || !group_ordered(a, g) || a.group_len[g] < 0) return false;
+LORA_HD bool group_alone_ok(const AttnPlanArgs &a, AttnOrder broken, int g) {
+  if (broken.seqs || !group_ordered(a, g) || a.group_len[g] < 0) return false;
   const int s0 = a.group_start[g];
-  return s0 == a.group_start[g + 1] || (seq_ok(a, s0) && a.group_len[g] <= a.kv_len[s0]);
+  return s0 == a.group_start[g + 1] || (seq_alone_ok(a, s0) && a.group_len[g] <= a.kv_len[s0]);
 }
 
 // Whether group g is served.  One rule for its members and for its tiles, since a
 // member's join reads what the group's tiles leave.  Where starts are out of order
 // (beside a bad group), group_end[g] is the furthest end of a group up to g, and a
 // group that starts before it shares sequences with an earlier one: it is bad.
-LORA_HD bool group_ok(const AttnPlanArgs &a, const TeamShared &common, int g) {
-  if (!group_alone_ok(a, common, g)) return false;
+LORA_HD bool group_ok(const AttnPlanArgs &a, AttnOrder broken, int g) {
+  if (!group_alone_ok(a, broken, g)) return false;
   const int s0 = a.group_start[g];
-  return !common.unordered_groups || g == 0 || s0 == a.group_start[g + 1] || s0 >= a.group_end[g - 1];
+  return !broken.groups || g == 0 || s0 == a.group_start[g + 1] || s0 >= a.group_end[g - 1];
 }
 
 // Group of sequence n, or -1: the last group that starts at or before n, or the first
 // whose furthest end lies past n.
-LORA_HD int group_of(const AttnPlanArgs &a, const TeamShared &common, int n) {
+LORA_HD int group_of(const AttnPlanArgs &a, AttnOrder broken, int n) {
   int lo = 0, hi = a.groups;
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (common.unordered_groups ? a.group_end[mid] <= n : a.group_start[mid] <= n) lo = mid + 1;
+    if (broken.groups ? a.group_end[mid] <= n : a.group_start[mid] <= n) lo = mid + 1;
     else hi = mid;
   }
-  const int g = common.unordered_groups ? lo : lo - 1;
-  if (g < 0 || g >= a.groups || n < a.group_start[g] || n >= a.group_start[g + 1] || a.group_len[g] == 0 || !group_ok(a, common, g)) return -1;
+  const int g = broken.groups ? lo : lo - 1;
+  if (g < 0 || g >= a.groups || n < a.group_start[g] || n >= a.group_start[g + 1] || a.group_len[g] == 0 ||
+      !group_ok(a, broken, g))
+    return -1;
   return g;
 }
 
-// What token t sees.
+// What token t of the usable sequence n sees.
+LORA_HD AttnLimit limit_in(const AttnPlanArgs &a, int n, int64_t t) {
+  const int kv = a.kv_len[n];
+  AttnLimit r{0, 0, (int)(kv - a.q_start[n + 1] + t), n};
+  r.hi = a.causal ? r.pos + 1 : kv;
+  if (a.prefix_len) r.hi = max_i(r.hi, a.prefix_len[n]);
+  if (a.window > 0) r.lo = max_i(0, r.pos + 1 - a.window);
+  if (a.key_lo) r.lo = max_i(r.lo, a.key_lo[t]);
+  if (a.key_hi) r.hi = min_i(r.hi, a.key_hi[t]);
+  r.hi = min_i(r.hi, kv);
+  if (r.hi <= r.lo) r.lo = r.hi = 0;
+  return r;
+}
+
+// What token t sees, for bounds in order.
 LORA_HD AttnLimit limit_of(const AttnPlanArgs &a, int64_t t) {
   int lo = 0, hi = a.seqs;  // first sequence whose tokens start after t
   while (lo < hi) {
@@ -110,24 +139,64 @@ LORA_HD AttnLimit limit_of(const AttnPlanArgs &a, int64_t t) {
     else hi = mid;
   }
   const int n = lo - 1;
-  AttnLimit r{0, 0, 0, -1};
-  if (n >= 0 && t < a.q_start[n + 1]) {
-    r.seq = n;
-    if (seq_ok(a, n)) {
-      const int kv = a.kv_len[n];
-      r.pos = (int)(kv - a.q_start[n + 1] + t);
-      r.hi = a.causal ? r.pos + 1 : kv;
-      if (a.prefix_len) r.hi = max_i(r.hi, a.prefix_len[n]);
-      if (a.window > 0) r.lo = max_i(0, r.pos + 1 - a.window);
-      if (a.key_lo) r.lo = max_i(r.lo, a.key_lo[t]);
-      if (a.key_hi) r.hi = min_i(r.hi, a.key_hi[t]);
-      r.hi = min_i(r.hi, kv);
-      if (r.hi <= r.lo) r.lo = r.hi = 0;
-    }
-  }
-  return r;
+  if (n < 0 || t >= a.q_start[n + 1]) return AttnLimit{0, 0, 0, -1};
+  return seq_alone_ok(a, n) ? limit_in(a, n, t) : AttnLimit{0, 0, 0, n};
 }
 
+// Furthest ends up to each of `count` intervals, end(i) being interval i's (0: none).
+template <typename Team, typename F>
+LORA_HD void furthest_ends(Team &team, int count, int32_t *out, F &&end) {
+  int far = 0;
+  for (int i0 = 0; i0 < count; i0 += team.size()) {
+    const int i = i0 + team.id(), mine = i < count ? end(i) : 0;
+    int most;
+    const int before = team.most_before(mine, most);
+    if (i < count) out[i] = max_i(far, max_i(before, mine));
+    far = max_i(far, most);
+  }
+  team.sync();
+}
+
+// Bounds out of order: every token's sequence again, over the furthest ends, which
+// ascend (the first that lies past a token is the one sequence that may hold it).  A
+// token that only bad sequences hold, by the number of those that begin at or before
+// it less that of those that end, gets -2.
+template <typename Team>
+LORA_HD void limits_out_of_order(const AttnPlanArgs &a, AttnOrder broken, Team &team) {
+  AttnLimit *limits = reinterpret_cast<AttnLimit *>(a.limits);
+  furthest_ends(team, a.seqs, a.seq_end,
+                [&](int n) { return seq_alone_ok(a, n) && a.q_start[n] < a.q_start[n + 1] ? a.q_start[n + 1] : 0; });
+  for (int64_t t = team.id(); t < a.tokens; t += team.size()) limits[t] = AttnLimit{0, 0, 0, -1};
+  team.sync();
+  for (int n = team.id(); n < a.seqs; n += team.size()) {
+    const int64_t q0 = max_l(a.q_start[n], 0), q1 = min_l(a.q_start[n + 1], a.tokens);
+    if (q0 >= q1 || seq_ok(a, broken, n)) continue;
+    team.add(&limits[q0].pos, 1);
+    if (q1 < a.tokens) team.add(&limits[q1].pos, -1);
+  }
+  team.sync();
+  int bad = 0;
+  for (int64_t t0 = 0; t0 < a.tokens; t0 += team.size()) {
+    const int64_t t = t0 + team.id();
+    const int step = t < a.tokens ? team.read(&limits[t].pos) : 0;
+    int total;
+    const int before = bad + team.before(step, total);
+    bad += total;
+    if (t >= a.tokens) continue;
+    int lo = 0, hi = a.seqs;
+    while (lo < hi) {
+      const int mid = (lo + hi) / 2;
+      if (a.seq_end[mid] <= t) lo = mid + 1;
+      else hi = mid;
+    }
+    if (lo < a.seqs && a.q_start[lo] <= t && t < a.q_start[lo + 1] && seq_ok(a, broken, lo)) limits[t] = limit_in(a, lo, t);
+    else limits[t] = AttnLimit{0, 0, 0, before + step > 0 ? -2 : -1};
+  }
+  team.sync();
+}
+
+// The work lists.  Every token is in one sequence's tiles and in those of at most one
+// group, so the lists fit the capacities of attn_caps whatever the arrays hold.
 template <typename Team>
 LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
   TeamShared &common = team.shared();
@@ -136,57 +205,65 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
   AttnTile *tile_list = reinterpret_cast<AttnTile *>(a.tiles);
   AttnParts *rec_list = reinterpret_cast<AttnParts *>(a.join);
   AttnJoin *join_list = reinterpret_cast<AttnJoin *>(a.join_list);
-  if (tid == 0) common = TeamShared{0, 0, 0, 0, 0};
+  if (tid == 0) common = TeamShared{0, 0, 0};
   team.sync();
 
   // ---- tiles per sequence, then per group: which one, and which of its tiles
   const int few_tokens = kFewRows / a.group, tile_tokens = a.tile_rows / a.group;
-  int own = 0, tiles = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    const int count_all = pass ? a.groups : a.seqs;
-    for (int n0 = 0; n0 < count_all; n0 += threads) {
+  int tiles = 0;
+  auto list_tiles = [&](int n, int len) {  // of this thread's sequence or group n
+    const int count = len <= few_tokens ? (len > 0) : (len + tile_tokens - 1) / tile_tokens;
+    int total;
+    const int before = tiles + team.before(count, total);
+    for (int i = 0; i < count; ++i) {
+      tile_list[before + i].seq = n;
+      tile_list[before + i].part = i;
+    }
+    tiles += total;
+  };
+  AttnOrder broken{false, false};
+  auto list_sequences = [&]() {
+    for (int n0 = 0; n0 < a.seqs; n0 += threads) {
       const int n = n0 + tid;
-      int count = 0;
-      if (n < count_all) {
-        int64_t q0 = 0, q1 = 0;
-        if (pass == 0) {
-          if (seq_ok(a, n)) q0 = a.q_start[n], q1 = a.q_start[n + 1];
-          else team.add(&common.bad_seqs, 1);
-          if (!seq_ordered(a, n)) team.add(&common.unordered, 1);
-          // (there are no more groups than sequences)
-          if (n < a.groups && !group_ordered(a, n)) team.add(&common.unordered_groups, 1);
-        } else if (!group_ok(a, common, n)) {
-          team.add(&common.bad_groups, 1);
-        } else if (a.group_len[n] > 0 && a.group_start[n] < a.group_start[n + 1]) {
-          q0 = a.q_start[a.group_start[n]];
-          q1 = a.q_start[a.group_start[n + 1]];
-        }
-        const int len = (int)(q1 - q0);
-        count = len <= few_tokens ? (len > 0) : (len + tile_tokens - 1) / tile_tokens;
+      if (!broken.seqs) {
+        // (there are no more groups than sequences)
+        const bool here = n < a.seqs && !seq_ordered(a, n), group = n < a.groups && !group_ordered(a, n);
+        broken.groups |= team.any(group);
+        if (team.any(here)) return false;
       }
-      int total;
-      const int before = tiles + team.before(count, total);
-      for (int i = 0; i < count && before + i < a.max_tiles; ++i) {
-        tile_list[before + i].seq = n;
-        tile_list[before + i].part = i;
+      int len = 0;
+      if (n < a.seqs) {
+        if (seq_ok(a, broken, n)) len = a.q_start[n + 1] - a.q_start[n];
+        else team.add(&common.bad_seqs, 1);
       }
-      tiles = min_i(tiles + total, a.max_tiles);
+      list_tiles(n, len);
     }
-    if (pass == 0) own = tiles;
-    team.sync();  // the counts; the list is written and read by this team alone
-    if (pass == 0 && common.unordered_groups) {
-      int end = 0;
-      for (int g0 = 0; g0 < a.groups; g0 += threads) {
-        const int g = g0 + tid;
-        const int mine = g < a.groups && group_alone_ok(a, common, g) && a.group_start[g] < a.group_start[g + 1] ? a.group_start[g + 1] : 0;
-        int most;
-        const int before = team.most_before(mine, most);
-        if (g < a.groups) a.group_end[g] = max_i(end, max_i(before, mine));
-        end = max_i(end, most);
-      }
-      team.sync();
-    }
+    return true;
+  };
+  if (!list_sequences()) {  // bounds out of order: once more
+    broken.seqs = true;
+    limits_out_of_order(a, broken, team);
+    if (tid == 0) common.bad_seqs = 0;
+    team.sync();
+    tiles = 0;
+    list_sequences();
   }
+  const int own = tiles;
+  if (broken.groups)
+    furthest_ends(team, a.groups, a.group_end, [&](int g) {
+      return group_alone_ok(a, broken, g) && a.group_start[g] < a.group_start[g + 1] ? a.group_start[g + 1] : 0;
+    });
+  for (int g0 = 0; g0 < a.groups; g0 += threads) {
+    const int g = g0 + tid;
+    int len = 0;
+    if (g < a.groups) {
+      if (!group_ok(a, broken, g)) team.add(&common.bad_groups, 1);
+      else if (a.group_len[g] > 0 && a.group_start[g] < a.group_start[g + 1])
+        len = a.q_start[a.group_start[g + 1]] - a.q_start[a.group_start[g]];
+    }
+    list_tiles(g, len);
+  }
+  team.sync();  // the counts; the list is written and read by this team alone
 
   // ---- the tiles' tokens and keys; few-row tiles take their place on the line
   long long line = 0;
@@ -205,7 +282,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       if (i < own) {
         q0 = a.q_start[n];
         q1 = a.q_start[n + 1];
-        const int g = a.groups ? group_of(a, common, n) : -1;
+        const int g = a.groups ? group_of(a, broken, n) : -1;
         if (g >= 0) {
           r.shared = 2;
           shared_len = a.group_len[g];
@@ -291,14 +368,9 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
     const int unit = units + team.before(join ? parts * ups : 0, nu);
     const int at_join = joins + team.before(join && r.shared != 1 ? r.ntok : 0, nj);
     if (i < tiles) {
-      // true for every batch in order, by the capacities' derivation; with a
-      // q_start out of order the surplus is dropped
-      const bool fits = (few ? at_few + parts <= a.max_few_items : at_tile + parts <= a.max_tile_items) &&
-                        unit + parts * ups <= a.max_units;
-      AttnItem item{r.tok0, fits ? r.ntok : 0, r.seq, r.key0, r.key1, r.full0, r.full1, -1};
+      AttnItem item{r.tok0, r.ntok, r.seq, r.key0, r.key1, r.full0, r.full1, -1};
       for (int s = 0; s < parts; ++s) {
         const int at = (few ? at_few : at_tile) + s;
-        if (at >= (few ? a.max_few_items : a.max_tile_items)) break;
         if (join) item.unit = unit + s * ups;
         if (few) {
           // the piece of the tile on slice k: the line from `from` on
@@ -320,9 +392,9 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       if (join) {
         for (int t = 0; t < r.ntok; ++t) {
           AttnParts *rec = rec_list + 2 * (int64_t)(r.tok0 + t);
-          rec[r.shared == 1] = AttnParts{unit, fits ? parts : 0, ups, t};
+          rec[r.shared == 1] = AttnParts{unit, parts, ups, t};
           if (r.shared == 0) rec[1] = AttnParts{0, 0, 0, 0};
-          if (r.shared != 1 && at_join + t < a.tokens) join_list[at_join + t].token = r.tok0 + t;
+          if (r.shared != 1) join_list[at_join + t].token = r.tok0 + t;
         }
       }
     }
@@ -337,26 +409,25 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
     team.sync();
     for (int64_t t0 = 0; t0 < a.tokens; t0 += threads) {
       const int64_t t = t0 + tid;
-      const bool bad = t < a.tokens && limits[t].seq >= 0 && !seq_ok(a, limits[t].seq);
+      const int seq = t < a.tokens ? limits[t].seq : -1;
+      const bool bad = seq == -2 || (seq >= 0 && !seq_ok(a, broken, seq));
       int total;
       const int at = joins + team.before((int)bad, total);
-      if (bad && at < a.tokens) {
+      if (bad) {
         rec_list[2 * t] = rec_list[2 * t + 1] = AttnParts{0, 0, 0, 0};
         join_list[at].token = (int)t;
       }
       joins += total;
     }
   }
-  few_items = min_i(few_items, a.max_few_items);
-  joins = (int)min_l(joins, a.tokens);
   if (tid == 0) {
     if (slots > 0) slot_list[slots - 1].end = few_items;
     a.info[0] = slots;
-    a.info[1] = min_i(tile_items, a.max_tile_items);
+    a.info[1] = tile_items;
     a.info[2] = common.bad_seqs;
     a.info[3] = common.bad_groups;
     a.info[4] = joins;
-    a.info[5] = min_i(units, a.max_units);
+    a.info[5] = units;
     a.info[6] = slice;
     a.info[7] = share;
     a.info[8] = few_items;

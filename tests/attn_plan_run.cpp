@@ -39,6 +39,8 @@ struct Solo {
   int size() const { return 1; }
   void sync() const {}
   TeamShared &shared() { return common; }
+  bool any(bool x) const { return x; }
+  int read(const int *p) const { return *p; }
   template <typename T, typename V>
   void add(T *p, V v) const { *p += v; }
   template <typename T>
@@ -126,7 +128,7 @@ static void follow(const Batch &b, bool records_only) {
   std::vector<int32_t> limits = ints(4 * b.tokens), info = ints(kAttnInfoInts), tiles = ints(kAttnTileInts * cap.tiles),
                        few = ints(kAttnItemInts * cap.few_items), slots = ints(kAttnSlotInts * cap.slots),
                        big = ints(kAttnItemInts * cap.tile_items), join = ints(8 * b.tokens),
-                       join_list = ints(kAttnJoinInts * b.tokens), group_end = ints(b.groups());
+                       join_list = ints(kAttnJoinInts * b.tokens), seq_end = ints(b.seqs()), group_end = ints(b.groups());
   AttnPlanArgs a = {};
   auto in = [](const std::vector<int32_t> &v) { return v.empty() ? nullptr : v.data(); };
   a.q_start = in(b.q_start), a.kv_len = in(b.kv_len), a.prefix_len = in(b.prefix), a.key_lo = in(b.key_lo);
@@ -134,11 +136,10 @@ static void follow(const Batch &b, bool records_only) {
   a.tokens = b.tokens, a.table_stride = b.stride, a.seqs = b.seqs(), a.groups = b.groups(), a.max_q_len = b.max_q_len;
   a.page_size = b.page, a.causal = b.causal, a.window = b.window;
   a.heads = sh.heads, a.group = sh.group, a.tile_rows = sh.tile_rows, a.few_slots = sh.few_slots;
-  a.max_tiles = (int)cap.tiles, a.max_few_items = (int)cap.few_items, a.max_tile_items = (int)cap.tile_items;
-  a.max_units = (int)cap.units, a.max_slots = (int)cap.slots;
+  a.max_slots = (int)cap.slots;
   a.limits = at(limits), a.info = info.data(), a.tiles = at(tiles), a.few_items = at(few), a.slots = at(slots);
   a.tile_items = at(big), a.join = at(join), a.join_list = at(join_list);
-  a.group_end = at(group_end);
+  a.seq_end = at(seq_end), a.group_end = at(group_end);
   for (int64_t t = 0; t < b.tokens; ++t) reinterpret_cast<AttnLimit *>(a.limits)[t] = limit_of(a, t);
   Solo team;
   attn_plan(a, team);

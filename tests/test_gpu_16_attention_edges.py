@@ -123,3 +123,65 @@ def test_rows_of_a_sequence_that_leaves_the_batch(L, most):
         if bad:
             check(b, out, lse, b.reference(bad_seqs=(3,)))
         assert torch.all(out[outside] == 9) and torch.all(lse[outside] == 5)
+
+
+def owners(starts, kv, most, T):
+    """The header's rules: which sequences are good, and of every token its sequence,
+    -1 if it is in none, -2 if in bad ones only."""
+    good, owner, end = [], [-1] * T, 0
+    for n, (s, e) in enumerate(zip(starts, starts[1:])):
+        ok = 0 <= s <= e <= T and e - s <= most and e - s <= kv[n]
+        good.append(ok and (s == e or s >= end))
+        end = max(end, e) if ok else end
+        for t in range(max(s, 0), min(e, T)):
+            owner[t] = n if good[-1] else (-2 if owner[t] == -1 else owner[t])
+    return good, owner
+
+
+STARTS = [[0, 2, 1, 6, 8], [-5, 2, 4, 6, 8], [0, 2, 4, 6, 900], [0, 900, 4, 6, 8], [8, 8, 8, 8, 8], [3, 2, 1, 0, -1],
+          [0, 5, 3, 8, 8], [4, 8, 0, 4, 2], [0, 8, 1, 3, 7], [6, 8, 8, 0, 6], [2, 4, 3, 5, -2 ** 31]]
+
+
+@pytest.mark.parametrize("cache", ["bf16", "f32", "e4m3"])
+@pytest.mark.parametrize("starts", STARTS, ids=str)
+@pytest.mark.parametrize("most", [1, 2, 8])
+@pytest.mark.parametrize("groups", [None, ([0, 2, 4], [30, 9])], ids=["alone", "groups"])
+def test_bounds_out_of_order(L, cache, starts, most, groups):
+    kv = [40, 50, 60, 70]
+    b = R.Batch([2, 2, 2, 2], kv, 4, 2, 64, 16, cache, seed=3)
+    good, owner = owners(starts, kv, most, 8)
+    b.q_start, b.q_len = np.array(starts), [e - s if ok else 0 for s, e, ok in zip(starts, starts[1:], good)]
+    if groups:
+        b.groups, b.group_len = groups
+        b.share()
+    d = Dev(L, b)
+    out, lse, info = poisoned(L, b, d, max_q_len=most)
+    ref = b.reference()
+    assert info[2] == 4 - sum(good)
+    inside = [t for t in range(8) if owner[t] != -1]
+    outside = [t for t in range(8) if owner[t] == -1]
+    check_rows(b, out, lse, ref, inside)
+    assert torch.all(out[outside] == 9) and torch.all(lse[outside] == 5)
+
+
+def test_many_bounds_out_of_order(L):
+    """More sequences and more tokens than the plan has threads."""
+    r = np.random.default_rng(3)
+    N, T = 1500, 2600
+    base = np.sort(r.integers(0, T, N + 1))
+    for wild in (1, 40, N + 1):
+        starts = base.copy()
+        at = r.choice(N + 1, wild, replace=False)
+        starts[at] = r.integers(-5, T + 50, wild)
+        starts, kv = starts.tolist(), [int(x) for x in r.integers(1, 60, N)]
+        b = R.Batch([1] * T, [1] * T, 2, 1, 16, 16, "bf16", seed=wild)      # tokens and their queries
+        c = R.Batch([0] * N, kv, 2, 1, 16, 16, "bf16", seed=wild + 1)       # the cache
+        good, owner = owners(starts, kv, T, T)
+        c.q, c.T = b.q, T
+        c.q_start, c.q_len = np.array(starts), [e - s if ok else 0 for s, e, ok in zip(starts, starts[1:], good)]
+        d = Dev(L, c)
+        out, lse, info = poisoned(L, c, d, max_q_len=T)
+        assert info[2] == N - sum(good)
+        check_rows(c, out, lse, c.reference(), [t for t in range(T) if owner[t] != -1])
+        outside = [t for t in range(T) if owner[t] == -1]
+        assert torch.all(out[outside] == 9) and torch.all(lse[outside] == 5)
