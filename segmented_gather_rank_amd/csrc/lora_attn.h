@@ -61,27 +61,26 @@ LORA_HD int heads_per_item(int per_kv) {
   return 1;
 }
 
-LORA_HD int round_to(int64_t keys, int step) {
-  const int64_t c = (keys + step - 1) & ~(int64_t)(step - 1);
-  return c > (1 << 30) ? (1 << 30) : (int)c;
-}
+LORA_HD int64_t round_to(int64_t keys, int step) { return (keys + step - 1) & ~(int64_t)(step - 1); }
 
 // Length of a slice (few-row kernel) or most keys of a part (tile kernel): an
-// equal share of all keys for each of the `slots` workgroups, heads of which
-// work on the same keys, and at least `least`, in whole steps.
+// equal share of all keys for each of the `slots` workers, heads of which
+// work on the same keys, and at least `least`, in whole steps.  (Few workers a head
+// and long sequences: beyond 32 bits.)
 LORA_HD int slots_per_head(int heads, int slots) { return slots / heads > 0 ? slots / heads : 1; }
-LORA_HD int share_of(int64_t total, int heads, int slots, int least, int step) {
+LORA_HD int64_t share_of(int64_t total, int heads, int slots, int least, int step) {
   const int64_t c = ceil_div64(total, slots_per_head(heads, slots));
   return round_to(c < least ? least : c, step);
 }
 
-// Keys that a few-row tile occupies on the line that is cut into slices.
-LORA_HD int line_keys(int keys) { return keys > 0 ? round_to(keys, kCutKeys) : kCutKeys; }
+// Keys that a few-row tile occupies on the line that is cut into slices (a sequence
+// has at most 2^31 - 2^16).
+LORA_HD int line_keys(int keys) { return keys > 0 ? (int)round_to(keys, kCutKeys) : kCutKeys; }
 
 // Parts of a tile-kernel tile: equal parts of at most `share` keys.
-LORA_HD int part_keys(int keys, int share) {
+LORA_HD int part_keys(int keys, int64_t share) {
   if (keys <= share) return keys > 0 ? keys : 1;
-  return round_to(ceil_div64(keys, ceil_div64(keys, share)), kPartKeys);
+  return (int)round_to(ceil_div64(keys, ceil_div64(keys, share)), kPartKeys);
 }
 
 // Capacities of the work lists, from sizes the host knows.

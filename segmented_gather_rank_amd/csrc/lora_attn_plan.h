@@ -228,7 +228,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       if (!broken.seqs) {
         // (there are no more groups than sequences)
         const bool here = n < a.seqs && !seq_ordered(a, n), group = n < a.groups && !group_ordered(a, n);
-        broken.groups |= team.any(group);
+        if (a.groups) broken.groups |= team.any(group);
         if (team.any(here)) return false;
       }
       int len = 0;
@@ -266,7 +266,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
   team.sync();  // the counts; the list is written and read by this team alone
 
   // ---- the tiles' tokens and keys; few-row tiles take their place on the line
-  long long line = 0;
+  int64_t line = 0;
   unsigned long long keys = 0;
   for (int i0 = 0; i0 < tiles; i0 += threads) {
     const int i = i0 + tid;
@@ -324,20 +324,23 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
       if (r.few) width = line_keys(r.key1 - r.key0) / kCutKeys;
       else keys += (unsigned long long)(r.key1 - r.key0);
     }
-    int total;
-    const int before = team.before(width, total);
+    // a sum of 32 bits holds the low 20 of every width; tiles of 2^25 keys, rounded up
+    // to whole cuts, and more take a second one
+    int total, high_total = 0, high = 0;
+    const int low = team.before(width & 0xfffff, total);
+    if (a.table_stride * a.page_size >> 24 && team.any(width >> 20)) high = team.before(width >> 20, high_total);
     if (i < tiles) {
-      r.at = line + before;
+      r.at = line + ((int64_t)high << 20) + low;
       tile_list[i] = r;
     }
-    line += total;
+    line += ((int64_t)high_total << 20) + total;
   }
   if (keys) team.add(&common.keys, keys);
   team.sync();
-  const int slice = share_of(line * kCutKeys, a.heads, a.few_slots, kFewMinKeys, kCutKeys);
-  const int share = share_of((int64_t)common.keys, a.heads, kTileSlots, kTileMinKeys, kPartKeys);
-  const int cuts = slice / kCutKeys;  // of a slice
-  const int slots = (int)min_l((line + cuts - 1) / cuts, a.max_slots - 1);
+  const int64_t slice = share_of(line * kCutKeys, a.heads, a.few_slots, kFewMinKeys, kCutKeys);
+  const int64_t share = share_of((int64_t)common.keys, a.heads, kTileSlots, kTileMinKeys, kPartKeys);
+  const int64_t cuts = slice / kCutKeys;  // of a slice
+  const int slots = (int)((line + cuts - 1) / cuts);
 
   // ---- items, slices, partial-result units, tokens to join
   int few_items = 0, tile_items = 0, units = 0, joins = 0;
@@ -356,7 +359,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
         parts = (int)(last / cuts - r.at / cuts) + 1;
       } else {
         per = part_keys(n, share);
-        parts = max_i(1, (n + per - 1) / per);
+        parts = max_i(1, (int)ceil_div64(n, per));
       }
       join = parts > 1 || r.shared;
       ups = (r.ntok * a.group + kUnitRows - 1) / kUnitRows;
@@ -378,7 +381,7 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
           item.key0 = r.key0 + (int)(from - r.at) * kCutKeys;
           item.key1 = (int)min_l(r.key1, r.key0 + ((k + 1) * cuts - r.at) * kCutKeys);
           few_list[at] = item;
-          if (from == k * cuts && k < a.max_slots) {
+          if (from == k * cuts) {
             slot_list[k].first = at;
             slot_list[k].item = item;
             if (k > 0) slot_list[k - 1].end = at;
@@ -428,8 +431,8 @@ LORA_HD void attn_plan(const AttnPlanArgs &a, Team &team) {
     a.info[3] = common.bad_groups;
     a.info[4] = joins;
     a.info[5] = units;
-    a.info[6] = slice;
-    a.info[7] = share;
+    a.info[6] = (int)min_l(slice, 0x7fffffff);
+    a.info[7] = (int)min_l(share, 0x7fffffff);
     a.info[8] = few_items;
     for (int k = 9; k < kAttnInfoInts; ++k) a.info[k] = 0;
   }

@@ -304,6 +304,18 @@ static void spoil_lengths(Batch &b) {  // bad by their lengths, bounds in order
   if (rnd() % 2) b.max_q_len = (int)upto(b.max_q_len);
 }
 
+static void lengthen(Batch &b) {  // as many keys as the table may hold
+  if (rnd() % 4 == 0) b.page = 1;
+  b.stride = (rnd() % 2 ? 0x7fff0000 : (1 << 25) - (int)upto(2)) / b.page;
+  const int64_t most = b.stride * b.page;
+  for (int n = 0; n < b.seqs(); ++n)
+    if (rnd() % 3) b.kv_len[n] = (int32_t)(rnd() % 2 ? most - upto(70) : most / (1 + upto(40)) - upto(5));
+  for (auto &x : b.prefix) x = (int32_t)upto(0x7fffffff);
+  for (size_t t = 0; t < b.key_lo.size(); ++t) b.key_lo[t] = (int32_t)upto(most), b.key_hi[t] = (int32_t)upto(0x7fffffff);
+  for (int g = 0; g < b.groups(); ++g)
+    if (b.group_start[g] < b.group_start[g + 1] && rnd() % 2) b.group_len[g] = (int32_t)upto(b.kv_len[b.group_start[g]]);
+}
+
 static void spoil_bounds(Batch &b) {
   const int N = b.seqs();
   if (!N) return;
@@ -340,6 +352,7 @@ int main(int argc, char **argv) {
   const long trials = argc > 2 ? std::atol(argv[2]) : 1000;
   for (trial = 0; trial < trials; ++trial) {
     Batch b = ordered(rnd() % 2, kind == "groups" || kind == "bad_groups" || kind == "everything" || rnd() % 2);
+    if (kind == "long") lengthen(b);
     if (kind == "bad_ends" && b.seqs()) {  // the last sequence leaves the batch
       b.q_start.back() = (int32_t)b.tokens + 900;
     }

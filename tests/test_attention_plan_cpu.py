@@ -18,7 +18,7 @@ def plan_run(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("kind", ["ordered", "groups", "bad_groups", "bad_lengths", "bad_ends", "bad_bounds", "everything"])
+@pytest.mark.parametrize("kind", ["ordered", "groups", "bad_groups", "bad_lengths", "bad_ends", "bad_bounds", "everything", "long"])
 def test_plan(plan_run, kind):
     r = subprocess.run([plan_run, kind, "3000"], capture_output=True, text=True, timeout=600)
     assert r.returncode == 0 and "all checks passed" in r.stdout, r.stdout[-500:] + r.stderr[-2000:]

@@ -185,3 +185,32 @@ def test_many_bounds_out_of_order(L):
         check_rows(c, out, lse, c.reference(), [t for t in range(T) if owner[t] != -1])
         outside = [t for t in range(T) if owner[t] == -1]
         assert torch.all(out[outside] == 9) and torch.all(lse[outside] == 5)
+
+
+@pytest.mark.parametrize("q", [1, 40])
+def test_as_many_keys_as_a_table_holds(L, q):
+    """2^31 - 2^16 keys of one sequence, two pages over and over: the first half of
+    them one page, the second half the other."""
+    D, page, n = 8, 65536, 32767
+    r = np.random.default_rng(5)
+    k, v = (r.standard_normal((2, 1, page, D)).astype(np.float32) for _ in range(2))
+    v[1] += 4
+    k, v = (torch.from_numpy(x).to(torch.bfloat16) for x in (k, v))
+    table = np.full((1, n), 1, np.int32)
+    table[0, :n // 2] = 0
+    cache = L.KvCache(k.cuda(), v.cuda())
+    qs = torch.from_numpy(r.standard_normal((q, 1, D)).astype(np.float32)).to(torch.bfloat16)
+    meta = L.lora_prepare_attn_meta(dev(np.array([0, q])), dev(np.array([n * page])), dev(table), cache, 1, q, causal=False)
+    lse = torch.empty((q, 1), device="cuda")
+    out, _ = L.lora_attention(meta, qs.cuda(), cache, lse=lse)
+    kk, vv = (x.double().numpy()[:, 0] for x in (k, v))
+    x = np.einsum("pjd,qd->qpj", kk, qs.double().numpy()[:, 0]) / np.sqrt(D)
+    w = np.exp(x) * np.array([n // 2, n - n // 2])[:, None]
+    total = w.sum((1, 2))
+    want = np.einsum("qpj,pjd->qd", w, vv) / total[:, None]
+    spread = np.einsum("qpj,pjd->qd", w, np.abs(vv)) / total[:, None]
+    # a lane adds a quarter of a slice's (part's) keys one after the other in fp32
+    keys = int(meta.tensors()["info"][6 if q == 1 else 7])
+    sums = min(keys, n * page) / 4 * R.F32_HALF
+    assert np.all(np.abs(lse.cpu().double().numpy()[:, 0] - np.log(total)) <= sums + 1e-3)
+    assert np.all(np.abs(out.cpu().double().numpy()[:, 0] - want) <= (2 * sums + 2 * R.BF16_HALF + 1e-3) * spread)
