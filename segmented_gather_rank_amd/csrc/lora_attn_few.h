@@ -207,10 +207,9 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
     }
     // ---- softmax
     if constexpr (GENERAL) {
+      const int away = pos - (k0 + 4 * g);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) st[t][i] = logit2<true>(sc, st[t][i], pos - (k0 + 16 * t + 4 * g + i));
+      for (int t = 0; t < 2; ++t) general_logits<4>(sc, st[t], [&](int i) { return away - (16 * t + i); });
     }
     uint32_t see = 0xff;  // of this lane's keys (bit 4 t + i)
     if (masked) {
@@ -350,17 +349,14 @@ __device__ __forceinline__ void run_few_f32(const AttnArgs &a, const AttnItem &i
 #pragma unroll
       for (int e = 0; e < 4; ++e) st = __builtin_amdgcn_mfma_f32_16x16x4f32(kr[s][e], q[s][e], st, 0, 0, 0);
     float top = m, seen[4];
+    if constexpr (GENERAL) general_logits<4>(sc, st, [&](int i) { return pos - (k0 + 4 * g + i); });
+    else st *= sc.mul;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = 4 * g + i, key = k0 + j;
       const bool see = key >= lo && key < hi && key < it.key1 && ((good >> j) & 1);
       seen[i] = see ? 1.f : 0.f;
-      float x = st[i] * sc.mul;
-      if constexpr (GENERAL) {
-        if (sc.cap > 0.f) x = sc.cap * tanhf(x / sc.cap);
-        x = (x - sc.slope * fabsf((float)(pos - key))) * kLog2e;
-      }
-      st[i] = see ? x : kNegInf;
+      st[i] = see ? st[i] : kNegInf;
       top = fmaxf(top, st[i]);
     }
     top = max_rows(top);

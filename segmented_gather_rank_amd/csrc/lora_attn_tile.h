@@ -173,12 +173,10 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
     }
     __builtin_amdgcn_sched_group_barrier(kSchedMfma, kAhead, 0);
   };
-  auto general_logits = [&](int tile, f32x16 (&st)[2]) {
+  auto logits = [&](int tile, f32x16 (&st)[2]) {
     const int away = pos - (it.key0 + tile * kKeys + 4 * g);
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) st[t][i] = logit2<true>(sc, st[t][i], away - (32 * t + 8 * (i / 4) + i % 4));
+    for (int t = 0; t < 2; ++t) general_logits<16>(sc, st[t], [&](int i) { return away - (32 * t + 8 * (i / 4) + i % 4); });
   };
   auto hide = [&](int tile, f32x16 (&st)[2]) {
     const int from = it.key0 + tile * kKeys + 4 * g - lo;
@@ -287,7 +285,7 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
       if (!wave_ok) continue;
       f32x16 st[2];
       scores(lds.k0, st);
-      if constexpr (GENERAL) general_logits(tile, st);
+      if constexpr (GENERAL) logits(tile, st);
       uint32_t see = 0;
 #pragma unroll
       for (int t = 0; t < 2; ++t)
@@ -387,7 +385,7 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
       if (wave_ok) {
         f32x16 st[2];
         scores(tile & 1 ? lds.k1 : lds.k0, st);
-        if constexpr (GENERAL) general_logits(tile, st);
+        if constexpr (GENERAL) logits(tile, st);
         if (is_masked(tile)) hide(tile, st);
         raise(st);
         minus = base == kNegInf ? 0.f : -base;
@@ -444,7 +442,7 @@ __device__ __forceinline__ bool run_tile(const AttnArgs &a, const AttnItem &it, 
       if (wave_ok) {
         f32x16 st[2];
         scores(k_now, st);
-        if constexpr (GENERAL) general_logits(t, st);
+        if constexpr (GENERAL) logits(t, st);
         if (masked) hide(t, st);
         raise(st);
         minus = base == kNegInf ? 0.f : -base;

@@ -214,3 +214,46 @@ def test_as_many_keys_as_a_table_holds(L, q):
     sums = min(keys, n * page) / 4 * R.F32_HALF
     assert np.all(np.abs(lse.cpu().double().numpy()[:, 0] - np.log(total)) <= sums + 1e-3)
     assert np.all(np.abs(out.cpu().double().numpy()[:, 0] - want) <= (2 * sums + 2 * R.BF16_HALF + 1e-3) * spread)
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-3, 0.5, 30.0, 1e4, 1e6, 1e8, 1e30, 3e38])
+@pytest.mark.parametrize("cache,tokens", [("bf16", 1), ("e4m3", 1), ("f32", 1), ("bf16", 300), ("e4m3", 300)])
+def test_capped_score_alone(L, cap, cache, tokens):
+    """Every row sees one key, so that its log-sum is its capped score: small and large
+    against the cap, on both sides of a quarter of it."""
+    D, T, page = 16, 300, 16
+    x = np.concatenate([np.geomspace(1e-4, 3e4, 120), cap * np.geomspace(1e-3, 20, 60), cap * np.linspace(0.2, 0.3, 90)])
+    x = np.concatenate([x, -x])[np.linspace(0, 2 * len(x) - 1, T).astype(int)]
+    x[0] = 0
+    scale = 0.731
+    q_type = torch.float32 if cache == "f32" else torch.bfloat16
+    q = torch.zeros((T, 1, D), dtype=q_type)
+    q[:, 0, 3] = torch.from_numpy(np.clip(x / scale, -3e38, 3e38)).to(q_type)
+    k = torch.zeros((T // page + 1, 1, page, D), dtype=torch.float32)
+    k[..., 3] = 1
+    k = k.to({"bf16": torch.bfloat16, "f32": torch.float32, "e4m3": torch.float8_e4m3fn}[cache])
+    seqs = T // tokens                       # of one token each, or one of all
+    kv = L.KvCache(k.cuda(), k.clone().cuda())
+    at = np.arange(T)
+    table = np.tile(np.arange(T // page + 1), (seqs, 1))
+    meta = L.lora_prepare_attn_meta(dev(np.arange(seqs + 1) * tokens), dev(np.full(seqs, T)), dev(table), kv, 1, T,
+                                    max_q_len=tokens, causal=False, key_lo=dev(at), key_hi=dev(at + 1))
+    lse = torch.empty((T, 1), device="cuda")
+    out, _ = L.lora_attention(meta, q.cuda(), kv, scale=scale, cap=cap, lse=lse)
+    x = q.double().numpy()[:, 0, 3] * float(np.float32(scale))
+    want = float(np.float32(cap)) * np.tanh(x / float(np.float32(cap)))
+    got = lse.cpu().double().numpy()[:, 0]
+    # every operation on the score off by half a step or one, and tanh by 5 half steps of
+    # 1 where it is at least a quarter: 32 half steps of the result
+    bound = 32 * R.F32_HALF * np.abs(want) + np.finfo(np.float32).tiny
+    assert np.all(np.abs(got - want) <= bound), (x[np.abs(got - want) > bound], got[np.abs(got - want) > bound])
+    assert torch.equal(out[:, 0, 3].cpu(), torch.ones(T, dtype=q_type))
+
+
+@pytest.mark.parametrize("cap", [1e4, 1e8, 1e30])
+@pytest.mark.parametrize("cache", ["bf16", "f32", "e4m3"])
+def test_cap_far_above_the_scores(L, cap, cache):
+    """Such a cap changes nothing: the bounds are those without one."""
+    b = R.Batch([1, 50, 2], [300, 120, 64], 8, 4, 128, 16, cache, seed=2)
+    o, lse, _, _ = run(L, b, cap=cap)
+    check(b, o, lse, b.reference())
