@@ -171,6 +171,18 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _empty_for(stream, size, dtype, device) -> torch.Tensor:
+    """Memory for work on `stream` (None: the current one; a Stream or a raw handle),
+    from that stream's own pool: earlier work on another stream may still use what
+    that one's pool gives out, and would get this back before the work here has ended."""
+    if stream is None:
+        return torch.empty(size, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream_handle(stream), device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=dtype, device=device)
+
+
 def _dtype(t: torch.Tensor) -> int:
     if t.dtype == torch.float32:
         return LORA_F32
@@ -656,7 +668,7 @@ def lora_prepare_attn_meta(q_start: torch.Tensor, kv_len: torch.Tensor, page_tab
     need = _sz(0)
     _check("lora_attn_meta_workspace_bytes", _lib.lora_attn_meta_workspace_bytes(C.byref(b), cache.ref, C.byref(need)))
     if workspace is None:
-        workspace = torch.empty(int(need.value), dtype=torch.uint8, device=kv_len.device)
+        workspace = _empty_for(stream, int(need.value), torch.uint8, kv_len.device)
     m = lora_attn_meta()
     st = _lib.lora_prepare_attn_meta(C.byref(b), cache.ref, _dev(workspace, "workspace"), workspace.numel(),
                                      C.byref(m), _stream(stream))
@@ -689,10 +701,11 @@ def lora_attention(meta: AttnMeta, q: torch.Tensor, cache: KvCache, out: torch.T
     """Attention of q [T][heads][dim] (or [T][heads * dim]) over the cached keys
     that meta says it sees; returns out, or (out, lse) when lse (float32
     [T][heads]) is given.  scale: default 1 / sqrt(dim); cap: tanh cap of the
-    scores (0: none); slopes: float32 [heads], bias per unit of distance."""
+    scores (0: none); slopes: float32 [heads], bias per unit of distance.  An out
+    or workspace that is not given is allocated on the stream of the call."""
     c = meta.c
     if out is None:
-        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        out = _empty_for(stream, q.shape, q.dtype, q.device)
     width = c.num_q_heads * c.head_dim
     for name, t in (("q", q), ("out", out)):
         rows = t.shape[0] == c.num_tokens and t.dtype == cache.query_dtype and t.stride(-1) == 1
@@ -704,9 +717,7 @@ def lora_attention(meta: AttnMeta, q: torch.Tensor, cache: KvCache, out: torch.T
     if lse is not None and (lse.dtype != torch.float32 or lse.shape != (c.num_tokens, c.num_q_heads) or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [T][heads]")
     if workspace is None:
-        workspace = torch.empty(meta.attention_bytes, dtype=torch.uint8, device=q.device)
-        if isinstance(stream, torch.cuda.Stream):
-            workspace.record_stream(stream)   # freed here, in use there
+        workspace = _empty_for(stream, meta.attention_bytes, torch.uint8, q.device)
     st = _lib.lora_attention(
         meta.ref, _dev(q, "q"), q.stride(0) if c.num_tokens > 1 else width, cache.ref,
         c.head_dim ** -0.5 if scale is None else scale, cap, None if slopes is None else _dev(slopes, "slopes"),

@@ -257,3 +257,34 @@ def test_cap_far_above_the_scores(L, cap, cache):
     b = R.Batch([1, 50, 2], [300, 120, 64], 8, 4, 128, 16, cache, seed=2)
     o, lse, _, _ = run(L, b, cap=cap)
     check(b, o, lse, b.reference())
+
+
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_memory_of_another_stream(L, raw):
+    """With a stream given, metadata, outputs and workspaces that the call allocates are
+    neither still in use on the current stream nor reused there while it runs."""
+    b = R.Batch([1, 30, 1], [2000, 500, 700], 8, 2, 128, 16, "bf16", seed=1)
+    d = Dev(L, b)
+    want = L.lora_attention(d.meta(L), d.q, d.cache)
+    need = L.lora_attention_workspace_bytes(d.meta(L))
+    busy = torch.randn((4096, 4096), device="cuda")
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    stream = s.cuda_stream if raw else s
+    for size in (need, 1 << 16, 1 << 14):
+        # the current stream: work that is still to write to memory it has freed
+        for _ in range(20):
+            busy.mul_(1.0001)
+        held = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        del held
+        # the other one: the call behind other work, and its memory freed at once
+        with torch.cuda.stream(s):
+            other = torch.ones((4096, 4096), device="cuda")
+            for _ in range(20):
+                other.mul_(1.0001)
+        meta = d.meta(L, stream=stream)
+        out = L.lora_attention(meta, d.q, d.cache, stream=stream)
+        for _ in range(4):
+            torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
