@@ -288,3 +288,24 @@ def test_memory_of_another_stream(L, raw):
             torch.full((size,), 255, dtype=torch.uint8, device="cuda")
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+def test_append_of_more_rows_than_one_launch(L):
+    """More tokens than a launch of 256 threads each may hold (2^24 - 1)."""
+    T, D = (1 << 24) + 5, 8
+    x = torch.zeros((T, 3 * D), dtype=torch.bfloat16, device="cuda")
+    rows = [0, 1, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, (1 << 24) - 1, 1 << 24, T - 1]
+    x[rows] = torch.randn((len(rows), 3 * D), device="cuda").to(torch.bfloat16)
+    slot = torch.full((T,), -1, dtype=torch.int64, device="cuda")
+    slot[rows] = torch.arange(len(rows), device="cuda")
+    slot[[5, T - 3]] = -2                                   # bad
+    k = torch.zeros((2, 1, 4, D), dtype=torch.bfloat16, device="cuda")
+    v, q = torch.zeros_like(k), torch.full((T, D), 7.0, dtype=torch.bfloat16, device="cuda")
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    L.lora_cache_append(x, L.KvCache(k, v), slot, q, num_bad=bad)
+    assert int(bad) == 2
+    assert torch.equal(k.view(-1, D), x[rows, D:2 * D]) and torch.equal(v.view(-1, D), x[rows, 2 * D:])
+    assert torch.equal(q[rows], x[rows, :D]) and torch.all(q[[5, T - 3]] == 7)
+    q[[5, T - 3]] = 0
+    q[rows] = 0
+    assert not q.any()
