@@ -591,7 +591,9 @@ def lora_cache_append(qkv: torch.Tensor, cache: KvCache, slot: torch.Tensor, q_o
         q_ptr, ldq = _dev(q_out, "q_out") if T else None, q_out.stride(0) if T > 1 else q_out.shape[1]
     rot = pos_ptr = None
     if rotation is not None:
-        if pos is None or pos.dtype != torch.int32 or not pos.is_contiguous() or pos.numel() != rotation.num_axes * T:
+        axes = rotation.num_axes
+        if pos is None or pos.dtype != torch.int32 or not pos.is_contiguous() or pos.numel() != axes * T or (
+                axes > 1 and pos.dim() > 1 and pos.shape != (axes, T)):
             raise ValueError("pos must be contiguous int32 [axes][T]")
         rot, pos_ptr = rotation.ref, _dev(pos, "pos") if T else None
     if num_bad is not None and num_bad.dtype != torch.int32:
