@@ -214,7 +214,7 @@ lora_status lora_prepare_attn_meta(const lora_attn_batch *b, const lora_kv_cache
   a.key_hi = b->d_key_hi;
   a.group_start = b->d_group_start;
   a.group_len = b->d_group_len;
-  a.tokens = b->num_seqs > 0 ? b->num_tokens : 0;
+  a.tokens = b->num_tokens;
   a.table_stride = b->page_table_stride;
   a.seqs = b->num_seqs;
   a.groups = b->num_groups;

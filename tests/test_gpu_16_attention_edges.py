@@ -309,3 +309,21 @@ def test_append_of_more_rows_than_one_launch(L):
     q[[5, T - 3]] = 0
     q[rows] = 0
     assert not q.any()
+
+
+@pytest.mark.parametrize("groups", [False, True])
+def test_tokens_without_sequences(L, groups):
+    """A batch of no sequences: its tokens are outside every one, and not written."""
+    b = R.Batch([1] * 5, [3] * 5, 4, 2, 64, 16, "bf16", seed=3)
+    d = Dev(L, b)
+    d.args = (dev(np.array([0])), dev(np.zeros(0)), torch.empty((0, 3), dtype=torch.int32, device="cuda"))
+    if groups:
+        d.kw.update(group_start=dev(np.array([0])), group_len=dev(np.zeros(0)))
+    meta = d.meta(L, max_q_len=1, workspace=torch.full((1 << 20,), 0x5a, dtype=torch.uint8, device="cuda"))
+    hold, lse = torch.full((5, 4, 64), 9.0, dtype=torch.bfloat16, device="cuda"), torch.full((5, 4), 5.0, device="cuda")
+    L.lora_attention(meta, d.q, d.cache, hold, lse=lse)
+    torch.cuda.synchronize()
+    assert torch.all(hold == 9) and torch.all(lse == 5)
+    t = meta.tensors()
+    assert t["info"].tolist()[:6] == [0] * 6
+    assert torch.equal(t["limits"].cpu(), torch.tensor([[0, 0, 0, -1]] * 5, dtype=torch.int32))
