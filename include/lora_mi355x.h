@@ -523,8 +523,10 @@ lora_status lora_attention_workspace_bytes(const lora_attn_meta *meta, size_t *b
  *     lse[t][h] = log sum_j exp(x[j]),   out[t][h] = sum_j exp(x[j] - lse) v_j
  * Query head h reads key head h / (num_q_heads / num_kv_heads).  Scores,
  * maxima, sums and products are kept in fp32; with a bf16 or e4m3 cache the
- * weights exp(.) are rounded to bf16 for the product with v, as the matrix
- * cores take them.
+ * weights exp(.) go to the product with v in bf16, as the matrix cores take them:
+ * as two terms (2^-16 of a weight is lost) for sequences of at most 16 rows, a
+ * query token and one of the heads_per_item heads being a row, rounded once (2^-8)
+ * for longer ones and for the shared keys of groups of more.
  *   d_q           device [T][ldq] (bf16, or fp32 with an fp32 cache): head h at
  *                 column h * head_dim
  *   d_out         device [T][ldo] of the same type, likewise; not overlapping q

@@ -11,6 +11,12 @@
 // the operand of the next product if V is taken in the same key order, which the
 // transposing LDS read does.  No weight ever leaves its lane.
 //
+// The matrix cores take bf16, so a weight goes in as two terms, its rounding and
+// what that leaves out (2^-16 of it is lost), and the products with V run twice.  The
+// kernel waits for memory anyway: 537 us with one term and with two on the decode
+// batch below, 349 and 354 on 512 decode tokens beside 4 prompts of 1024.  (The tile
+// kernel, which the matrix cores bound, takes one term.)
+//
 // Bound: the keys and values are read once and used by at most 16 rows, 16 / 2
 // operations per byte, so HBM bounds it.  Hence no sharing: every wave is a
 // worker of its own with a slice of the keys (lora_attn.h), 32 keys a step, and
@@ -240,7 +246,7 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
         for (int i = 0; i < 4; ++i) o[d][i] *= fade;
     }
     const float minus = base == kNegInf ? 0.f : -base;
-    u32x4 pw;
+    u32x4 pw, rest;  // the weights in bf16; what that leaves out
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
 #pragma unroll
@@ -248,10 +254,14 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
         st[t][i] = exp2_fast(__builtin_fmaf(st[t][i], mul, minus));
         l += st[t][i];
       }
-      pw[2 * t] = pack_bf16x2(st[t][0], st[t][1]);
-      pw[2 * t + 1] = pack_bf16x2(st[t][2], st[t][3]);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t w = pack_bf16x2(st[t][2 * i], st[t][2 * i + 1]);
+        pw[2 * t + i] = w;
+        rest[2 * t + i] = pack_bf16x2(st[t][2 * i] - __uint_as_float(w << 16), st[t][2 * i + 1] - __uint_as_float(w & 0xffff0000u));
+      }
     }
-    const bf16x8 p = __builtin_bit_cast(bf16x8, pw);
+    const bf16x8 p = __builtin_bit_cast(bf16x8, pw), p_rest = __builtin_bit_cast(bf16x8, rest);
     // ---- O^T += V^T P^T
 #pragma unroll
     for (int d = 0; d < DP / 16; ++d) {
@@ -271,6 +281,7 @@ __device__ __forceinline__ bool run_few(const AttnArgs &a, const AttnItem &it, i
         for (int i = 0; i < 4; ++i) o[d][i] = add_counted_infs(o[d][i], pi[i], ni[i]);
         v = v_part(v, kVFinite);
       }
+      o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), p_rest, o[d], 0, 0, 0);
       o[d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, v), p, o[d], 0, 0, 0);
     }
   }

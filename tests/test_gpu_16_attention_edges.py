@@ -327,3 +327,19 @@ def test_tokens_without_sequences(L, groups):
     t = meta.tensors()
     assert t["info"].tolist()[:6] == [0] * 6
     assert torch.equal(t["limits"].cpu(), torch.tensor([[0, 0, 0, -1]] * 5, dtype=torch.int32))
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+@pytest.mark.parametrize("q,kv", [([1] * 8, [5, 20, 33, 64, 150, 300, 700, 1500]), ([2, 4, 3], [90, 40, 600])])
+def test_weights_of_few_rows(L, cache, q, kv):
+    """Weights beyond bf16: an output that cancels is still right to its own rounding."""
+    b = R.Batch(q, kv, 8, 2, 64, 16, cache, seed=12)
+    o, lse, _, _ = run(L, b)
+    out, rl, _, lse_tol = b.reference()
+    b.v_store = b.v_store.float().abs().to(b.v_store.dtype)
+    spread = b.reference()[0]                       # sum of weight * |v|
+    # a weight: 2^-16 and twice its score's error (which the log-sum's bound holds), and as
+    # many fp32 half steps as there are keys in a lane's sum; then one rounding
+    w = 2.0 ** -16 + 2 * lse_tol[..., None] + max(kv) / 4 * R.F32_HALF
+    tol = w * spread + R.BF16_HALF * (np.abs(out) + w * spread)
+    check(b, o, lse, (out, rl, tol, lse_tol))
