@@ -476,7 +476,7 @@ typedef struct lora_attn_batch {
     int32_t causal, window;
     int32_t num_groups;
     const int32_t *d_prefix_len;    /* [num_seqs] or NULL */
-    const int32_t *d_key_lo, *d_key_hi;   /* [num_tokens] or NULL */
+    const int32_t *d_key_lo, *d_key_hi;   /* [num_tokens], both or neither */
     const int32_t *d_group_start, *d_group_len;
 } lora_attn_batch;
 
@@ -533,7 +533,10 @@ lora_status lora_attention_workspace_bytes(const lora_attn_meta *meta, size_t *b
  *   d_slopes      device fp32 [num_q_heads] or NULL (no bias)
  *   d_lse         device fp32 [T][num_q_heads] or NULL, contiguous
  * Tokens outside every sequence are not written.  A non-finite key or value
- * reaches the tokens that see it and no others.  Calls that run at the same
+ * reaches the tokens that see it (a key possibly as NaN where its score is -inf) and
+ * no others.  The query heads of a key head are taken in equal parts of at most 16,
+ * and each part reads the keys: counts above 16 without a divisor near it (17, 71)
+ * read them many times.  Calls that run at the same
  * time need workspaces of their own. */
 lora_status lora_attention(const lora_attn_meta *meta, const void *d_q, int64_t ldq,
                            const lora_kv_cache *cache, float scale, float cap,

@@ -664,7 +664,7 @@ def lora_prepare_attn_meta(q_start: torch.Tensor, kv_len: torch.Tensor, page_tab
     """Attention metadata of a batch: q_start int32 [N + 1], kv_len int32 [N],
     page_table int32 [N][pages]; the masks and groups of ``lora_attn_batch``.
     max_q_len: the most query tokens of a sequence (default num_tokens); a batch
-    that states it has few, as in decode, spares a launch."""
+    that states it has few, as in decode, has no tile work to launch."""
     b = _attn_batch(q_start, kv_len, page_table, num_q_heads, num_tokens, max_q_len, causal, window, prefix_len,
                     key_lo, key_hi, group_start, group_len)
     need = _sz(0)

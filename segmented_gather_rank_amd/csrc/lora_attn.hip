@@ -7,8 +7,8 @@
 // construction, so each has one wave.  Tile items are taken longest first,
 // by as many workgroups as there are items, or in rounds beyond kMaxTileBlocks.
 //
-// Measured: 512 decode tokens (window 1024) and 4 prompts of 1024, 347 us, where
-// the slices alone take 287 and the tiles alone 96; 8 and 8 workgroups of the two
+// Measured: 512 decode tokens (window 1024) and 4 prompts of 1024, 350 to 354 us (347
+// before the slices took weights of two terms, alone 287 then, and the tiles alone 96); 8 and 8 workgroups of the two
 // kinds in turn leave places empty where one kind has no work (a long prompt took
 // 3268 instead of 2630 us), tiles first take 454 us on the mixed batch.
 #include <algorithm>

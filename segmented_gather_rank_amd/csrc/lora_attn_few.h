@@ -26,8 +26,8 @@
 // computed, and page ids are fetched two steps ahead.
 //
 // Measured (32 / 8 heads of 128): 256 decode sequences of 64 to 6000 keys, bf16
-// pages of 16, 535 us, 5.87 TB/s; 24 of 30 to 65 thousand keys, e4m3, capped, 364
-// us, 5.88 TB/s.  Twice as many waves read no faster (544 us).
+// pages of 16, 530 us, 5.9 TB/s; 24 of 30 to 65 thousand keys, e4m3, capped, 367
+// us, 5.8 TB/s; 64 of 64 to 3000 keys, fp32, 204 us, 3.8 TB/s.  Twice as many waves read no faster (544 us).
 #pragma once
 
 #include "lora_attn_dev.h"

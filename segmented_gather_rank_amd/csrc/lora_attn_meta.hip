@@ -13,9 +13,11 @@
 //                       items and, for tokens whose result comes in parts, where
 //                       the parts lie.
 //
-// Both are bound by latency and shared by the layers of a step: 4 and 9 us for one
-// sequence, 6 and 21 us for 512 decode tokens and 4 prompts of 1024, 5 and 33 us
-// for 67 tiles of 128 tokens (a thread reads a tile's intervals).
+// The algorithm is in lora_attn_plan.h.  Both are bound by latency and shared by the
+// layers of a step: 2 and 17 us for one sequence of 1000 keys (a thread writes its
+// slices), 5 and 12 us for 256 decode tokens, 6 and 20 us for those of 512 and 4
+// prompts of 1024, 5 and 42 us for 512 tiles of 128 rows (a thread reads a tile's
+// intervals).
 #include "lora_attn_host.h"
 #include "lora_attn_plan.h"
 #include "lora_common.h"

@@ -11,7 +11,7 @@
 //
 // The weights are rounded to bf16 (their sum is not): a second term, as the few-row
 // kernel takes, would be half as many products again where they are the bound.  The
-// error of a bf16 result is then 2.0e-3 to 2.4e-3 of its size, where fp32 weights
+// error of a bf16 result is then 1.9e-3 to 2.2e-3 of its size, where fp32 weights
 // leave the 1.7e-3 of its own rounding.
 //
 // Bound: 4 dim operations per row and key on the matrix cores against one
@@ -23,8 +23,9 @@
 // reads run six matrix instructions ahead in the first product, and in the second
 // every matrix instruction is followed by its share of the exponentials.
 //
-// Measured (16384-token prompt, 32 / 8 heads of 128, causal): 2250 us, 977 TFLOP/s,
-// where a library product of 8192^3 reaches 1200; through registers 2419 us.  At
+// Measured (16384-token prompt, 32 / 8 heads of 128, causal): 2230 to 2290 us, 960 to
+// 990 TFLOP/s, where a library product of 8192^3 reaches 1200; through registers 2419
+// us, but an e4m3 cache 2209.  At
 // this rate the chip lowers its clock (2.0 GHz): with the scores of tile t + 1
 // computed beside the weights of tile t the matrix cores were busy 45 % of the
 // cycles instead of 37 %, for 2290 us in all, and short ranges lost a quarter.
