@@ -11,6 +11,7 @@ or ``__graft_entry__.build()``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 from dataclasses import dataclass
@@ -171,15 +172,20 @@ def _stream_handle(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _empty_for(stream, size, dtype, device) -> torch.Tensor:
-    """Memory for work on `stream` (None: the current one; a Stream or a raw handle),
-    from that stream's own pool: earlier work on another stream may still use what
-    that one's pool gives out, and would get this back before the work here has ended."""
+def _on(stream, device):
+    """Where memory for work on `stream` (None: the current one; a Stream or a raw
+    handle) is allocated and cleared: on that stream, from its own pool.  Earlier work on
+    another stream may still use what that one's pool gives out, and would get this back
+    before the work here has ended."""
     if stream is None:
-        return torch.empty(size, dtype=dtype, device=device)
+        return contextlib.nullcontext()
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream_handle(stream), device)
-    with torch.cuda.stream(stream):
+    return torch.cuda.stream(stream)
+
+
+def _empty_for(stream, size, dtype, device) -> torch.Tensor:
+    with _on(stream, device):
         return torch.empty(size, dtype=dtype, device=device)
 
 
@@ -288,7 +294,7 @@ def lora_prepare_meta(token_slot: torch.Tensor, num_slots: int, workspace: torch
     T = token_slot.shape[0]
     need = lora_meta_workspace_bytes(T, num_slots)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=token_slot.device)
+        workspace = _empty_for(stream, need, torch.uint8, token_slot.device)
     m = lora_meta()
     st = _lib.lora_prepare_meta(_dev(token_slot, "token_slot") if T else None, T, num_slots,
                                 _dev(workspace, "workspace"), workspace.numel(), C.byref(m), _stream(stream))
@@ -317,7 +323,7 @@ def lora_prepare_moe_meta(topk_ids: torch.Tensor, token_slot: torch.Tensor, num_
     T, K = topk_ids.shape
     need = lora_moe_meta_workspace_bytes(T, K, num_slots, num_local_experts)
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=topk_ids.device)
+        workspace = _empty_for(stream, need, torch.uint8, topk_ids.device)
     em = None
     if expert_map is not None:
         if expert_map.dtype != torch.int32 or expert_map.numel() != num_experts:
@@ -407,7 +413,7 @@ def lora_shrink(meta: LoraMeta, x: torch.Tensor, A, u: torch.Tensor, scale: floa
     n = len(A_list)
     need = lora_shrink_workspace_bytes(meta.num_tokens, meta.num_slots, d_in, n, r, x.dtype, mode)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _empty_for(stream, max(need, 16), torch.uint8, x.device)
     ss = None if slot_scale is None else _dev(slot_scale, "slot_scale")
     st = _lib.lora_shrink(C.byref(meta.c), xp, ldx, d_in, _dtype(x), n, A_arr, r, float(scale), ss,
                           _ranks(slot_rank), _dev(u, "u"), MODES[mode], _dev(workspace, "workspace"),
@@ -463,7 +469,8 @@ def lora_apply(meta: LoraMeta, x: torch.Tensor, A, B, offsets, y: torch.Tensor, 
         raise ValueError("A and B need one entry per slice")
     need = lora_apply_workspace_bytes(meta.num_tokens, meta.num_slots, d_in, n, r, x.dtype, mode)
     if workspace is None:
-        workspace = apply_workspace(need, x.device)
+        with _on(stream, x.device):
+            workspace = apply_workspace(need, x.device)
     if y.dim() != 2 or y.stride(1) != 1:
         raise ValueError("y must be [T][ldy] with unit column stride")
     ss = None if slot_scale is None else _dev(slot_scale, "slot_scale")
