@@ -2,8 +2,9 @@
  * lora_mi355x.h -- C ABI of the multi-LoRA batched low-rank delta on MI355X
  * (gfx950): slot metadata, shrink, expand, and the fused apply; and of the
  * attention that its q/k/v rows go on to: cache append, attention metadata,
- * attention (the last part of this file, with conventions of its own where it
- * says so).
+ * attention; and of the 8-bit base products that it is added to, with a MoE layer's
+ * routing, activation and weighted sum (the last parts of this file, with conventions
+ * of their own where they say so).
  *
  * For a batch of T tokens, token t names an adapter slot token_slot[t] in
  * [0, S), or -1 for "no adapter".  The library adds, for every packed output
@@ -542,6 +543,141 @@ lora_status lora_attention(const lora_attn_meta *meta, const void *d_q, int64_t 
                            const lora_kv_cache *cache, float scale, float cap,
                            const float *d_slopes, void *d_out, int64_t ldo,
                            float *d_lse, void *d_ws, size_t ws_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The base side of a layer.  lora_apply adds the adapters' delta to a base product
+ * that is already in y; the entry points below make that product where the base
+ * weights are 8-bit integers, dense or by expert, and what a MoE layer needs around
+ * it: the choice of experts (which lora_prepare_moe_meta takes), the rows' 8-bit
+ * form, the gated activation between the two products, the weighted sum of a token's
+ * choices.  None of them allocates or needs an initialised workspace; calls on one
+ * stream may share one.
+ * ------------------------------------------------------------------------- */
+
+typedef enum lora_score {
+    LORA_SCORE_SOFTMAX = 0,
+    LORA_SCORE_SIGMOID = 1,
+    LORA_SCORE_RANGE_MIN_ = -2147483647 - 1,  /* range markers, as above */
+    LORA_SCORE_RANGE_MAX_ = 2147483647
+} lora_score;
+
+/* How a router's logits become expert choices.  With s = softmax(x) or sigmoid(x)
+ * and c = s + bias:
+ *   - the experts stand in num_groups equal groups of consecutive ids; a group's rank
+ *     is the sum of the group_top largest c in it, and the topk_groups of highest rank
+ *     stay (num_groups = 1: all stay, the other two are not read);
+ *   - the topk experts of largest c among them are chosen, in descending order;
+ *   - choice e gets the weight s[e] * scale, divided by the chosen s's sum if
+ *     renormalize (a sum of 0 gives weights of 0).
+ * Equal values go to the lowest id, for groups and experts.  Without bias the order of
+ * experts is that of the logits themselves; else c and the ranks are compared as
+ * 64-bit arithmetic gives them.  A logit of -inf masks its expert: s = 0, and it comes
+ * after every other expert of the kept groups, whatever its bias (it is still chosen
+ * where fewer than topk others are left).  +inf logits share the softmax's mass.  NaN
+ * logits are ordered like -inf, and every weight of their token is NaN; a NaN bias masks
+ * like -inf.  Ids are distinct and valid whatever the logits hold.
+ * Supported: num_experts in [1, 1024], num_groups in [1, 64] dividing it, group_top 1 or
+ * 2 (at most a group's experts), topk in [1, 32], at most the kept groups' experts. */
+typedef struct lora_routing {
+    int32_t num_experts, topk;
+    int32_t score;                  /* a lora_score value */
+    int32_t num_groups, topk_groups, group_top;
+    int32_t renormalize;
+    float scale;
+    const float *d_bias;            /* device fp32 [num_experts] or NULL */
+} lora_routing;
+
+/* Expert choices of every token.
+ *   d_logits      device [T][ld] of dtype (fp32 or bf16), num_experts columns; any ld
+ *                 and alignment of whole elements
+ *   d_topk_ids    device int32 [T][topk], contiguous: as lora_prepare_moe_meta takes it
+ *   d_weights     device fp32 [T][topk], contiguous */
+lora_status lora_moe_route(const lora_routing *routing, const void *d_logits, int64_t ld,
+                           int64_t num_tokens, lora_dtype dtype, int32_t *d_topk_ids,
+                           float *d_weights, void *stream);
+
+typedef enum lora_activation {
+    LORA_ACT_NONE = 0,              /* v = x: width columns */
+    LORA_ACT_SILU_MUL = 1,          /* v = x / (1 + exp(-x)) * u: width columns of x, then width of u */
+    LORA_ACT_RANGE_MIN_ = -2147483647 - 1,  /* range markers, as above */
+    LORA_ACT_RANGE_MAX_ = 2147483647
+} lora_activation;
+
+/* Rows to 8-bit integers with a scale each: with v the row (or its activation, in
+ * fp32) and m its largest |v|,
+ *     scale = m / 127,   q = 127 v / m, rounded to the nearest integer, halves to even
+ * exactly as these real numbers give it.  A row of zeros has scale 0; a row whose v
+ * holds an infinity or NaN has scale NaN and q 0, so that its products are NaN.
+ *   d_x           device [num_rows][ldx] of dtype (fp32 or bf16)
+ *   meta          NULL: every row.  Else metadata of num_rows rows with x_row_div = 1:
+ *                 only rows with a key are read and written (a MoE layer's pairs whose
+ *                 expert is local)
+ *   d_q           device int8 [num_rows][ldq]
+ *   d_scale       device fp32 [num_rows]
+ *   d_act         device [num_rows][ldact] of dtype, or NULL: v itself, rounded once
+ *                 (the x of the down projection's lora_apply)
+ * width is a multiple of 16, at most 2^24; ldx and ldact are multiples of 8, ldq of 16;
+ * the matrices are 16-byte aligned and do not overlap. */
+lora_status lora_quantize(const void *d_x, int64_t ldx, int64_t num_rows, int64_t width,
+                          lora_dtype dtype, lora_activation activation, const lora_meta *meta,
+                          int8_t *d_q, int64_t ldq, float *d_scale, void *d_act, int64_t ldact,
+                          void *stream);
+
+/* 8-bit base weights: expert e's matrix is d_out rows of d_in bytes (output-major, as
+ * checkpoints hold them), row n at ptr + e * expert_stride + n * row_stride; value n, k
+ * stands for ptr[...] * scale[e][n].
+ * Supported: d_in a multiple of 16, at most 131056 (the int32 sum of a row then cannot
+ * overflow), d_out a multiple of 8, at most 2^24, num_experts in [1, 1023] (1 for a dense
+ * layer), strides multiples of 16, (a block of 256 rows is addressed with 32-bit offsets:)
+ * row_stride below 2^23, ptr 16-byte aligned. */
+typedef struct lora_int8_weight {
+    const int8_t *ptr;
+    int64_t expert_stride, row_stride;   /* bytes */
+    const float *scale;             /* device fp32 [num_experts][d_out], contiguous */
+    const float *bias;              /* device fp32 likewise, or NULL */
+    int64_t d_in, d_out;
+    int32_t num_experts;
+    int32_t reserved;               /* must be 0 */
+} lora_int8_weight;
+
+/* Device workspace of lora_int8_matmul for num_rows rows of y (a larger call's serves a
+ * smaller one). */
+lora_status lora_int8_matmul_workspace_bytes(int64_t num_rows, const lora_int8_weight *w,
+                                             size_t *bytes);
+
+/* y[i][n] = x_scale[r] * scale[e][n] * sum_k x[r][k] * w[e][n][k] (+ bias[e][n]): the sum
+ * exact, its scaling in fp32, y rounded once.
+ *   meta          NULL: a dense layer (num_experts = 1): r = i, e = 0.  Else metadata of
+ *                 num_rows rows and num_experts keys: e is row i's key, r = i /
+ *                 x_row_div, and rows without a key are not read or written.
+ *                 lora_prepare_moe_meta with one slot, every token in it, groups the
+ *                 (token, choice) pairs by expert
+ *   d_x           device int8 [num_rows / x_row_div][ldx], values in [-128, 127]
+ *   d_x_scale     device fp32, one for each row of x
+ *   d_y           device [num_rows][ldy] of dtype (fp32 or bf16), d_out columns
+ * ldx is a multiple of 16, ldy of 8; x and y are 16-byte aligned.  num_rows is at most
+ * 2^24. */
+lora_status lora_int8_matmul(const lora_meta *meta, const int8_t *d_x, int64_t ldx,
+                             const float *d_x_scale, int64_t num_rows,
+                             const lora_int8_weight *w, void *d_y, int64_t ldy, lora_dtype dtype,
+                             void *d_ws, size_t ws_bytes, void *stream);
+
+/* out[t] = add[t] + sum_j weights[t][j] * y[t * topk + j] over the choices j whose expert is
+ * local (in ascending j, in fp32, rounded once).  The others' rows are not read.
+ *   d_y           device [T * topk][ldy] of dtype (fp32 or bf16), width columns
+ *   d_topk_ids, d_expert_map, num_experts, num_local_experts: as in lora_prepare_moe_meta;
+ *                 ids that count as bad there are not local here
+ *   d_weights     device fp32 [T][topk]
+ *   d_add         device [T][ldadd] of dtype, or NULL (= 0); it may be d_out itself
+ *   d_out         device [T][ldout] of dtype
+ * width is a multiple of 8, row strides are multiples of 8, matrices 16-byte aligned;
+ * topk at most 64.  d_out overlaps nothing else. */
+lora_status lora_moe_combine(const void *d_y, int64_t ldy, int64_t width, lora_dtype dtype,
+                             const int32_t *d_topk_ids, const float *d_weights,
+                             int64_t num_tokens, int32_t topk, int32_t num_experts,
+                             int32_t num_local_experts, const int32_t *d_expert_map,
+                             const void *d_add, int64_t ldadd, void *d_out, int64_t ldout,
+                             void *stream);
 
 /* Human-readable name of a status code (static storage). */
 const char *lora_status_string(lora_status status);

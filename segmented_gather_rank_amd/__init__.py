@@ -86,6 +86,18 @@ class lora_attn_meta(C.Structure):
                 ("tile_items", C.c_void_p), ("join", C.c_void_p), ("join_list", C.c_void_p)]
 
 
+class lora_routing(C.Structure):
+    _fields_ = [("num_experts", C.c_int32), ("topk", C.c_int32), ("score", C.c_int32), ("num_groups", C.c_int32),
+                ("topk_groups", C.c_int32), ("group_top", C.c_int32), ("renormalize", C.c_int32), ("scale", C.c_float),
+                ("d_bias", C.c_void_p)]
+
+
+class lora_int8_weight(C.Structure):
+    _fields_ = [("ptr", C.c_void_p), ("expert_stride", C.c_int64), ("row_stride", C.c_int64), ("scale", C.c_void_p),
+                ("bias", C.c_void_p), ("d_in", C.c_int64), ("d_out", C.c_int64), ("num_experts", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
 _p, _i32, _i64, _sz = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t
 _decl = {
     "lora_abi_version": ([], _i32),
@@ -117,6 +129,12 @@ _decl = {
     "lora_attention_workspace_bytes": ([C.POINTER(lora_attn_meta), C.POINTER(_sz)], _i32),
     "lora_attention": ([C.POINTER(lora_attn_meta), _p, _i64, C.POINTER(lora_kv_cache), C.c_float, C.c_float, _p,
                         _p, _i64, _p, _p, _sz, _p], _i32),
+    "lora_moe_route": ([C.POINTER(lora_routing), _p, _i64, _i64, _i32, _p, _p, _p], _i32),
+    "lora_quantize": ([_p, _i64, _i64, _i64, _i32, _i32, C.POINTER(lora_meta), _p, _i64, _p, _p, _i64, _p], _i32),
+    "lora_int8_matmul_workspace_bytes": ([_i64, C.POINTER(lora_int8_weight), C.POINTER(_sz)], _i32),
+    "lora_int8_matmul": ([C.POINTER(lora_meta), _p, _i64, _p, _i64, C.POINTER(lora_int8_weight), _p, _i64, _i32, _p,
+                          _sz, _p], _i32),
+    "lora_moe_combine": ([_p, _i64, _i64, _i32, _p, _p, _i64, _i32, _i32, _i32, _p, _p, _i64, _p, _i64, _p], _i32),
 }
 
 
@@ -736,7 +754,206 @@ def lora_attention(meta: AttnMeta, q: torch.Tensor, cache: KvCache, out: torch.T
     return out if lse is None else (out, lse)
 
 
-__all__ = ["KvCache", "Rotation", "AttnMeta", "lora_cache_append", "lora_prepare_attn_meta",
+SCORES = {"softmax": 0, "sigmoid": 1}
+ACTIVATIONS = {None: 0, "silu_mul": 1}
+
+
+def _together(device, **tensors) -> None:
+    """Every tensor that is given lies on `device`."""
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _at(device):
+    """The device of a call's tensors made current: launches go to the current one."""
+    if device.type != "cuda" or device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(device)
+
+
+def _rows(t: torch.Tensor, name: str, dtype, rows: int | None = None, cols: int | None = None) -> tuple:
+    """Address and row stride of a matrix of `rows` rows of at least `cols` columns."""
+    if t.dim() != 2 or t.dtype != dtype or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix of {dtype} with unit column stride")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
+    # the stride of a single row says nothing
+    return (_dev(t, name) if t.numel() else None), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+
+
+def _vector(t: torch.Tensor, name: str, dtype, shape) -> int | None:
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} of {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
+    return _dev(t, name) if t.numel() else None
+
+
+class Routing:
+    """How a router's logits become expert choices (see ``lora_routing`` in the C
+    header).  bias: float32 [experts], decides but does not weigh."""
+
+    def __init__(self, num_experts: int, topk: int, score: str = "softmax", bias: torch.Tensor | None = None,
+                 num_groups: int = 1, topk_groups: int = 1, group_top: int = 2, renormalize: bool = True,
+                 scale: float = 1.0):
+        if score not in SCORES:
+            raise ValueError(f"score must be one of {sorted(SCORES)}")
+        self.num_experts, self.topk, self.bias = int(num_experts), int(topk), bias
+        self.c = lora_routing(self.num_experts, self.topk, SCORES[score], num_groups, topk_groups, group_top,
+                              int(bool(renormalize)), float(scale),
+                              None if bias is None else _vector(bias, "bias", torch.float32, (self.num_experts,)))
+        self.ref = C.byref(self.c)
+
+
+def lora_moe_route(logits: torch.Tensor, routing: Routing, topk_ids: torch.Tensor | None = None,
+                   weights: torch.Tensor | None = None, stream=None):
+    """Expert choices of every token: logits [T][experts] (float32 or bfloat16, rows of
+    any stride) -> topk_ids int32 [T][topk], as lora_prepare_moe_meta takes them, and
+    weights float32 [T][topk]; outputs that are not given are allocated on the stream of
+    the call."""
+    if logits.dim() != 2 or logits.shape[1] != routing.num_experts or (routing.num_experts > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [T][experts] with unit column stride")
+    T, K, device = logits.shape[0], routing.topk, logits.device
+    _together(device, bias=routing.bias, topk_ids=topk_ids, weights=weights)
+    with _at(device):
+        if topk_ids is None:
+            topk_ids = _empty_for(stream, (T, K), torch.int32, device)
+        if weights is None:
+            weights = _empty_for(stream, (T, K), torch.float32, device)
+        st = _lib.lora_moe_route(routing.ref, _dev(logits, "logits") if T else None,
+                                 logits.stride(0) if T > 1 else routing.num_experts, T, _dtype(logits),
+                                 _vector(topk_ids, "topk_ids", torch.int32, (T, K)),
+                                 _vector(weights, "weights", torch.float32, (T, K)), _stream_handle(stream))
+    _check("lora_moe_route", st)
+    return topk_ids, weights
+
+
+def lora_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None,
+                  activation: str | None = None, act: torch.Tensor | None = None, meta: LoraMeta | None = None,
+                  stream=None):
+    """Rows of x [rows][width] as 8-bit integers q and a scale each (q * scale is near x).
+    activation "silu_mul": x is gate | up and silu(gate) * up is what is rounded, which
+    act, if given, takes in x's type.  meta: only the rows that it gives a key.  q and
+    scale that are not given are allocated on the stream of the call (with meta, rows
+    without a key hold anything)."""
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}")
+    xp, ldx = _rows(x, "x", x.dtype)
+    rows, width = x.shape
+    if activation:
+        if width % 2:
+            raise ValueError("x must be gate | up, of one width")
+        width //= 2
+    elif act is not None:
+        raise ValueError("act goes with an activation")
+    _together(x.device, q=q, scale=scale, act=act, meta=None if meta is None else meta.workspace)
+    with _at(x.device):
+        if q is None:
+            q = _empty_for(stream, (rows, width), torch.int8, x.device)
+        if scale is None:
+            scale = _empty_for(stream, (rows,), torch.float32, x.device)
+        qp, ldq = _rows(q, "q", torch.int8, rows, width)
+        ap, lda = (None, 0) if act is None else _rows(act, "act", x.dtype, rows, width)
+        st = _lib.lora_quantize(xp, ldx, rows, width, _dtype(x), ACTIVATIONS[activation],
+                                None if meta is None else C.byref(meta.c), qp, ldq,
+                                _vector(scale, "scale", torch.float32, (rows,)), ap, lda, _stream_handle(stream))
+    _check("lora_quantize", st)
+    return q, scale
+
+
+class Int8Weight:
+    """8-bit base weights: w int8 [d_out][d_in], or [experts][d_out][d_in] (rows and
+    experts of any stride, bytes of a row contiguous), scale float32 [d_out] or
+    [experts][d_out], bias likewise or None."""
+
+    def __init__(self, w: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor | None = None):
+        if w.dim() not in (2, 3) or w.dtype != torch.int8 or w.stride(-1) != 1:
+            raise ValueError("w must be int8 [d_out][d_in] or [experts][d_out][d_in] with contiguous rows")
+        shape = w.shape[:-1]
+        _together(w.device, scale=scale, bias=bias)
+        self.w, self.scale, self.bias = w, scale, bias
+        self.num_experts, self.d_out, self.d_in = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2], w.shape[-1]
+        self.c = lora_int8_weight(_dev(w, "w"), w.stride(0) if w.dim() == 3 and len(w) > 1 else 0,
+                                  w.stride(-2) if self.d_out > 1 else self.d_in,
+                                  _vector(scale, "scale", torch.float32, shape),
+                                  None if bias is None else _vector(bias, "bias", torch.float32, shape), self.d_in,
+                                  self.d_out, self.num_experts, 0)
+        self.ref = C.byref(self.c)
+
+
+def lora_int8_matmul_workspace_bytes(num_rows: int, weight: Int8Weight) -> int:
+    b = _sz(0)
+    _check("lora_int8_matmul_workspace_bytes", _lib.lora_int8_matmul_workspace_bytes(num_rows, weight.ref, C.byref(b)))
+    return int(b.value)
+
+
+def lora_int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, weight: Int8Weight, out: torch.Tensor | None = None,
+                     meta: LoraMeta | None = None, dtype: torch.dtype = torch.bfloat16,
+                     workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[i] = (x[i] @ w.T) * x_scale[i] * w_scale (+ bias), x int8 [rows][d_in] as
+    lora_quantize leaves it.  meta: metadata of the output's rows, keyed by expert (row i
+    of the output reads row i / x_row_div of x; rows without a key are not written).  An
+    out that is not given is allocated on the stream of the call, of type dtype."""
+    xp, ldx = _rows(x, "x", torch.int8, None, weight.d_in)
+    div = 1 if meta is None else int(meta.c.x_row_div)
+    rows = x.shape[0] if meta is None else meta.num_tokens
+    if x.shape[0] != -(-rows // div):
+        raise ValueError(f"x must have {-(-rows // div)} rows, one for {div} of the metadata's")
+    device = x.device
+    _together(device, x_scale=x_scale, w=weight.w, out=out, workspace=workspace,
+              meta=None if meta is None else meta.workspace)
+    with _at(device):
+        if out is None:
+            out = _empty_for(stream, (rows, weight.d_out), dtype, device)
+        yp, ldy = _rows(out, "out", out.dtype, rows, weight.d_out)
+        need = lora_int8_matmul_workspace_bytes(rows, weight)
+        if workspace is None and need:
+            workspace = _empty_for(stream, need, torch.uint8, device)
+        st = _lib.lora_int8_matmul(None if meta is None else C.byref(meta.c), xp, ldx,
+                                   _vector(x_scale, "x_scale", torch.float32, (x.shape[0],)), rows, weight.ref, yp, ldy,
+                                   _dtype(out), None if workspace is None else _dev(workspace, "workspace"),
+                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                   _stream_handle(stream))
+    _check("lora_int8_matmul", st)
+    return out
+
+
+def lora_moe_combine(y: torch.Tensor, weights: torch.Tensor, topk_ids: torch.Tensor, out: torch.Tensor | None = None,
+                     num_experts: int | None = None, num_local_experts: int | None = None,
+                     expert_map: torch.Tensor | None = None, add: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """out[t] = add[t] + sum of weights[t][j] * y[t * topk + j] over the choices whose
+    expert is local (as in lora_prepare_moe_meta; without a map ids below
+    num_local_experts, by default all).  add may be out itself."""
+    if topk_ids.dim() != 2:
+        raise ValueError("topk_ids must be [T][topk]")
+    T, K = topk_ids.shape
+    yp, ldy = _rows(y, "y", y.dtype, T * K)
+    width, device = y.shape[1], y.device
+    if expert_map is not None:
+        if num_local_experts is None:
+            raise ValueError("an expert_map needs num_local_experts")
+        if num_experts is None:
+            num_experts = expert_map.shape[0]
+    if num_experts is None:
+        num_experts = num_local_experts if num_local_experts is not None else 0x7fffffff
+    if num_local_experts is None:
+        num_local_experts = num_experts
+    _together(device, weights=weights, topk_ids=topk_ids, out=out, expert_map=expert_map, add=add)
+    with _at(device):
+        if out is None:
+            out = _empty_for(stream, (T, width), y.dtype, device)
+        op, ldout = _rows(out, "out", y.dtype, T, width)
+        ap, ldadd = (None, 0) if add is None else _rows(add, "add", y.dtype, T, width)
+        st = _lib.lora_moe_combine(
+            yp, ldy, width, _dtype(y), _vector(topk_ids, "topk_ids", torch.int32, (T, K)),
+            _vector(weights, "weights", torch.float32, (T, K)), T, K, num_experts, num_local_experts,
+            None if expert_map is None else _vector(expert_map, "expert_map", torch.int32, (num_experts,)), ap, ldadd,
+            op, ldout, _stream_handle(stream))
+    _check("lora_moe_combine", st)
+    return out
+
+
+__all__ = ["Routing", "Int8Weight", "lora_moe_route", "lora_quantize", "lora_int8_matmul",
+           "lora_int8_matmul_workspace_bytes", "lora_moe_combine", "lora_routing", "lora_int8_weight", "KvCache", "Rotation", "AttnMeta", "lora_cache_append", "lora_prepare_attn_meta",
            "lora_attn_meta_workspace_bytes", "lora_attention", "lora_attention_workspace_bytes", "lora_kv_cache",
            "lora_rotation", "lora_attn_batch", "lora_attn_meta", "LORA_E4M3",
            "lora_apply_noalloc", "NOALLOC_SCRATCH_BYTES", "lora_abi_version", "lora_status_string", "lora_meta_workspace_bytes", "lora_prepare_meta",
