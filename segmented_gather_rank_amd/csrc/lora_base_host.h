@@ -42,6 +42,8 @@ struct Int8Args {
   MetaView meta;                 // sorted == NULL: dense
 };
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s);
+// Rows in tiles through LDS; with metadata, the segments of at least `fewest` rows.
+hipError_t launch_int8_tile(const Int8Args &a, bool bf16, int fewest, hipStream_t s);
 
 struct CombineArgs {
   const char *y, *add;           // add: NULL or rows

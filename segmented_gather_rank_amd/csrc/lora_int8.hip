@@ -18,6 +18,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
+constexpr int kFewRows = 64;  // most rows of a segment (or a dense batch) that few_kernel takes
 constexpr int kStep = 128;  // bytes of d_in a step takes: two matrix instructions
 
 // The rows that a workgroup works on: a segment of the metadata, or all.
@@ -146,14 +147,14 @@ __device__ __forceinline__ void few_block(const Int8Args &a, const Rows &rows, i
 }
 
 template <typename Y, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void few_kernel(Int8Args a, int group0) {
+__global__ __launch_bounds__(64 * WAVES) void few_kernel(Int8Args a, int group0, int most) {
   __shared__ i32x4 lds[4 * NT * WAVES * 64];
   const int n0 = blockIdx.x * 16 * NT;
   Rows rows{nullptr, (int)a.rows, 0, 1};
   int r0 = 0, end = rows.count;
   if (a.meta.sorted) {
     rows = segment(a, group0 + blockIdx.y);
-    end = rows.count;
+    end = rows.count <= most ? rows.count : 0;
   } else {
     r0 = (group0 + blockIdx.y) * 64;
     end = min(end, r0 + 64);
@@ -165,16 +166,17 @@ __global__ __launch_bounds__(64 * WAVES) void few_kernel(Int8Args a, int group0)
   }
 }
 
+// With metadata, the segments of at most `most` rows.
 template <typename Y>
-hipError_t launch_for(const Int8Args &a, hipStream_t s) {
+hipError_t launch_few(const Int8Args &a, int most, hipStream_t s) {
   const int64_t groups = a.meta.sorted ? std::min<int64_t>(a.rows, a.experts) + 1 : (a.rows + 63) / 64;
   constexpr int kNT = 2, kWaves = 8;
   const int64_t cols = (a.d_out + 16 * kNT - 1) / (16 * kNT);
   // a launch holds fewer than 2^32 threads, and 2^16 rows of its grid
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>(32768, ((int64_t)1 << 22) / cols));
-  for (int64_t g0 = 0; g0 < groups; g0 += most) {
-    const dim3 grid((unsigned)cols, (unsigned)std::min(groups - g0, most));
-    few_kernel<Y, kNT, kWaves><<<grid, dim3(64 * kWaves), 0, s>>>(a, (int)g0);
+  const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(32768, ((int64_t)1 << 22) / cols));
+  for (int64_t g0 = 0; g0 < groups; g0 += rows) {
+    const dim3 grid((unsigned)cols, (unsigned)std::min(groups - g0, rows));
+    few_kernel<Y, kNT, kWaves><<<grid, dim3(64 * kWaves), 0, s>>>(a, (int)g0, most);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -184,7 +186,15 @@ hipError_t launch_for(const Int8Args &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s) {
-  return bf16 ? launch_for<uint16_t>(a, s) : launch_for<float>(a, s);
+  // tiles address x in 32 bits: all of it where rows are gathered, 256 rows else
+  const int64_t x_rows = a.meta.sorted ? (a.rows - 1) / a.meta.x_row_div + 1 : 256;
+  const bool tiles = a.rows > kFewRows && x_rows * a.ldx < ((int64_t)1 << 32);
+  const int most = tiles ? kFewRows : INT32_MAX;
+  if (a.meta.sorted || !tiles) {
+    const hipError_t err = bf16 ? launch_few<uint16_t>(a, most, s) : launch_few<float>(a, most, s);
+    if (err != hipSuccess) return err;
+  }
+  return tiles ? launch_int8_tile(a, bf16, kFewRows + 1, s) : hipSuccess;
 }
 
 }  // namespace lora

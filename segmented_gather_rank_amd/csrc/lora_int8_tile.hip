@@ -1,0 +1,360 @@
+// lora_int8_tile.hip -- 8-bit products of many rows: tiles of rows and columns, whose
+// operands go through LDS.
+#include <algorithm>
+
+#include "lora_base_host.h"
+
+namespace lora {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
+
+constexpr int kDepth = 128;  // bytes of d_in a stage holds of every row
+constexpr int kPieces = kDepth / 16;
+
+// What a lane past the end of d_in reads instead: zeros on x's side are enough.
+__device__ const u32x4 zero_piece = {0, 0, 0, 0};
+
+struct Tile {
+  int expert, n0, m0, count, start;  // rows m0 .. of a segment of `count` rows from `start` in `sorted`
+};
+
+// Tile i of a rows x cols grid, taken `kBand` row tiles at a time, so that what is in
+// work at once reads few different rows of either operand.
+constexpr int kBand = 4;
+__device__ __forceinline__ void place(int i, int row_tiles, int col_tiles, int &m, int &n) {
+  const int band = i / (kBand * col_tiles), in = i - band * kBand * col_tiles;
+  const int high = min(kBand, row_tiles - band * kBand);
+  n = in / high;
+  m = band * kBand + in - n * high;
+}
+
+__device__ __forceinline__ void to_lds(const int8_t *from, u32x4 *to) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
+                                   (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+}
+
+// LDS written by this wave is read by this wave.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Instruction kinds of __builtin_amdgcn_sched_group_barrier.
+constexpr int kSchedMfma = 0x8, kSchedVmem = 0x20, kSchedDsRead = 0x100;
+
+template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewest) {
+  constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;          // blocks of 32 of a wave
+  constexpr int XQ = BM / 8 / kWaves, WQ = BN / 8 / kWaves;    // transfers of 8 rows of a wave and stage
+  __shared__ u32x4 buf0[(BM + BN) * kPieces], buf1[(BM + BN) * kPieces];
+  __shared__ int32_t ids[2][GROUPED ? BM : 1];
+  __shared__ __align__(16) float columns[kWaves][2][TN * 32];
+  extern __shared__ __align__(16) char table[];
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l32 = lane % 32, half = lane / 32;
+  const int col_tiles = (a.d_out + BN - 1) / BN;
+  const SegTable tb = seg_table_at(table, a.experts);
+  int tiles;
+  if constexpr (GROUPED) {
+    build_items(a.meta, tb, true, [&](int count, int) { return count >= fewest ? (count + BM - 1) / BM * col_tiles : 0; });
+    tiles = uniform_value(tb.scal[2]);
+  } else {
+    tiles = (int)((a.rows + BM - 1) / BM) * col_tiles;
+  }
+  // every XCD takes a run of neighbouring tiles
+  const int share = (tiles + 7) / 8, per = gridDim.x / 8;
+  const int last = min(tiles, (int)(blockIdx.x % 8 + 1) * share);
+  int index = blockIdx.x % 8 * share + blockIdx.x / 8;
+  if (index >= last) return;
+
+  auto tile_at = [&](int i) {
+    Tile t;
+    int m, n;
+    if constexpr (GROUPED) {
+      const int s = find_item_segment(tb, i), at = tb.scal[1] + s;
+      t.expert = uniform_value(tb.slot[at]);
+      t.count = uniform_value(tb.count[at]);
+      t.start = uniform_value(tb.start[at]);
+      const int from = s ? tb.item_end[s - 1] : 0;
+      place(uniform_value(i - from), (t.count + BM - 1) / BM, col_tiles, m, n);
+    } else {
+      t.expert = t.start = 0;
+      t.count = (int)a.rows;
+      place(i, (t.count + BM - 1) / BM, col_tiles, m, n);
+    }
+    t.m0 = m * BM;
+    t.n0 = n * BN;
+    return t;
+  };
+
+  // ---- transfers of the tile that `aim` was called for
+  const int8_t *xb = a.x, *wb = a.w;              // where its rows of either operand are counted from
+  uint32_t xo[XQ], wo[WQ];                        // bytes from there to the piece of its row that a lane transfers
+  const int piece = (lane % 8) ^ (lane / 8);
+  constexpr int kIds = (BM + kThreads - 1) / kThreads;
+  int32_t pending[kIds];
+  auto fetch_ids = [&](const Tile &t) {
+    if constexpr (GROUPED) {
+#pragma unroll
+      for (int q = 0; q < kIds; ++q)
+        pending[q] = a.meta.sorted[t.start + min(t.m0 + q * kThreads + (int)threadIdx.x, t.count - 1)];
+    }
+  };
+  auto keep_ids = [&](int slot) {
+    if constexpr (GROUPED) {
+#pragma unroll
+      for (int q = 0; q < kIds; ++q)
+        if (q * kThreads + (int)threadIdx.x < BM) ids[slot][q * kThreads + threadIdx.x] = pending[q];
+    }
+  };
+  auto aim = [&](const Tile &t, int slot) {
+    if constexpr (!GROUPED) xb = a.x + (int64_t)t.m0 * a.ldx;
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) {
+      const int r = (q * kWaves + wave) * 8 + lane / 8;
+      uint32_t row;
+      if constexpr (GROUPED) {
+        row = (uint32_t)ids[slot][r];
+        if (a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
+      } else {
+        row = (uint32_t)min(r, t.count - 1 - t.m0);
+      }
+      xo[q] = row * (uint32_t)a.ldx + 16 * piece;
+    }
+    wb = a.w + t.expert * a.expert_stride + t.n0 * a.row_stride;
+#pragma unroll
+    for (int q = 0; q < WQ; ++q)
+      wo[q] = (uint32_t)min((q * kWaves + wave) * 8 + lane / 8, a.d_out - 1 - t.n0) * (uint32_t)a.row_stride + 16 * piece;
+  };
+  auto transfer = [&](u32x4 *buf, int k) {
+    // hidden from the optimiser, which would keep a 64-bit address for every transfer
+    asm volatile("" : "+s"(k));
+    const int8_t *xk = xb + k, *wk = wb + k;
+#pragma unroll
+    for (int q = 0; q < XQ; ++q) to_lds(xk + xo[q], buf + (q * kWaves + wave) * 64);
+#pragma unroll
+    for (int q = 0; q < WQ; ++q) to_lds(wk + wo[q], buf + BM * kPieces + (q * kWaves + wave) * 64);
+  };
+  // the same where d_in may end: lanes past the end take zeros for x, and for w stay inside the row
+  auto transfer_end = [&](u32x4 *buf, int k) {
+    const bool in = k + 16 * piece < a.d_in;
+#pragma unroll
+    for (int q = 0; q < XQ; ++q)
+      to_lds(in ? xb + k + xo[q] : reinterpret_cast<const int8_t *>(&zero_piece), buf + (q * kWaves + wave) * 64);
+#pragma unroll
+    for (int q = 0; q < WQ; ++q)
+      to_lds(wb + (in ? k : -16 * piece) + wo[q], buf + BM * kPieces + (q * kWaves + wave) * 64);
+  };
+
+  // ---- products
+  i32x16 sum[TM][TN];
+  i32x4 xv[2][TM], wv[2][TN];
+  // a row's piece p lies at place p ^ (row % 8) of its 8: 8 neighbouring rows' pieces fill the banks
+  const int xr = (wm * TM * 32 + l32) * kPieces + (half ^ (lane % 8));
+  const int wr = (BM + wn * TN * 32 + l32) * kPieces + (half ^ (lane % 8));
+  auto read = [&](const u32x4 *buf, int phase, int set) {
+#pragma unroll
+    for (int n = 0; n < TN; ++n)
+      wv[set][n] = __builtin_bit_cast(i32x4, buf[(wr ^ (2 * phase)) + n * 32 * kPieces]);
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+      xv[set][m] = __builtin_bit_cast(i32x4, buf[(xr ^ (2 * phase)) + m * 32 * kPieces]);
+  };
+  auto multiply = [&](int set) {
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+        sum[m][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][n], xv[set][m], sum[m][n], 0, 0, 0);
+  };
+  // The order of a quarter: its reads, and its transfers, between the products.
+  constexpr int kReads = TM + TN, kProducts = TM * TN;
+  auto spread_reads = [&]() {
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+      if (i < kReads) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+    }
+  };
+  auto spread_transfers = [&]() {
+#pragma unroll
+    for (int i = 0; i < kProducts; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+      if (i < kReads) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
+      if (i < XQ + WQ) __builtin_amdgcn_sched_group_barrier(kSchedVmem, 1, 0);
+    }
+  };
+  // the first three quarters of a stage; the last one's operands are in registers then, so
+  // that the transfers of the stage after the next may overwrite it
+  auto three_quarters = [&](const u32x4 *here) {
+    read(here, 1, 1);
+    multiply(0);
+    spread_reads();
+    read(here, 2, 0);
+    multiply(1);
+    spread_reads();
+    read(here, 3, 1);
+    multiply(0);
+    spread_reads();
+  };
+  auto stage = [&](u32x4 *here, const u32x4 *next, int k) {
+    three_quarters(here);
+    __builtin_amdgcn_sched_barrier(0);
+    __syncthreads();
+    read(next, 0, 0);
+    transfer(here, k + 2 * kDepth);
+    multiply(1);
+    spread_transfers();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  const int stages = (a.d_in + kDepth - 1) / kDepth, whole = a.d_in / kDepth;
+  // a stage that may be among a tile's last ones
+  auto stage_end = [&](u32x4 *here, const u32x4 *next, int s) {
+    three_quarters(here);
+    if (s + 1 < stages) {
+      __syncthreads();
+      if (s + 2 < stages) transfer_end(here, (s + 2) * kDepth);
+      read(next, 0, 0);
+    }
+    multiply(1);
+  };
+
+  // ---- y of the finished tile, through LDS so that whole lines are stored
+  auto finish = [&](const Tile &t, int slot, u32x4 *scratch) {
+    constexpr int kRowPieces = TN * 32 * (int)sizeof(Y) / 16;
+    u32x4 *mine = scratch + wave * 32 * kRowPieces;
+    const int c0 = t.n0 + wn * TN * 32;
+    // the wave's columns' scales and bias: fetched once, read from LDS as they are needed
+    float *ws = columns[wave][0], *bs = columns[wave][1];
+#pragma unroll
+    for (int c = lane; c < TN * 32; c += 64) {
+      const int64_t at = (int64_t)t.expert * a.d_out + min(c0 + c, a.d_out - 1);
+      ws[c] = a.w_scale[at];
+      bs[c] = a.bias ? a.bias[at] : 0.f;
+    }
+    wave_sync();
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      const int r = (wm * TM + m) * 32;           // of the tile
+      uint32_t row = (uint32_t)min(t.m0 + r + l32, t.count - 1);
+      if constexpr (GROUPED) {
+        row = (uint32_t)ids[slot][r + l32];
+        if (a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
+      }
+      const float xs = a.x_scale[row];
+#pragma unroll
+      for (int n = 0; n < TN; ++n)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          // columns 32 n + 8 g + 4 half .. + 3 of row l32
+          const f32x4 w4 = *reinterpret_cast<const f32x4 *>(ws + 32 * n + 8 * g + 4 * half);
+          const f32x4 b4 = *reinterpret_cast<const f32x4 *>(bs + 32 * n + 8 * g + 4 * half);
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = (float)sum[m][n][4 * g + e] * (xs * w4[e]) + b4[e];
+          // the pieces of a row change places by its number: neither these writes nor the reads below meet in a bank
+          if constexpr (sizeof(Y) == 2) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            u32x2 *to = reinterpret_cast<u32x2 *>(mine + l32 * kRowPieces + ((4 * n + g) ^ (l32 % kRowPieces)));
+            to[half] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          } else {
+            mine[l32 * kRowPieces + ((8 * n + 2 * g + half) ^ (l32 % kRowPieces))] =
+                __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+          }
+        }
+      wave_sync();
+      constexpr int kRowsAtOnce = 64 / kRowPieces;
+#pragma unroll
+      for (int q = 0; q < 32 / kRowsAtOnce; ++q) {
+        const int lr = q * kRowsAtOnce + lane / kRowPieces, p = lane % kRowPieces;
+        const u32x4 v = mine[lr * kRowPieces + (p ^ (lr % kRowPieces))];
+        const int c = c0 + p * (16 / (int)sizeof(Y));
+        if (t.m0 + r + lr < t.count && c < a.d_out) {
+          int64_t to = t.m0 + r + lr;
+          if constexpr (GROUPED) to = (uint32_t)ids[slot][r + lr];
+          gstore16(a.y + (to * a.ldy + c) * (int64_t)sizeof(Y), v);
+        }
+      }
+      wave_sync();
+    }
+  };
+
+  Tile now = tile_at(index), then;
+  int slot = 0;
+  if constexpr (GROUPED) {
+    fetch_ids(now);
+    keep_ids(0);
+    __syncthreads();
+  }
+  aim(now, 0);
+  transfer_end(buf0, 0);
+  while (true) {
+    const bool follows = index + per < last;
+    if (follows) {
+      then = tile_at(index + per);
+      fetch_ids(then);
+    }
+    __syncthreads();  // the first stage is there, and the last tile's scratch is free
+    if (follows) keep_ids(slot ^ 1);
+    if (stages > 1) transfer_end(buf1, kDepth);
+#pragma unroll
+    for (int m = 0; m < TM; ++m)
+#pragma unroll
+      for (int n = 0; n < TN; ++n) sum[m][n] = i32x16{};
+    read(buf0, 0, 0);
+    int s = 0;
+    for (; s + 3 < whole; s += 2) {
+      stage(buf0, buf1, s * kDepth);
+      stage(buf1, buf0, (s + 1) * kDepth);
+    }
+    while (true) {
+      stage_end(buf0, buf1, s);
+      if (++s == stages) break;
+      stage_end(buf1, buf0, s);
+      if (++s == stages) break;
+    }
+    __syncthreads();  // every wave has read its last stage
+    // the next tile's first stage arrives while this one's results leave
+    if (follows) {
+      aim(then, slot ^ 1);
+      transfer_end(buf0, 0);
+    }
+    finish(now, slot, buf1);
+    if (!follows) return;
+    now = then;
+    slot ^= 1;
+    index += per;
+  }
+}
+
+template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
+hipError_t launch_as(const Int8Args &a, int fewest, hipStream_t s) {
+  static std::atomic<int> cache[kMaxDevices];
+  // the table's size only matters where it costs a workgroup its place: sized for the most
+  const size_t lds = GROUPED ? seg_table_bytes(a.experts) : 0;
+  const void *f = reinterpret_cast<const void *>(&tile_kernel<Y, GROUPED, BM, BN, WM, WN>);
+  const int64_t cols = (a.d_out + BN - 1) / BN;
+  const int64_t bound = ((a.rows + BM - 1) / BM + (GROUPED ? std::min<int64_t>(a.experts, a.rows) : 0)) * cols;
+  const int grid = xcd_grid(bound, resident_groups(cache, f, 64 * WM * WN, lds));
+  tile_kernel<Y, GROUPED, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), lds, s>>>(a, fewest);
+  return hipGetLastError();
+}
+
+template <typename Y>
+hipError_t launch_for(const Int8Args &a, int fewest, hipStream_t s) {
+  if (a.meta.sorted) return launch_as<Y, true, 256, 256, 2, 4>(a, fewest, s);
+  return launch_as<Y, false, 256, 256, 2, 4>(a, fewest, s);
+}
+
+}  // namespace
+
+hipError_t launch_int8_tile(const Int8Args &a, bool bf16, int fewest, hipStream_t s) {
+  return bf16 ? launch_for<uint16_t>(a, fewest, s) : launch_for<float>(a, fewest, s);
+}
+
+}  // namespace lora
