@@ -18,6 +18,7 @@ struct RouteArgs {
   float *weights;
   float scale;
   int32_t experts, topk, sigmoid, groups, kept, group_top, renorm, aligned;
+  int32_t group_lanes;           // set by the launcher: lanes of a group, 0 where groups are not whole lanes
 };
 hipError_t launch_route(const RouteArgs &a, bool bf16, hipStream_t s);
 

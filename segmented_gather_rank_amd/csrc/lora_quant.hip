@@ -40,10 +40,15 @@ __device__ __forceinline__ uint32_t wave_most(uint32_t v) {
   return max(b[0], b[1]);
 }
 
-// x / (1 + exp(-x)) * u, from exp(-|x|), which does not overflow
+// x / (1 + exp(-x)) * u.  exp(-|x|), which does not overflow, as the square of its root,
+// which the hardware's exponential does not flush to 0 before the square does; the
+// quotient by the hardware's inverse, corrected once.
 __device__ __forceinline__ float gated(float x, float u) {
-  const float e = expf(-fabsf(x));
-  return x * (x < 0.f ? e : 1.f) / (1.f + e) * u;
+  const float m = fabsf(x);
+  const float z = fmaf(m, -9.6e-9f, m * -0.72134752f);  // -m / (2 ln 2)
+  const float root = __builtin_amdgcn_exp2f(z), e = root * root;
+  const float d = 1.f + e, r = __builtin_amdgcn_rcpf(d);
+  return x * (x < 0.f ? e : 1.f) * fmaf(fmaf(-d, r, 1.f), r, r) * u;
 }
 
 template <typename X, bool ACT>
@@ -67,18 +72,32 @@ struct Step {
     exact_only = !(by < INFINITY);
   }
   __device__ __forceinline__ float scale() const { return finite ? m / 127.f : __builtin_nanf(""); }
-  __device__ __forceinline__ int nearest(float v) const {
-    if (!finite) return 0;
-    const float t = v * by, n = rintf(t);
-    if (exact_only || fabsf(fabsf(t - n) - 0.5f) < 0x1p-15f) return (int)rint((double)v * 127. / (double)m);
-    return (int)n;
-  }
+  __device__ __forceinline__ int nearest(float v) const { return (int)rint((double)v * 127. / (double)m); }
 };
 
 __device__ __forceinline__ void put(int8_t *q, const Step &s, const float v[8]) {
-  uint32_t w[2] = {0, 0};
+  // adding 1.5 * 2^23 rounds to an integer, which the low bits then hold
+  constexpr float kRound = 12582912.f;
+  float t[8], off = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e / 4] |= ((uint32_t)s.nearest(v[e]) & 0xffu) << (8 * (e % 4));
+  for (int e = 0; e < 8; ++e) {
+    const float p = v[e] * s.by;
+    t[e] = p + kRound;
+    off = fmaxf(off, fabsf(p - (t[e] - kRound)));
+  }
+  uint32_t w[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t lo = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 1]), __float_as_uint(t[4 * h]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(__float_as_uint(t[4 * h + 3]), __float_as_uint(t[4 * h + 2]), 0x04000c0cu);
+    w[h] = lo | hi;
+  }
+  if (s.exact_only || off > 0.5f - 0x1p-15f) {
+    w[0] = w[1] = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e / 4] |= ((uint32_t)s.nearest(v[e]) & 0xffu) << (8 * (e % 4));
+  }
+  if (!s.finite) w[0] = w[1] = 0;
   typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
   typedef __attribute__((address_space(1))) u32x2 g_u32x2;
   *(g_u32x2 *)q = u32x2{w[0], w[1]};

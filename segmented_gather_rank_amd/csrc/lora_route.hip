@@ -1,17 +1,20 @@
 // lora_route.hip -- expert choices from a router's logits.
 //
-// 16 lanes (or a wave, beyond 256 experts) hold a token's values as integers that order
-// like them, PER consecutive experts a lane, so that equal values go to the lowest id by
-// going to the lowest lane.  Each of topk rounds takes the largest: a lane's own by its
-// registers, a token's by rotations inside a row of 16 lanes.
+// 16 lanes hold a token's values (a wave does, beyond 256 experts or 16 choices) as
+// integers that order like them, PER consecutive experts a lane, so that equal values go
+// to the lowest id by going to the lowest lane.
+//
+// 16 lanes: the topk-th largest of the lanes' maxima bounds the choices from below, and
+// few values reach it (8 choices of 256: 12 or so).  They are laid out one a lane, and
+// each counts how many come before it.  A wave, or a token of whose values more than 16
+// reach the bound: topk rounds, each of which takes the largest that is left.
 //
 // What decides a choice is compared exactly.  Without bias (and where a group's rank is
 // its largest value) the logits themselves are ordered.  With it c = s + bias is
 // rounded, and two values that differ in 64 bits may agree or change places in 32: a
-// token whose neighbours in the chosen order (or whose last kept and first dropped
-// group) come within the error bound of each other is done again in 64 bits.  That is
-// one token in some hundred; where all biases are equal and logits repeat (bf16), up to
-// all of them.
+// token whose neighbours in the chosen order (or whose groups' ranks) come within the
+// error bound of each other is done again in 64 bits.  That is one token in some
+// hundred; where all biases are equal and logits repeat (bf16), up to all of them.
 #include <algorithm>
 #include <cmath>
 
@@ -98,8 +101,12 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+// In 32 bits the exponential and the quotient are the hardware's, a step off each: the
+// choice allows for it, and the weights are taken in 64.
+__device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
+__device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ __forceinline__ double inverse(double v) { return 1. / v; }
 
 template <typename X>
 __device__ __forceinline__ float logit_at(const char *row, int e) {
@@ -109,116 +116,169 @@ __device__ __forceinline__ float logit_at(const char *row, int e) {
 
 // ---------------------------------------------------------------- one token
 
-template <int LANES, int PER>
+template <int PER>
 struct Token {
-  float x[PER];                  // logits of experts base .. base + PER - 1; -inf past the last
+  float x[PER], bias[PER];       // of experts base .. base + PER - 1; -inf and 0 past the last
   int base, lane;                // lane of the token's
   float top;                     // largest logit (NaN aside)
 };
 
 // How near two values in 32 bits may be for their order to stand: twice a value's error.
-// s is within (30 + 104) * 2^-24 of its size (the exponential, sums of 16 a lane and of the
-// lanes, the division; then the exponent's argument, rounded, up to where the exponential
-// ends).  With a bias, whose sum adds half a step, the argument's part is at most
-// |z| e^-|z| < 0.4 steps of 1, and s at most 1.
+// s is within 30 * 2^-24 of its size (the exponential, sums of 16 a lane and of the lanes,
+// the quotient) and, by the exponent's argument z and the logarithm's own step, 1.5 |z| *
+// 2^-24, up to |z| = 104 where the exponential ends (below 1e-38 it is 0).  With a bias,
+// whose sum adds half a step, the argument's part is at most |z| e^-|z| < 0.4 steps of 1,
+// and s at most 1.
 __device__ __forceinline__ float near(float v, bool biased) {
-  return biased ? 64.f * 0x1p-24f * (1.f + fabsf(v)) : 320.f * 0x1p-24f * fabsf(v) + 1e-36f;
+  return biased ? 64.f * 0x1p-24f * (1.f + fabsf(v)) : 400.f * 0x1p-24f * fabsf(v) + 1e-36f;
 }
 
-// The chosen experts of the token: lane j % LANES keeps choice j in id[j / LANES].
-// Returns whether 32 bits could not tell (S = double: never).
-template <typename S, int LANES, int PER, int KEEP>
-__device__ __forceinline__ bool choose(const RouteArgs &a, const Token<LANES, PER> &t, S *lds, int id[KEEP]) {
+template <typename S> __device__ __forceinline__ void two_largest(S v, S &first, S &second) {
+  second = larger(second, smaller(first, v));
+  first = larger(first, v);
+}
+
+// The values' own order where nothing is added to them, and c where it is; kGone for
+// experts past the last and in groups that do not stay.  `unsure`: 32 bits could not
+// tell which groups stay.  lds: LANES * PER values and kMaxGroups ranks.
+template <typename S, int LANES, int PER>
+__device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t, S *lds, typename Ordered<S>::key k[PER],
+                                        bool &unsure) {
   typedef Ordered<S> O;
-  typedef typename O::key key;
   constexpr bool kExact = std::is_same<S, double>::value;
-  const bool by_value = a.bias != nullptr || (a.groups > 1 && a.group_top > 1);  // the order needs s
-  bool unsure = false;
-  key k[PER];
-  // the order of experts without bias
+  const bool by_rank = a.groups > 1 && a.group_top > 1, biased = a.bias != nullptr;
+  S c[PER];                      // what groups are ranked by
 #pragma unroll
-  for (int i = 0; i < PER; ++i) k[i] = O::of(t.x[i] == t.x[i] ? (S)t.x[i] : -(S)INFINITY);
-  if (by_value) {
-    S sum = 0;
-    S s[PER];
-    const S top = (S)t.top;
+  for (int i = 0; i < PER; ++i) {
+    c[i] = t.x[i] == t.x[i] ? (S)t.x[i] : -(S)INFINITY;
+    k[i] = O::of(c[i]);
+  }
+  if (biased || by_rank) {       // the order needs s
+    if (a.sigmoid) {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const S x = (S)t.x[i];
-      if (a.sigmoid) {
-        s[i] = (S)1 / ((S)1 + exp_of(-x));
-      } else {
-        s[i] = x == top ? (S)1 : exp_of(x - top);
-        sum += x == x ? s[i] : (S)0;
+      for (int i = 0; i < PER; ++i) c[i] = inverse((S)1 + exp_of(-(S)t.x[i]));
+    } else {
+      S sum = 0;
+      const S top = (S)t.top;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        const S x = (S)t.x[i];
+        c[i] = x == top ? (S)1 : exp_of(x - top);
+        sum += x == x ? c[i] : (S)0;
       }
+      // one lane's sum for all: equal logits have equal scores
+      const S by = __shfl(total<LANES>(sum), 0, LANES);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) c[i] = kExact ? c[i] / by : c[i] * inverse(by);
     }
-    // one lane's sum for all: equal logits have equal scores
-    if (!a.sigmoid) sum = __shfl(total<LANES>(sum), 0, LANES);
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      const int e = t.base + i;
-      S c = a.sigmoid ? s[i] : s[i] / sum;
-      if (a.bias && e < a.experts) c += (S)a.bias[e];
-      // masked, NaN
-      if (!(t.x[i] > -INFINITY) || c != c) c = -(S)INFINITY;
-      if (a.bias) k[i] = O::of(c);
-      if (a.groups > 1) lds[e] = c;
+      if (biased) c[i] += (S)t.bias[i];
+      if (!(t.x[i] > -INFINITY) || c[i] != c[i]) c[i] = -(S)INFINITY;  // masked, NaN
+      if (biased) k[i] = O::of(c[i]);
     }
-  } else if (a.groups > 1) {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) lds[t.base + i] = O::value(k[i]);
   }
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (t.base + i >= a.experts) k[i] = O::kGone;
+  if (a.groups == 1) return;
 
-  if (a.groups > 1) {
-    // ranks: the token's values are in LDS, a group a lane
-    const int size = a.experts / a.groups;
-    S *rank = lds + LANES * PER;
-    wave_sync();
-    for (int g = t.lane; g < a.groups; g += LANES) {
-      S first = -(S)INFINITY, second = -(S)INFINITY;
-      for (int i = 0; i < size; ++i) {
-        const S v = lds[g * size + i];
-        second = larger(second, smaller(first, v));
-        first = larger(first, v);
-      }
-      rank[g] = a.group_top > 1 ? first + second : first;
-    }
-    wave_sync();
-    // a group stays if fewer than `kept` come before it
-    uint64_t stays = 0;
-    for (int g = t.lane; g < a.groups; g += LANES) {
-      const S mine = rank[g];
-      int before = 0;
-      for (int f = 0; f < a.groups; ++f) {
-        const S v = rank[f];
-        before += v > mine || (v == mine && f < g);
-        if constexpr (!kExact) {
-          // the ranks around the border only matter, but ranks this near are rare enough
-          if (by_value && f != g && v > -INFINITY && fabsf(v - mine) <= 2.f * near(mine, a.bias != nullptr)) unsure = true;
-        }
-      }
-      if (before < a.kept) stays |= 1ull << g;
-    }
-    wave_sync();
-    stays = fold<LANES>((int64_t)stays, [](int64_t p, int64_t q) { return p | q; });
-    int g = t.base / size, left = (g + 1) * size - t.base;  // experts of group g from this one on
+  const int size = a.experts / a.groups;
+  // ranks this near may stand the other way round in 64 bits; only those around the border matter, but such pairs are rare
+  auto too_near = [&](S v, S mine) {
+    if constexpr (kExact) return false;
+    else return (biased || by_rank) && v > -INFINITY && fabsf(v - mine) <= 2.f * near(mine, biased);
+  };
+  if (LANES == 16 && a.group_lanes) {
+    // a group is `group_lanes` neighbouring lanes, a power of two
+    S first = -(S)INFINITY, second = -(S)INFINITY;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      if (g < a.groups && !((uint64_t)stays >> g & 1)) k[i] = O::kGone;
-      if (--left == 0) {
-        ++g;
-        left = size;
-      }
+    for (int i = 0; i < PER; ++i) two_largest(t.base + i < a.experts ? c[i] : -(S)INFINITY, first, second);
+    auto join = [&](S f, S s) {
+      second = larger(larger(second, s), smaller(first, f));
+      first = larger(first, f);
+    };
+    if (a.group_lanes > 1) join(turned<0xB1>(first), turned<0xB1>(second));    // lane ^ 1
+    if (a.group_lanes > 2) join(turned<0x4E>(first), turned<0x4E>(second));    // lane ^ 2
+    if (a.group_lanes > 4) join(turned<0x141>(first), turned<0x141>(second));  // 7 - lane: the other four
+    const S mine = a.group_top > 1 ? first + second : first;
+    int before = 0;
+    // lane l reads lane l - n of its 16: a group before its own where l >= n, n whole groups
+    auto against = [&](S v, int n) {
+      before += v > mine || (v == mine && t.lane >= n);
+      if (too_near(v, mine)) unsure = true;
+    };
+    if (a.group_lanes == 1) {
+      against(turned<0x121>(mine), 1);
+      against(turned<0x123>(mine), 3);
+      against(turned<0x125>(mine), 5);
+      against(turned<0x127>(mine), 7);
+      against(turned<0x129>(mine), 9);
+      against(turned<0x12B>(mine), 11);
+      against(turned<0x12D>(mine), 13);
+      against(turned<0x12F>(mine), 15);
+    }
+    if (a.group_lanes <= 2) {
+      against(turned<0x122>(mine), 2);
+      against(turned<0x126>(mine), 6);
+      against(turned<0x12A>(mine), 10);
+      against(turned<0x12E>(mine), 14);
+    }
+    if (a.group_lanes <= 4) {
+      against(turned<0x124>(mine), 4);
+      against(turned<0x12C>(mine), 12);
+    }
+    against(turned<0x128>(mine), 8);
+    if (before >= a.kept) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) k[i] = O::kGone;
+    }
+    return;
+  }
+  // groups of any size: the token's values in LDS, a group a lane
+  S *rank = lds + LANES * PER;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) lds[t.base + i] = c[i];
+  wave_sync();
+  for (int g = t.lane; g < a.groups; g += LANES) {
+    S first = -(S)INFINITY, second = -(S)INFINITY;
+    for (int i = 0; i < size; ++i) two_largest(lds[g * size + i], first, second);
+    rank[g] = a.group_top > 1 ? first + second : first;
+  }
+  wave_sync();
+  uint64_t stays = 0;
+  for (int g = t.lane; g < a.groups; g += LANES) {
+    const S mine = rank[g];
+    int before = 0;
+    for (int f = 0; f < a.groups; ++f) {
+      const S v = rank[f];
+      before += v > mine || (v == mine && f < g);
+      if (f != g && too_near(v, mine)) unsure = true;
+    }
+    if (before < a.kept) stays |= 1ull << g;
+  }
+  wave_sync();
+  stays = fold<LANES>((int64_t)stays, [](int64_t p, int64_t q) { return p | q; });
+  int g = t.base / size, left = (g + 1) * size - t.base;  // experts of group g from this one on
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    if (g < a.groups && !((uint64_t)stays >> g & 1)) k[i] = O::kGone;
+    if (--left == 0) {
+      ++g;
+      left = size;
     }
   }
+}
 
+// The topk largest in rounds: choice j stays in lane j.
+template <typename S, int LANES, int PER>
+__device__ __forceinline__ void by_rounds(const RouteArgs &a, const Token<PER> &t, typename Ordered<S>::key k[PER], int &id,
+                                          bool &unsure) {
+  typedef Ordered<S> O;
+  typedef typename O::key key;
+  const bool margins = std::is_same<S, float>::value && a.bias != nullptr;
   S last = 0;
-  const bool margins = !kExact && a.bias != nullptr;
-  const int rounds = a.topk + (margins ? 1 : 0);
-  for (int j = 0; j < rounds; ++j) {
+  for (int j = 0; j < a.topk + (margins ? 1 : 0); ++j) {
     key m = k[0];
     int at = 0;
 #pragma unroll
@@ -235,30 +295,88 @@ __device__ __forceinline__ bool choose(const RouteArgs &a, const Token<LANES, PE
       if (j == a.topk) break;
     }
     const int e = least<LANES>(m == best ? t.base + at : 0x7fffffff);
-#pragma unroll
-    for (int q = 0; q < KEEP; ++q)
-      if (j == t.lane + q * LANES) id[q] = e;
+    if (j == t.lane) id = e;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       if (e == t.base + i) k[i] = O::kGone;
   }
-  return unsure;
 }
 
+// How many of the 16 lanes' values come before this lane's: larger ones, and equal ones
+// of lower lanes.
+template <int N = 1>
+__device__ __forceinline__ int before_me(int32_t v, int lane) {
+  if constexpr (N == 16) {
+    return 0;
+  } else {
+    const int32_t o = turned<0x120 + N>(v);  // lane - N's
+    return (int)(lane >= N ? o >= v : o > v) + before_me<N + 1>(v, lane);
+  }
+}
+
+// A value that reached the bound.
+struct Reached {
+  int32_t key, id;
+};
+
+// The topk (at most 16) largest of 16 lanes' values; false where more than 16 reach the
+// bound.  `box`: 16 places of this token's in LDS.
+template <int PER>
+__device__ __forceinline__ bool by_bound(const RouteArgs &a, const Token<PER> &t, const int32_t k[PER], Reached *box, int &id,
+                                         bool &unsure) {
+  typedef Ordered<float> O;
+  const bool margins = a.bias != nullptr;
+  int32_t m = k[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) m = larger(m, k[i]);
+  int32_t bound = most<16>(before_me(m, t.lane) == a.topk - 1 ? m : INT32_MIN);
+  // fewer lanes than choices hold any value: all that are left
+  bound = larger(bound, O::kGone + 1);
+  if (margins) {
+    // what 64 bits might put before the last choice reaches it too
+    const float v = O::value(bound);
+    if (fabsf(v) < INFINITY) bound = O::of(v - near(v, true));
+  }
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) n += k[i] >= bound;
+  int upto = n;
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x111, 0xf, 0xf, false);  // row_shr:1
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x112, 0xf, 0xf, false);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x114, 0xf, 0xf, false);
+  upto += __builtin_amdgcn_update_dpp(0, upto, 0x118, 0xf, 0xf, false);
+  const int all = __shfl(upto, 15, 16);
+  if (__any(all > 16)) return false;
+  int at = upto - n;
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (k[i] >= bound) box[at++] = Reached{k[i], t.base + i};
+  wave_sync();
+  Reached mine{O::kGone, 0};
+  if (t.lane < all) mine = box[t.lane];      // by ascending id: a lower lane has the lower one
+  const int place = before_me(mine.key, t.lane);
+  wave_sync();
+  if (t.lane < all) box[place] = mine;
+  wave_sync();
+  Reached it{O::kGone, 0};
+  if (t.lane < all) it = box[t.lane];
+  id = it.id;
+  if (margins) {
+    const int32_t prior = __builtin_amdgcn_update_dpp(O::kGone, it.key, 0x111, 0xf, 0xf, false);
+    const float v = O::value(it.key), p = O::value(prior);
+    if (t.lane > 0 && t.lane <= a.topk && t.lane < all && v > -INFINITY && p - v <= near(p, true)) unsure = true;
+    // 16 choices: the next one has no lane, and did not reach the bound, or there would be more than 16
+  }
+  wave_sync();
+  return true;
+}
+
+// A token's logits and biases, over LANES lanes.
 template <typename X, int LANES, int PER>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
-  constexpr int KEEP = LANES == 16 ? 2 : 1;  // choices a lane keeps: at most kMaxTopk in all
-  constexpr int kTokens = 64 / LANES;        // a wave's
-  // values and ranks of a token, in 64 bits
-  extern __shared__ __align__(16) double lds[];
-  const int lane = threadIdx.x % 64;
-  Token<LANES, PER> t;
-  t.lane = lane % LANES;
+__device__ __forceinline__ Token<PER> token_at(const RouteArgs &a, const char *row) {
+  Token<PER> t;
+  t.lane = threadIdx.x % LANES;
   t.base = t.lane * PER;
-  const int64_t token = (int64_t)blockIdx.x * (4 * kTokens) + threadIdx.x / LANES;
-  const bool real = token < a.tokens;
-  // a wave's surplus lanes do the last token again, and do not write
-  const char *row = a.logits + (real ? token : a.tokens - 1) * a.ld * (int64_t)sizeof(X);
   constexpr int kVec = 16 / (int)sizeof(X);
   if (PER % kVec == 0 && a.aligned && a.experts == LANES * PER) {
     if constexpr (PER % kVec == 0) {
@@ -271,41 +389,75 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
           else t.x[i + v] = __uint_as_float(w[v]);
         }
       }
+#pragma unroll
+      for (int i = 0; i < PER; ++i) t.bias[i] = a.bias ? a.bias[t.base + i] : 0.f;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < PER; ++i) t.x[i] = t.base + i < a.experts ? logit_at<X>(row, t.base + i) : -INFINITY;
+    for (int i = 0; i < PER; ++i) {
+      const bool in = t.base + i < a.experts;
+      t.x[i] = in ? logit_at<X>(row, t.base + i) : -INFINITY;
+      t.bias[i] = in && a.bias ? a.bias[t.base + i] : 0.f;
+    }
   }
   float top = -INFINITY;
-  int nan = 0;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    top = fmaxf(top, t.x[i]);
-    nan |= t.x[i] != t.x[i];
-  }
+  for (int i = 0; i < PER; ++i) top = fmaxf(top, t.x[i]);
   t.top = most<LANES>(top);
-  nan = fold<LANES>(nan, [](int p, int q) { return p | q; });
+  return t;
+}
 
-  double *mine = lds + (threadIdx.x / LANES) * (a.groups > 1 ? LANES * PER + kMaxGroups : 0);
-  int id[KEEP];
+template <typename X, int LANES, int PER>
+__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  constexpr int kTokens = 64 / LANES;             // a wave's
+  constexpr int kExactPer = LANES * PER / 64 < 1 ? 1 : LANES * PER / 64;
+  __shared__ Reached boxes[LANES == 16 ? 256 : 1];
+  // a wave's: values and ranks of its tokens, or of one token in 64 bits
+  constexpr int kShort = kTokens * (LANES * PER + kMaxGroups) * (int)sizeof(float);
+  constexpr int kExact = (64 * kExactPer + kMaxGroups) * (int)sizeof(double);
+  __shared__ __align__(16) char values[4][kShort > kExact ? kShort : kExact];
+  const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
+  const int64_t first = (int64_t)blockIdx.x * (4 * kTokens) + wave * kTokens;
+  const int64_t token = first + lane / LANES;
+  const bool real = token < a.tokens;
+  // a wave's surplus lanes do the last token again, and do not write
+  auto row_of = [&](int64_t i) { return a.logits + min(i, a.tokens - 1) * a.ld * (int64_t)sizeof(X); };
+  const char *row = row_of(token);
+  const Token<PER> t = token_at<X, LANES, PER>(a, row);
+  bool nan = false;
 #pragma unroll
-  for (int q = 0; q < KEEP; ++q) id[q] = 0;
-  const bool unsure = choose<float, LANES, PER, KEEP>(a, t, reinterpret_cast<float *>(mine), id);
-  if (__any(unsure)) choose<double, LANES, PER, KEEP>(a, t, mine, id);
+  for (int i = 0; i < PER; ++i) nan |= t.x[i] != t.x[i];
+  nan = fold<LANES>((int)nan, [](int p, int q) { return p | q; });
 
-  // the chosen ones' scores, in 64 bits: a lane has one or two
-  double s[KEEP], sum = 0;
-#pragma unroll
-  for (int q = 0; q < KEEP; ++q) {
-    s[q] = 0;
-    if (t.lane + q * LANES < a.topk) {
-      const float x = logit_at<X>(row, id[q]);
-      if (x > -INFINITY) s[q] = a.sigmoid ? 1. / (1. + exp(-(double)x)) : x == t.top ? 1. : exp((double)x - (double)t.top);
-    }
-    sum += s[q];
+  int id = 0;
+  bool unsure = false, done = false;
+  int32_t k[PER];
+  keys_of<float, LANES, PER>(a, t, reinterpret_cast<float *>(values[wave]) + lane / LANES * (LANES * PER + kMaxGroups), k, unsure);
+  if constexpr (LANES == 16) done = by_bound<PER>(a, t, k, boxes + threadIdx.x / 16 * 16, id, unsure);
+  if (!done) by_rounds<float, LANES, PER>(a, t, k, id, unsure);
+  // in 64 bits, the whole wave a token
+  for (uint64_t left = __ballot(unsure); left;) {
+    const int q = __builtin_ctzll(left) / LANES;
+    left &= LANES == 64 ? 0 : ~(((1ull << LANES % 64) - 1) << q * LANES);
+    const Token<kExactPer> u = token_at<X, 64, kExactPer>(a, row_of(first + q));
+    int64_t v[kExactPer];
+    int e = 0;
+    bool never = false;
+    wave_sync();
+    keys_of<double, 64, kExactPer>(a, u, reinterpret_cast<double *>(values[wave]), v, never);
+    by_rounds<double, 64, kExactPer>(a, u, v, e, never);
+    e = __shfl(e, lane % LANES, 64);
+    if (lane / LANES == q) id = e;
+  }
+
+  // the chosen one's score, in 64 bits
+  double s = 0, sum = 1;
+  if (t.lane < a.topk) {
+    const float x = logit_at<X>(row, id);
+    if (x > -INFINITY) s = a.sigmoid ? 1. / (1. + exp(-(double)x)) : x == t.top ? 1. : exp((double)x - (double)t.top);
   }
   if (a.renorm) {
-    sum = total<LANES>(sum);
+    sum = total<LANES>(s);
   } else if (!a.sigmoid) {
     // the sum of all: 32 bits a lane (at most 16 of them), 64 across
     float part = 0;
@@ -313,33 +465,30 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     for (int i = 0; i < PER; ++i)
       if (t.x[i] > -INFINITY) part += t.x[i] == t.top ? 1.f : expf(t.x[i] - t.top);
     sum = total<LANES>((double)part);
-  } else {
-    sum = 1;
   }
-#pragma unroll
-  for (int q = 0; q < KEEP; ++q) {
-    const int j = t.lane + q * LANES;
-    if (real && j < a.topk) {
-      float w = sum > 0 ? (float)(s[q] / sum * (double)a.scale) : 0.f;
-      if (nan) w = __builtin_nanf("");
-      a.ids[token * a.topk + j] = id[q];
-      a.weights[token * a.topk + j] = w;
-    }
+  if (real && t.lane < a.topk) {
+    float w = sum > 0 ? (float)(s / sum * (double)a.scale) : 0.f;
+    if (nan) w = __builtin_nanf("");
+    a.ids[token * a.topk + t.lane] = id;
+    a.weights[token * a.topk + t.lane] = w;
   }
 }
 
 template <typename X, int LANES, int PER>
-hipError_t launch_as(const RouteArgs &all, hipStream_t s) {
+hipError_t launch_as(RouteArgs all, hipStream_t s) {
   constexpr int kTokens = 256 / LANES;
+  // groups that are 1, 2, 4 or 8 whole lanes
+  const int size = all.experts / all.groups, lanes = size / PER;
+  const bool whole = LANES == 16 && all.groups > 1 && size % PER == 0 && lanes <= 8 && (lanes & (lanes - 1)) == 0;
+  all.group_lanes = whole ? lanes : 0;
   constexpr int64_t kMost = (int64_t)1 << 22;  // workgroups of a launch
-  const size_t lds = all.groups > 1 ? sizeof(double) * kTokens * (LANES * PER + kMaxGroups) : 0;
   for (int64_t t0 = 0; t0 < all.tokens; t0 += kMost * kTokens) {
     RouteArgs a = all;
     a.tokens = std::min(all.tokens - t0, kMost * kTokens);
     a.logits += t0 * a.ld * (int64_t)sizeof(X);
     a.ids += t0 * a.topk;
     a.weights += t0 * a.topk;
-    route_kernel<X, LANES, PER><<<dim3((unsigned)((a.tokens + kTokens - 1) / kTokens)), dim3(256), lds, s>>>(a);
+    route_kernel<X, LANES, PER><<<dim3((unsigned)((a.tokens + kTokens - 1) / kTokens)), dim3(256), 0, s>>>(a);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -348,10 +497,13 @@ hipError_t launch_as(const RouteArgs &all, hipStream_t s) {
 
 template <typename X>
 hipError_t launch_for(const RouteArgs &a, hipStream_t s) {
-  if (a.experts <= 16) return launch_as<X, 16, 1>(a, s);
-  if (a.experts <= 64) return launch_as<X, 16, 4>(a, s);
-  if (a.experts <= 128) return launch_as<X, 16, 8>(a, s);
-  if (a.experts <= 256) return launch_as<X, 16, 16>(a, s);
+  if (a.experts <= 256 && a.topk <= 16) {
+    if (a.experts <= 16) return launch_as<X, 16, 1>(a, s);
+    if (a.experts <= 64) return launch_as<X, 16, 4>(a, s);
+    if (a.experts <= 128) return launch_as<X, 16, 8>(a, s);
+    return launch_as<X, 16, 16>(a, s);
+  }
+  if (a.experts <= 256) return launch_as<X, 64, 4>(a, s);
   if (a.experts <= 512) return launch_as<X, 64, 8>(a, s);
   return launch_as<X, 64, 16>(a, s);
 }
