@@ -36,6 +36,13 @@ __device__ __forceinline__ void to_lds(const int8_t *from, u32x4 *to) {
                                    (__attribute__((address_space(3))) void *)to, 16, 0, 0);
 }
 
+// Every wave's transfers to LDS have arrived, and its reads have left.  (A barrier alone
+// waits for LDS operations, not for transfers that memory still holds.)
+__device__ __forceinline__ void settle() {
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+}
+
 // LDS written by this wave is read by this wave.
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -95,7 +102,10 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   // ---- transfers of the tile that `aim` was called for
   const int8_t *xb = a.x, *wb = a.w;              // where its rows of either operand are counted from
   uint32_t xo[XQ], wo[WQ];                        // bytes from there to the piece of its row that a lane transfers
-  const int piece = (lane % 8) ^ (lane / 8);
+  // A row's piece p lies at place p ^ (row / 2 % 8) of its 8: the same piece of 16 neighbouring rows fills the 64 banks.
+  // A transfer takes 8 rows, 8 (wave + kWaves q) and on.
+  static_assert(kWaves % 2 == 0, "the place of a lane's piece is the same in all transfers");
+  const int piece = (lane % 8) ^ (4 * (wave % 2) + lane / 16);
   constexpr int kIds = (BM + kThreads - 1) / kThreads;
   int32_t pending[kIds];
   auto fetch_ids = [&](const Tile &t) {
@@ -154,9 +164,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   // ---- products
   i32x16 sum[TM][TN];
   i32x4 xv[2][TM], wv[2][TN];
-  // a row's piece p lies at place p ^ (row % 8) of its 8: 8 neighbouring rows' pieces fill the banks
-  const int xr = (wm * TM * 32 + l32) * kPieces + (half ^ (lane % 8));
-  const int wr = (BM + wn * TN * 32 + l32) * kPieces + (half ^ (lane % 8));
+  const int xr = (wm * TM * 32 + l32) * kPieces + (half ^ (l32 / 2 % 8));
+  const int wr = (BM + wn * TN * 32 + l32) * kPieces + (half ^ (l32 / 2 % 8));
   auto read = [&](const u32x4 *buf, int phase, int set) {
 #pragma unroll
     for (int n = 0; n < TN; ++n)
@@ -205,7 +214,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   auto stage = [&](u32x4 *here, const u32x4 *next, int k) {
     three_quarters(here);
     __builtin_amdgcn_sched_barrier(0);
-    __syncthreads();
+    settle();
     read(next, 0, 0);
     transfer(here, k + 2 * kDepth);
     multiply(1);
@@ -217,7 +226,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   auto stage_end = [&](u32x4 *here, const u32x4 *next, int s) {
     three_quarters(here);
     if (s + 1 < stages) {
-      __syncthreads();
+      settle();
       if (s + 2 < stages) transfer_end(here, (s + 2) * kDepth);
       read(next, 0, 0);
     }
@@ -228,6 +237,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   auto finish = [&](const Tile &t, int slot, u32x4 *scratch) {
     constexpr int kRowPieces = TN * 32 * (int)sizeof(Y) / 16;
     u32x4 *mine = scratch + wave * 32 * kRowPieces;
+    // the pieces of a row change places by its number, so that neither the writes nor the reads meet in a bank
+    auto turn = [&](int row) { return kRowPieces >= 16 ? row % kRowPieces : row * kRowPieces / 16 % kRowPieces; };
     const int c0 = t.n0 + wn * TN * 32;
     // the wave's columns' scales and bias: fetched once, read from LDS as they are needed
     float *ws = columns[wave][0], *bs = columns[wave][1];
@@ -257,13 +268,12 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
           float v[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[e] = (float)sum[m][n][4 * g + e] * (xs * w4[e]) + b4[e];
-          // the pieces of a row change places by its number: neither these writes nor the reads below meet in a bank
           if constexpr (sizeof(Y) == 2) {
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            u32x2 *to = reinterpret_cast<u32x2 *>(mine + l32 * kRowPieces + ((4 * n + g) ^ (l32 % kRowPieces)));
+            u32x2 *to = reinterpret_cast<u32x2 *>(mine + l32 * kRowPieces + ((4 * n + g) ^ turn(l32)));
             to[half] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           } else {
-            mine[l32 * kRowPieces + ((8 * n + 2 * g + half) ^ (l32 % kRowPieces))] =
+            mine[l32 * kRowPieces + ((8 * n + 2 * g + half) ^ turn(l32))] =
                 __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
           }
         }
@@ -272,7 +282,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
 #pragma unroll
       for (int q = 0; q < 32 / kRowsAtOnce; ++q) {
         const int lr = q * kRowsAtOnce + lane / kRowPieces, p = lane % kRowPieces;
-        const u32x4 v = mine[lr * kRowPieces + (p ^ (lr % kRowPieces))];
+        const u32x4 v = mine[lr * kRowPieces + (p ^ turn(lr))];
         const int c = c0 + p * (16 / (int)sizeof(Y));
         if (t.m0 + r + lr < t.count && c < a.d_out) {
           int64_t to = t.m0 + r + lr;
@@ -299,7 +309,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
       then = tile_at(index + per);
       fetch_ids(then);
     }
-    __syncthreads();  // the first stage is there, and the last tile's scratch is free
+    settle();         // the first stage is there, and the last tile's scratch is free
     if (follows) keep_ids(slot ^ 1);
     if (stages > 1) transfer_end(buf1, kDepth);
 #pragma unroll
