@@ -9,7 +9,6 @@ namespace lora {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x16 __attribute__((ext_vector_type(16)));
 
 constexpr int kDepth = 128;  // bytes of d_in a stage holds of every row
 constexpr int kPieces = kDepth / 16;
@@ -50,20 +49,20 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // Instruction kinds of __builtin_amdgcn_sched_group_barrier.
-constexpr int kSchedMfma = 0x8, kSchedVmem = 0x20, kSchedDsRead = 0x100;
+constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 
 template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewest) {
   constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
-  constexpr int TM = BM / WM / 32, TN = BN / WN / 32;          // blocks of 32 of a wave
+  constexpr int TM = BM / WM / 16, TN = BN / WN / 16;          // blocks of 16 of a wave
   constexpr int XQ = BM / 8 / kWaves, WQ = BN / 8 / kWaves;    // transfers of 8 rows of a wave and stage
   __shared__ u32x4 buf0[(BM + BN) * kPieces], buf1[(BM + BN) * kPieces];
   __shared__ int32_t ids[2][GROUPED ? BM : 1];
-  __shared__ __align__(16) float columns[kWaves][2][TN * 32];
+  __shared__ __align__(16) float columns[kWaves][2][TN * 16];
   extern __shared__ __align__(16) char table[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
-  const int l32 = lane % 32, half = lane / 32;
+  const int l16 = lane % 16, quarter = lane / 16;
   const int col_tiles = (a.d_out + BN - 1) / BN;
   const SegTable tb = seg_table_at(table, a.experts);
   int tiles;
@@ -105,7 +104,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   // A row's piece p lies at place p ^ (row / 2 % 8) of its 8: the same piece of 16 neighbouring rows fills the 64 banks.
   // A transfer takes 8 rows, 8 (wave + kWaves q) and on.
   static_assert(kWaves % 2 == 0, "the place of a lane's piece is the same in all transfers");
-  const int piece = (lane % 8) ^ (4 * (wave % 2) + lane / 16);
+  auto piece_of = [&](int lane) { return (lane % 8) ^ (4 * (wave % 2) + lane / 16); };
   constexpr int kIds = (BM + kThreads - 1) / kThreads;
   int32_t pending[kIds];
   auto fetch_ids = [&](const Tile &t) {
@@ -123,6 +122,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     }
   };
   auto aim = [&](const Tile &t, int slot) {
+    int lane = threadIdx.x % 64;  // hidden, as in `finish` below
+    asm volatile("" : "+v"(lane));
+    const int piece = piece_of(lane);
     if constexpr (!GROUPED) xb = a.x + (int64_t)t.m0 * a.ldx;
 #pragma unroll
     for (int q = 0; q < XQ; ++q) {
@@ -141,17 +143,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     for (int q = 0; q < WQ; ++q)
       wo[q] = (uint32_t)min((q * kWaves + wave) * 8 + lane / 8, a.d_out - 1 - t.n0) * (uint32_t)a.row_stride + 16 * piece;
   };
-  auto transfer = [&](u32x4 *buf, int k) {
-    // hidden from the optimiser, which would keep a 64-bit address for every transfer
-    asm volatile("" : "+s"(k));
-    const int8_t *xk = xb + k, *wk = wb + k;
-#pragma unroll
-    for (int q = 0; q < XQ; ++q) to_lds(xk + xo[q], buf + (q * kWaves + wave) * 64);
-#pragma unroll
-    for (int q = 0; q < WQ; ++q) to_lds(wk + wo[q], buf + BM * kPieces + (q * kWaves + wave) * 64);
-  };
-  // the same where d_in may end: lanes past the end take zeros for x, and for w stay inside the row
+  // a stage's transfers where d_in may end: lanes past the end take zeros for x, and for w stay inside the row
   auto transfer_end = [&](u32x4 *buf, int k) {
+    const int piece = piece_of(lane);
     const bool in = k + 16 * piece < a.d_in;
 #pragma unroll
     for (int q = 0; q < XQ; ++q)
@@ -161,122 +155,138 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
       to_lds(wb + (in ? k : -16 * piece) + wo[q], buf + BM * kPieces + (q * kWaves + wave) * 64);
   };
 
-  // ---- products
-  i32x16 sum[TM][TN];
-  i32x4 xv[2][TM], wv[2][TN];
-  const int xr = (wm * TM * 32 + l32) * kPieces + (half ^ (l32 / 2 % 8));
-  const int wr = (BM + wn * TN * 32 + l32) * kPieces + (half ^ (l32 / 2 % 8));
-  auto read = [&](const u32x4 *buf, int phase, int set) {
+  // ---- products: a stage is two phases of 64 bytes.  A block of x's operands is overwritten
+  // with the next phase's as soon as its products are on their way; w's have two sets.
+  static_assert(TM >= TN, "w's operands are read along with x's");
+  i32x4 sum[TM][TN];
+  i32x4 xv[TM], wv[2][TN];
+  const int xr = (wm * TM * 16 + l16) * kPieces + (quarter ^ (l16 / 2));
+  const int wr = (BM + wn * TN * 16 + l16) * kPieces + (quarter ^ (l16 / 2));
+  auto read_x = [&](const u32x4 *buf, int phase, int m) {
+    xv[m] = __builtin_bit_cast(i32x4, buf[(xr ^ (4 * phase)) + m * 16 * kPieces]);
+  };
+  auto read_w = [&](const u32x4 *buf, int phase, int n) {
+    wv[phase][n] = __builtin_bit_cast(i32x4, buf[(wr ^ (4 * phase)) + n * 16 * kPieces]);
+  };
+  auto multiply = [&](int phase, int m) {
 #pragma unroll
     for (int n = 0; n < TN; ++n)
-      wv[set][n] = __builtin_bit_cast(i32x4, buf[(wr ^ (2 * phase)) + n * 32 * kPieces]);
-#pragma unroll
-    for (int m = 0; m < TM; ++m)
-      xv[set][m] = __builtin_bit_cast(i32x4, buf[(xr ^ (2 * phase)) + m * 32 * kPieces]);
+      sum[m][n] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[phase][n], xv[m], sum[m][n], 0, 0, 0);
   };
-  auto multiply = [&](int set) {
-#pragma unroll
-    for (int m = 0; m < TM; ++m)
-#pragma unroll
-      for (int n = 0; n < TN; ++n)
-        sum[m][n] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][n], xv[set][m], sum[m][n], 0, 0, 0);
+  // the next phase's operands that are read behind block m's products
+  auto refill = [&](const u32x4 *buf, int phase, int m) {
+    if (m < TN) read_w(buf, phase, m);
+    read_x(buf, phase, m);
   };
-  // The order of a quarter: its reads, and its transfers, between the products.
-  constexpr int kReads = TM + TN, kProducts = TM * TN;
-  auto spread_reads = [&]() {
+  constexpr int kEarly = 2;      // blocks of the second phase that are multiplied before the barrier
+  auto first_phase = [&](const u32x4 *here) {
 #pragma unroll
-    for (int i = 0; i < kProducts; ++i) {
-      if (i < kReads) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
+    for (int m = 0; m < TM; ++m) {
+      multiply(0, m);
+      refill(here, 1, m);
     }
-  };
-  auto spread_transfers = [&]() {
+    // the order: products of a block, then its reads
 #pragma unroll
-    for (int i = 0; i < kProducts; ++i) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, 1, 0);
-      if (i < kReads) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
-      if (i < XQ + WQ) __builtin_amdgcn_sched_group_barrier(kSchedVmem, 1, 0);
+    for (int m = 0; m < TM; ++m) {
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, TN, 0);
+      if (m < TN) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 2, 0);
+      else __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);
   };
-  // the first three quarters of a stage; the last one's operands are in registers then, so
-  // that the transfers of the stage after the next may overwrite it
-  auto three_quarters = [&](const u32x4 *here) {
-    read(here, 1, 1);
-    multiply(0);
-    spread_reads();
-    read(here, 2, 0);
-    multiply(1);
-    spread_reads();
-    read(here, 3, 1);
-    multiply(0);
-    spread_reads();
-  };
+  // the second phase's operands are in registers by the barrier, so that the transfers of the
+  // stage after the next may overwrite this one's place
   auto stage = [&](u32x4 *here, const u32x4 *next, int k) {
-    three_quarters(here);
+    first_phase(here);
+#pragma unroll
+    for (int m = 0; m < kEarly; ++m) multiply(1, m);
     __builtin_amdgcn_sched_barrier(0);
     settle();
-    read(next, 0, 0);
-    transfer(here, k + 2 * kDepth);
-    multiply(1);
-    spread_transfers();
-    __builtin_amdgcn_sched_barrier(0);
+    k += 2 * kDepth;
+    // hidden from the optimiser, which would keep a 64-bit address for every transfer
+    asm volatile("" : "+s"(k));
+    const int8_t *xk = xb + k, *wk = wb + k;
+#pragma unroll
+    for (int m = 0; m < kEarly; ++m) refill(next, 0, m);
+#pragma unroll
+    for (int m = kEarly; m < TM; ++m) {
+      multiply(1, m);
+      refill(next, 0, m);
+#pragma unroll
+      for (int q = 0; q < XQ; ++q)
+        if (kEarly + q * (TM - kEarly) / (XQ + WQ) == m) to_lds(xk + xo[q], here + (q * kWaves + wave) * 64);
+#pragma unroll
+      for (int q = 0; q < WQ; ++q)
+        if (kEarly + (XQ + q) * (TM - kEarly) / (XQ + WQ) == m)
+          to_lds(wk + wo[q], here + BM * kPieces + (q * kWaves + wave) * 64);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   const int stages = (a.d_in + kDepth - 1) / kDepth, whole = a.d_in / kDepth;
   // a stage that may be among a tile's last ones
   auto stage_end = [&](u32x4 *here, const u32x4 *next, int s) {
-    three_quarters(here);
-    if (s + 1 < stages) {
+    first_phase(here);
+    const bool goes_on = s + 1 < stages;
+    if (goes_on) {
       settle();
       if (s + 2 < stages) transfer_end(here, (s + 2) * kDepth);
-      read(next, 0, 0);
     }
-    multiply(1);
+#pragma unroll
+    for (int m = 0; m < TM; ++m) {
+      multiply(1, m);
+      if (goes_on) refill(next, 0, m);
+    }
   };
 
-  // ---- y of the finished tile, through LDS so that whole lines are stored
+  // ---- y of the finished tile, through LDS so that whole lines are stored: 32 rows at a time
   auto finish = [&](const Tile &t, int slot, u32x4 *scratch) {
-    constexpr int kRowPieces = TN * 32 * (int)sizeof(Y) / 16;
+    constexpr int kRowPieces = TN * 16 * (int)sizeof(Y) / 16;
     u32x4 *mine = scratch + wave * 32 * kRowPieces;
+    // hidden from the optimiser, which would keep what follows from it in registers all through the products
+    int lane = threadIdx.x % 64;
+    asm volatile("" : "+v"(lane));
+    const int l16 = lane % 16, quarter = lane / 16;
     // the pieces of a row change places by its number, so that neither the writes nor the reads meet in a bank
     auto turn = [&](int row) { return kRowPieces >= 16 ? row % kRowPieces : row * kRowPieces / 16 % kRowPieces; };
-    const int c0 = t.n0 + wn * TN * 32;
+    const int c0 = t.n0 + wn * TN * 16;
     // the wave's columns' scales and bias: fetched once, read from LDS as they are needed
     float *ws = columns[wave][0], *bs = columns[wave][1];
-#pragma unroll
-    for (int c = lane; c < TN * 32; c += 64) {
+    for (int c = lane; c < TN * 16; c += 64) {
       const int64_t at = (int64_t)t.expert * a.d_out + min(c0 + c, a.d_out - 1);
       ws[c] = a.w_scale[at];
       bs[c] = a.bias ? a.bias[at] : 0.f;
     }
     wave_sync();
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      const int r = (wm * TM + m) * 32;           // of the tile
-      uint32_t row = (uint32_t)min(t.m0 + r + l32, t.count - 1);
-      if constexpr (GROUPED) {
-        row = (uint32_t)ids[slot][r + l32];
-        if (a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
-      }
-      const float xs = a.x_scale[row];
+    for (int m = 0; m < TM; m += 2) {
+      const int r = (wm * TM + m) * 16;           // of the tile
 #pragma unroll
-      for (int n = 0; n < TN; ++n)
+      for (int b = 0; b < 2; ++b) {
+        uint32_t row = (uint32_t)min(t.m0 + r + 16 * b + l16, t.count - 1);
+        if constexpr (GROUPED) {
+          row = (uint32_t)ids[slot][r + 16 * b + l16];
+          if (a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
+        }
+        const float xs = a.x_scale[row];
+        u32x4 *line = mine + (16 * b + l16) * kRowPieces;
+        const int places = turn(16 * b + l16);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          // columns 32 n + 8 g + 4 half .. + 3 of row l32
-          const f32x4 w4 = *reinterpret_cast<const f32x4 *>(ws + 32 * n + 8 * g + 4 * half);
-          const f32x4 b4 = *reinterpret_cast<const f32x4 *>(bs + 32 * n + 8 * g + 4 * half);
+        for (int n = 0; n < TN; ++n) {
+          // columns 16 n + 4 quarter .. + 3 of the row
+          const f32x4 w4 = *reinterpret_cast<const f32x4 *>(ws + 16 * n + 4 * quarter);
+          const f32x4 b4 = *reinterpret_cast<const f32x4 *>(bs + 16 * n + 4 * quarter);
           float v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = (float)sum[m][n][4 * g + e] * (xs * w4[e]) + b4[e];
+          for (int e = 0; e < 4; ++e) v[e] = (float)sum[m + b][n][e] * (xs * w4[e]) + b4[e];
           if constexpr (sizeof(Y) == 2) {
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            u32x2 *to = reinterpret_cast<u32x2 *>(mine + l32 * kRowPieces + ((4 * n + g) ^ turn(l32)));
-            to[half] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+            u32x2 *to = reinterpret_cast<u32x2 *>(line + ((2 * n + quarter / 2) ^ places));
+            to[quarter % 2] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
           } else {
-            mine[l32 * kRowPieces + ((8 * n + 2 * g + half) ^ turn(l32))] =
-                __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
+            line[(4 * n + quarter) ^ places] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
           }
         }
+      }
       wave_sync();
       constexpr int kRowsAtOnce = 64 / kRowPieces;
 #pragma unroll
@@ -315,8 +325,9 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
 #pragma unroll
     for (int m = 0; m < TM; ++m)
 #pragma unroll
-      for (int n = 0; n < TN; ++n) sum[m][n] = i32x16{};
-    read(buf0, 0, 0);
+      for (int n = 0; n < TN; ++n) sum[m][n] = i32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int m = 0; m < TM; ++m) refill(buf0, 0, m);
     int s = 0;
     for (; s + 3 < whole; s += 2) {
       stage(buf0, buf1, s * kDepth);
