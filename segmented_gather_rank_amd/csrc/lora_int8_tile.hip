@@ -13,8 +13,8 @@ typedef int i32x4 __attribute__((ext_vector_type(4)));
 constexpr int kDepth = 128;  // bytes of d_in a stage holds of every row
 constexpr int kPieces = kDepth / 16;
 
-// What a lane past the end of d_in reads instead: zeros on x's side are enough.
-__device__ const u32x4 zero_piece = {0, 0, 0, 0};
+// An offset past the end of every buffer: a lane that transfers from there gets zeros.
+constexpr uint32_t kNowhere = 0xffffffffu;
 
 struct Tile {
   int expert, n0, m0, count, start;  // rows m0 .. of a segment of `count` rows from `start` in `sorted`
@@ -30,9 +30,10 @@ __device__ __forceinline__ void place(int i, int row_tiles, int col_tiles, int &
   m = band * kBand + in - n * high;
 }
 
-__device__ __forceinline__ void to_lds(const int8_t *from, u32x4 *to) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void *)from,
-                                   (__attribute__((address_space(3))) void *)to, 16, 0, 0);
+// 16 bytes a lane from `at` + k of the buffer; `to` is the wave's.  (A transfer by address
+// would count as an LDS operation too, and every wait for LDS would be one for all of them.)
+__device__ __forceinline__ void to_lds(rsrc_t from, uint32_t at, int k, u32x4 *to) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)at, k, 0, 0);
 }
 
 // Every wave's transfers to LDS have arrived, and its reads have left.  (A barrier alone
@@ -47,9 +48,6 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   __builtin_amdgcn_wave_barrier();
 }
-
-// Instruction kinds of __builtin_amdgcn_sched_group_barrier.
-constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 
 template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
 __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewest) {
@@ -99,7 +97,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   };
 
   // ---- transfers of the tile that `aim` was called for
-  const int8_t *xb = a.x, *wb = a.w;              // where its rows of either operand are counted from
+  rsrc_t xb, wb;                                  // from where its rows of either operand are counted
   uint32_t xo[XQ], wo[WQ];                        // bytes from there to the piece of its row that a lane transfers
   // A row's piece p lies at place p ^ (row / 2 % 8) of its 8: the same piece of 16 neighbouring rows fills the 64 banks.
   // A transfer takes 8 rows, 8 (wave + kWaves q) and on.
@@ -125,7 +123,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     int lane = threadIdx.x % 64;  // hidden, as in `finish` below
     asm volatile("" : "+v"(lane));
     const int piece = piece_of(lane);
-    if constexpr (!GROUPED) xb = a.x + (int64_t)t.m0 * a.ldx;
+    xb = make_rsrc(GROUPED ? a.x : a.x + (int64_t)t.m0 * a.ldx, kNowhere - 1);
 #pragma unroll
     for (int q = 0; q < XQ; ++q) {
       const int r = (q * kWaves + wave) * 8 + lane / 8;
@@ -138,21 +136,18 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
       }
       xo[q] = row * (uint32_t)a.ldx + 16 * piece;
     }
-    wb = a.w + t.expert * a.expert_stride + t.n0 * a.row_stride;
+    wb = make_rsrc(a.w + t.expert * a.expert_stride + t.n0 * a.row_stride, kNowhere - 1);
 #pragma unroll
     for (int q = 0; q < WQ; ++q)
       wo[q] = (uint32_t)min((q * kWaves + wave) * 8 + lane / 8, a.d_out - 1 - t.n0) * (uint32_t)a.row_stride + 16 * piece;
   };
-  // a stage's transfers where d_in may end: lanes past the end take zeros for x, and for w stay inside the row
+  // a stage's transfers where d_in may end
   auto transfer_end = [&](u32x4 *buf, int k) {
-    const int piece = piece_of(lane);
-    const bool in = k + 16 * piece < a.d_in;
+    const bool in = k + 16 * piece_of(lane) < a.d_in;
 #pragma unroll
-    for (int q = 0; q < XQ; ++q)
-      to_lds(in ? xb + k + xo[q] : reinterpret_cast<const int8_t *>(&zero_piece), buf + (q * kWaves + wave) * 64);
+    for (int q = 0; q < XQ; ++q) to_lds(xb, in ? xo[q] : kNowhere, k, buf + (q * kWaves + wave) * 64);
 #pragma unroll
-    for (int q = 0; q < WQ; ++q)
-      to_lds(wb + (in ? k : -16 * piece) + wo[q], buf + BM * kPieces + (q * kWaves + wave) * 64);
+    for (int q = 0; q < WQ; ++q) to_lds(wb, in ? wo[q] : kNowhere, k, buf + BM * kPieces + (q * kWaves + wave) * 64);
   };
 
   // ---- products: a stage is two phases of 64 bytes.  A block of x's operands is overwritten
@@ -184,15 +179,8 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     for (int m = 0; m < TM; ++m) {
       multiply(0, m);
       refill(here, 1, m);
+      __builtin_amdgcn_sched_barrier(0);  // in this order: a read that is moved back is waited for too early
     }
-    // the order: products of a block, then its reads
-#pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      __builtin_amdgcn_sched_group_barrier(kSchedMfma, TN, 0);
-      if (m < TN) __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 2, 0);
-      else __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
-    }
-    __builtin_amdgcn_sched_barrier(0);
   };
   // the second phase's operands are in registers by the barrier, so that the transfers of the
   // stage after the next may overwrite this one's place
@@ -203,9 +191,6 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     __builtin_amdgcn_sched_barrier(0);
     settle();
     k += 2 * kDepth;
-    // hidden from the optimiser, which would keep a 64-bit address for every transfer
-    asm volatile("" : "+s"(k));
-    const int8_t *xk = xb + k, *wk = wb + k;
 #pragma unroll
     for (int m = 0; m < kEarly; ++m) refill(next, 0, m);
 #pragma unroll
@@ -214,11 +199,11 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
       refill(next, 0, m);
 #pragma unroll
       for (int q = 0; q < XQ; ++q)
-        if (kEarly + q * (TM - kEarly) / (XQ + WQ) == m) to_lds(xk + xo[q], here + (q * kWaves + wave) * 64);
+        if (kEarly + q * (TM - kEarly) / (XQ + WQ) == m) to_lds(xb, xo[q], k, here + (q * kWaves + wave) * 64);
 #pragma unroll
       for (int q = 0; q < WQ; ++q)
         if (kEarly + (XQ + q) * (TM - kEarly) / (XQ + WQ) == m)
-          to_lds(wk + wo[q], here + BM * kPieces + (q * kWaves + wave) * 64);
+          to_lds(wb, wo[q], k, here + BM * kPieces + (q * kWaves + wave) * 64);
       __builtin_amdgcn_sched_barrier(0);
     }
   };
