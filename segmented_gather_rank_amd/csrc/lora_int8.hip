@@ -52,18 +52,42 @@ __device__ __forceinline__ i32x4 product(u32x4 w, u32x4 x, i32x4 sum) {
   return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, w), __builtin_bit_cast(i32x4, x), sum, 0, 0, 0);
 }
 
+// An offset past the end of every buffer: a load from there gives zeros.
+constexpr uint32_t kNowhere = 0xffffffffu;
+
+// Where a lane reads a row of x from: 32 bits from x's start, or an address where x is
+// larger than that.
+template <bool WIDE> struct XRow;
+template <> struct XRow<false> {
+  uint32_t at;
+  __device__ __forceinline__ void aim(const int8_t *, int64_t offset) { at = (uint32_t)offset; }
+  __device__ __forceinline__ u32x4 load(rsrc_t x, int k, bool in) const {
+    return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(x, (int)(in ? at : kNowhere), k, 0));
+  }
+};
+template <> struct XRow<true> {
+  const int8_t *at;
+  __device__ __forceinline__ void aim(const int8_t *x, int64_t offset) { at = x + offset; }
+  __device__ __forceinline__ u32x4 load(rsrc_t, int k, bool in) const { return in ? gload16(at + k) : u32x4{0, 0, 0, 0}; }
+};
+
 // Output columns n0 .. n0 + 16 NT - 1 of rows r0 .. r0 + 16 MT - 1.
-template <typename Y, int MT, int NT, int WAVES, int AHEAD>
+template <typename Y, bool WIDE, int MT, int NT, int WAVES, int AHEAD>
 __device__ __forceinline__ void few_block(const Int8Args &a, const Rows &rows, int r0, int n0, i32x4 *lds) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, l16 = lane % 16, quarter = lane / 16;
+  static_assert(MT * NT <= WAVES, "a wave adds up one block");
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  const int l16 = lane % 16, quarter = lane / 16;
   // past the last row and column: the last one again, not stored
-  const int8_t *wp[NT], *xp[MT];
-  const int8_t *w = a.w + (int64_t)rows.expert * a.expert_stride + 16 * quarter;
+  int64_t row[MT];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) wp[n] = w + (int64_t)min(n0 + 16 * n + l16, a.d_out - 1) * a.row_stride;
+  for (int m = 0; m < MT; ++m) row[m] = rows.at(min(r0 + 16 * m + l16, rows.count - 1));
+  const rsrc_t w = make_rsrc(a.w + rows.expert * a.expert_stride + n0 * a.row_stride, kNowhere - 1);
+  const rsrc_t x = make_rsrc(a.x, kNowhere - 1);
+  uint32_t wo[NT];
 #pragma unroll
-  for (int m = 0; m < MT; ++m)
-    xp[m] = a.x + rows.x_row(rows.at(min(r0 + 16 * m + l16, rows.count - 1))) * a.ldx + 16 * quarter;
+  for (int n = 0; n < NT; ++n)
+    wo[n] = (uint32_t)min(16 * n + l16, a.d_out - 1 - n0) * (uint32_t)a.row_stride + 16 * quarter;
+  XRow<WIDE> xo[MT];
 
   i32x4 sum[MT][NT];
 #pragma unroll
@@ -72,14 +96,24 @@ __device__ __forceinline__ void few_block(const Int8Args &a, const Rows &rows, i
     for (int n = 0; n < NT; ++n) sum[m][n] = i32x4{0, 0, 0, 0};
 
   u32x4 wv[AHEAD][NT][2], xv[AHEAD][MT][2];
-  auto load = [&](int d, int step) {
-    const int k = step * kStep;
+  // a step's bytes of the weights, and of x; pieces past the end of d_in are zeros
+  auto load_w = [&](int d, int step) {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const int k = step * kStep + 64 * h;
+      const bool in = k + 16 * quarter < a.d_in;
 #pragma unroll
-      for (int n = 0; n < NT; ++n) wv[d][n][h] = gload16(wp[n] + k + 64 * h);
+      for (int n = 0; n < NT; ++n)
+        wv[d][n][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(w, (int)(in ? wo[n] : kNowhere), k, 0));
+    }
+  };
+  auto load_x = [&](int d, int step) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xv[d][m][h] = gload16(xp[m] + k + 64 * h);
+    for (int h = 0; h < 2; ++h) {
+      const int k = step * kStep + 64 * h;
+      const bool in = k + 16 * quarter < a.d_in;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xv[d][m][h] = xo[m].load(x, k, in);
     }
   };
   auto multiply = [&](int d) {
@@ -90,64 +124,61 @@ __device__ __forceinline__ void few_block(const Int8Args &a, const Rows &rows, i
 #pragma unroll
         for (int n = 0; n < NT; ++n) sum[m][n] = product(wv[d][n][h], xv[d][m][h], sum[m][n]);
   };
-  const int steps = a.d_in / kStep;
+  const int steps = (a.d_in + kStep - 1) / kStep;
 #pragma unroll
   for (int d = 0; d < AHEAD; ++d)
-    if (wave + d * WAVES < steps) load(d, wave + d * WAVES);
+    if (wave + d * WAVES < steps) load_w(d, wave + d * WAVES);
+  int64_t from[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    from[m] = rows.x_row(row[m]);
+    xo[m].aim(a.x, from[m] * a.ldx + 16 * quarter);
+  }
+#pragma unroll
+  for (int d = 0; d < AHEAD; ++d)
+    if (wave + d * WAVES < steps) load_x(d, wave + d * WAVES);
   for (int s = wave; s < steps; s += AHEAD * WAVES) {
 #pragma unroll
     for (int d = 0; d < AHEAD; ++d) {
       if (s + d * WAVES < steps) multiply(d);
-      if (s + (d + AHEAD) * WAVES < steps) load(d, s + (d + AHEAD) * WAVES);
+      if (s + (d + AHEAD) * WAVES < steps) {
+        load_w(d, s + (d + AHEAD) * WAVES);
+        load_x(d, s + (d + AHEAD) * WAVES);
+      }
     }
-  }
-  // the last bytes of d_in, a multiple of 16: pieces past the end are zeros
-  if (a.d_in % kStep && wave == steps % WAVES) {
-    const int k = steps * kStep;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const bool in = k + 64 * h + 16 * quarter < a.d_in;
-      const u32x4 none = {0, 0, 0, 0};
-#pragma unroll
-      for (int n = 0; n < NT; ++n) wv[0][n][h] = in ? gload16(wp[n] + k + 64 * h) : none;
-#pragma unroll
-      for (int m = 0; m < MT; ++m) xv[0][m][h] = in ? gload16(xp[m] + k + 64 * h) : none;
-    }
-    multiply(0);
   }
 
-  // the waves' sums together: wave w adds up the blocks w, w + WAVES, ...
+  // the waves' sums together: wave b adds up block b
   __syncthreads();  // what the workgroup's block before this one left is read
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) lds[((m * NT + n) * WAVES + wave) * 64 + lane] = sum[m][n];
   __syncthreads();
+  if (wave >= MT * NT) return;
+  const int m = wave / NT, n = wave % NT;
+  const int r = r0 + 16 * m + l16, c = n0 + 16 * n + 4 * quarter;
+  if (r >= rows.count || c >= a.d_out) return;
+  const int64_t en = (int64_t)rows.expert * a.d_out + c;
+  const int64_t to = rows.at(r);
+  f32x4 ws, bs = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int b = 0; b < MT * NT; ++b) {
-    if (b % WAVES != wave) continue;
-    const int m = b / NT, n = b % NT;
-    i32x4 t = lds[b * WAVES * 64 + lane];
-#pragma unroll
-    for (int o = 1; o < WAVES; ++o) t += lds[(b * WAVES + o) * 64 + lane];
-    const int r = r0 + 16 * m + l16, c = n0 + 16 * n + 4 * quarter;
-    if (r < rows.count && c < a.d_out) {
-      const int64_t row = rows.at(r);
-      const float xs = a.x_scale[rows.x_row(row)];
-      const int64_t en = (int64_t)rows.expert * a.d_out + c;
-      float v[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[e] = (float)t[e] * (xs * a.w_scale[en + e]);
-        if (a.bias) v[e] += a.bias[en + e];
-      }
-      store4<Y>(a.y, row * a.ldy + c, v);
-    }
+  for (int e = 0; e < 4; ++e) {
+    ws[e] = a.w_scale[en + e];
+    if (a.bias) bs[e] = a.bias[en + e];
   }
+  const float xs = a.x_scale[rows.x_row(to)];
+  i32x4 t = lds[wave * WAVES * 64 + lane];
+#pragma unroll
+  for (int o = 1; o < WAVES; ++o) t += lds[(wave * WAVES + o) * 64 + lane];
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = (float)t[e] * (xs * ws[e]) + bs[e];
+  store4<Y>(a.y, to * a.ldy + c, v);
 }
 
-template <typename Y, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void few_kernel(Int8Args a, int group0, int most) {
+template <typename Y, bool WIDE, int NT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Int8Args a, int group0, int most) {
   __shared__ i32x4 lds[4 * NT * WAVES * 64];
   const int n0 = blockIdx.x * 16 * NT;
   Rows rows{nullptr, (int)a.rows, 0, 1};
@@ -160,38 +191,49 @@ __global__ __launch_bounds__(64 * WAVES) void few_kernel(Int8Args a, int group0,
     end = min(end, r0 + 64);
   }
   for (; r0 < end; r0 += 64) {
-    if (end - r0 <= 16) few_block<Y, 1, NT, WAVES, 4>(a, rows, r0, n0, lds);
-    else if (end - r0 <= 32) few_block<Y, 2, NT, WAVES, 2>(a, rows, r0, n0, lds);
-    else few_block<Y, 4, NT, WAVES, 2>(a, rows, r0, n0, lds);
+    if (end - r0 <= 16) few_block<Y, WIDE, 1, NT, WAVES, 4>(a, rows, r0, n0, lds);
+    else if (end - r0 <= 32) few_block<Y, WIDE, 2, NT, WAVES, 2>(a, rows, r0, n0, lds);
+    else few_block<Y, WIDE, 4, NT, WAVES, 1>(a, rows, r0, n0, lds);
   }
 }
 
 // With metadata, the segments of at most `most` rows.
-template <typename Y>
+template <typename Y, bool WIDE, int NT>
 hipError_t launch_few(const Int8Args &a, int most, hipStream_t s) {
+  constexpr int kWaves = 8;
   const int64_t groups = a.meta.sorted ? std::min<int64_t>(a.rows, a.experts) + 1 : (a.rows + 63) / 64;
-  constexpr int kNT = 2, kWaves = 8;
-  const int64_t cols = (a.d_out + 16 * kNT - 1) / (16 * kNT);
+  const int64_t cols = (a.d_out + 16 * NT - 1) / (16 * NT);
   // a launch holds fewer than 2^32 threads, and 2^16 rows of its grid
   const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(32768, ((int64_t)1 << 22) / cols));
   for (int64_t g0 = 0; g0 < groups; g0 += rows) {
     const dim3 grid((unsigned)cols, (unsigned)std::min(groups - g0, rows));
-    few_kernel<Y, kNT, kWaves><<<grid, dim3(64 * kWaves), 0, s>>>(a, (int)g0, most);
+    few_kernel<Y, WIDE, NT, kWaves><<<grid, dim3(64 * kWaves), 0, s>>>(a, (int)g0, most);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
   return hipSuccess;
 }
 
+template <typename Y>
+hipError_t launch_few(const Int8Args &a, int most, bool wide, hipStream_t s) {
+  if (wide) return launch_few<Y, true, 2>(a, most, s);
+  // 16 columns a workgroup where 32 would leave CUs without one
+  const int64_t groups = a.meta.sorted ? std::min<int64_t>(a.rows, a.experts) : (a.rows + 63) / 64;
+  if (groups * a.d_out < 512 * 32) return launch_few<Y, false, 1>(a, most, s);
+  return launch_few<Y, false, 2>(a, most, s);
+}
+
 }  // namespace
 
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s) {
-  // tiles address x in 32 bits: all of it where rows are gathered, 256 rows else
-  const int64_t x_rows = a.meta.sorted ? (a.rows - 1) / a.meta.x_row_div + 1 : 256;
-  const bool tiles = a.rows > kFewRows && x_rows * a.ldx < ((int64_t)1 << 32);
+  // x is addressed in 32 bits: all of it, or in tiles of a dense batch their 256 rows
+  const int64_t x_rows = a.meta.sorted ? (a.rows - 1) / a.meta.x_row_div + 1 : a.rows;
+  const bool wide = x_rows * a.ldx >= ((int64_t)1 << 32) - 256;
+  const bool tiles = a.rows > (a.meta.sorted ? kFewRows : 512) &&
+                     (a.meta.sorted ? !wide : 256 * a.ldx < ((int64_t)1 << 32) - 256);
   const int most = tiles ? kFewRows : INT32_MAX;
   if (a.meta.sorted || !tiles) {
-    const hipError_t err = bf16 ? launch_few<uint16_t>(a, most, s) : launch_few<float>(a, most, s);
+    const hipError_t err = bf16 ? launch_few<uint16_t>(a, most, wide, s) : launch_few<float>(a, most, wide, s);
     if (err != hipSuccess) return err;
   }
   return tiles ? launch_int8_tile(a, bf16, kFewRows + 1, s) : hipSuccess;
