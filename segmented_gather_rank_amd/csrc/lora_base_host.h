@@ -43,7 +43,9 @@ struct Int8Args {
   MetaView meta;                 // sorted == NULL: dense
 };
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s);
-// Rows in tiles through LDS; with metadata, the segments of at least `fewest` rows.
+// Rows in tiles of 64; with metadata, the segments of fewest .. most rows.
+hipError_t launch_int8_mid(const Int8Args &a, bool bf16, int fewest, int most, hipStream_t s);
+// Rows in tiles of 256; with metadata, the segments of at least `fewest` rows.
 hipError_t launch_int8_tile(const Int8Args &a, bool bf16, int fewest, hipStream_t s);
 
 struct CombineArgs {

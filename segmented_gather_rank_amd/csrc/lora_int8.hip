@@ -19,6 +19,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kFewRows = 64;  // most rows of a segment (or a dense batch) that few_kernel takes
+constexpr int kMidRows = 512; // most rows that take tiles of 64
 constexpr int kStep = 128;  // bytes of d_in a step takes: two matrix instructions
 
 // The rows that a workgroup works on: a segment of the metadata, or all.
@@ -229,14 +230,18 @@ hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s) {
   // x is addressed in 32 bits: all of it, or in tiles of a dense batch their 256 rows
   const int64_t x_rows = a.meta.sorted ? (a.rows - 1) / a.meta.x_row_div + 1 : a.rows;
   const bool wide = x_rows * a.ldx >= ((int64_t)1 << 32) - 256;
-  const bool tiles = a.rows > (a.meta.sorted ? kFewRows : 512) &&
-                     (a.meta.sorted ? !wide : 256 * a.ldx < ((int64_t)1 << 32) - 256);
-  const int most = tiles ? kFewRows : INT32_MAX;
-  if (a.meta.sorted || !tiles) {
-    const hipError_t err = bf16 ? launch_few<uint16_t>(a, most, wide, s) : launch_few<float>(a, most, wide, s);
-    if (err != hipSuccess) return err;
+  const bool tiles = a.meta.sorted ? !wide : 256 * a.ldx < ((int64_t)1 << 32) - 256;
+  hipError_t err = hipSuccess;
+  if (!tiles) return bf16 ? launch_few<uint16_t>(a, INT32_MAX, wide, s) : launch_few<float>(a, INT32_MAX, wide, s);
+  if (!a.meta.sorted) {
+    if (a.rows <= kFewRows) return bf16 ? launch_few<uint16_t>(a, kFewRows, wide, s) : launch_few<float>(a, kFewRows, wide, s);
+    return a.rows <= kMidRows ? launch_int8_mid(a, bf16, 1, INT32_MAX, s) : launch_int8_tile(a, bf16, 1, s);
   }
-  return tiles ? launch_int8_tile(a, bf16, kFewRows + 1, s) : hipSuccess;
+  // by expert: who takes a segment goes by its rows, which only the device knows
+  err = bf16 ? launch_few<uint16_t>(a, kFewRows, wide, s) : launch_few<float>(a, kFewRows, wide, s);
+  if (err == hipSuccess && a.rows > kFewRows) err = launch_int8_mid(a, bf16, kFewRows + 1, kMidRows, s);
+  if (err == hipSuccess && a.rows > kMidRows) err = launch_int8_tile(a, bf16, kMidRows + 1, s);
+  return err;
 }
 
 }  // namespace lora

@@ -2,99 +2,26 @@
 // operands go through LDS.
 #include <algorithm>
 
-#include "lora_base_host.h"
+#include "lora_int8_tile.h"
 
 namespace lora {
 
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-
-constexpr int kDepth = 128;  // bytes of d_in a stage holds of every row
-constexpr int kPieces = kDepth / 16;
-
-// An offset past the end of every buffer: a lane that transfers from there gets zeros.
-constexpr uint32_t kNowhere = 0xffffffffu;
-
-struct Tile {
-  int expert, n0, m0, count, start;  // rows m0 .. of a segment of `count` rows from `start` in `sorted`
-};
-
-// Tile i of a rows x cols grid, taken `kBand` row tiles at a time, so that what is in
-// work at once reads few different rows of either operand.
-constexpr int kBand = 4;
-__device__ __forceinline__ void place(int i, int row_tiles, int col_tiles, int &m, int &n) {
-  const int band = i / (kBand * col_tiles), in = i - band * kBand * col_tiles;
-  const int high = min(kBand, row_tiles - band * kBand);
-  n = in / high;
-  m = band * kBand + in - n * high;
-}
-
-// 16 bytes a lane from `at` + k of the buffer; `to` is the wave's.  (A transfer by address
-// would count as an LDS operation too, and every wait for LDS would be one for all of them.)
-__device__ __forceinline__ void to_lds(rsrc_t from, uint32_t at, int k, u32x4 *to) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (__attribute__((address_space(3))) void *)to, 16, (int)at, k, 0, 0);
-}
-
-// Every wave's transfers to LDS have arrived, and its reads have left.  (A barrier alone
-// waits for LDS operations, not for transfers that memory still holds.)
-__device__ __forceinline__ void settle() {
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-}
-
-// LDS written by this wave is read by this wave.
-__device__ __forceinline__ void wave_sync() {
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-}
-
 template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewest) {
-  constexpr int kWaves = WM * WN, kThreads = 64 * kWaves;
+__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewest, int most) {
+  constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;          // blocks of 16 of a wave
   constexpr int XQ = BM / 8 / kWaves, WQ = BN / 8 / kWaves;    // transfers of 8 rows of a wave and stage
   __shared__ u32x4 buf0[(BM + BN) * kPieces], buf1[(BM + BN) * kPieces];
-  __shared__ int32_t ids[2][GROUPED ? BM : 1];
-  __shared__ __align__(16) float columns[kWaves][2][TN * 16];
+  __shared__ __align__(16) float columns[kWaves][2 * TN * 16];
   extern __shared__ __align__(16) char table[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane % 16, quarter = lane / 16;
-  const int col_tiles = (a.d_out + BN - 1) / BN;
-  const SegTable tb = seg_table_at(table, a.experts);
-  int tiles;
-  if constexpr (GROUPED) {
-    build_items(a.meta, tb, true, [&](int count, int) { return count >= fewest ? (count + BM - 1) / BM * col_tiles : 0; });
-    tiles = uniform_value(tb.scal[2]);
-  } else {
-    tiles = (int)((a.rows + BM - 1) / BM) * col_tiles;
-  }
-  // every XCD takes a run of neighbouring tiles
-  const int share = (tiles + 7) / 8, per = gridDim.x / 8;
-  const int last = min(tiles, (int)(blockIdx.x % 8 + 1) * share);
-  int index = blockIdx.x % 8 * share + blockIdx.x / 8;
-  if (index >= last) return;
-
-  auto tile_at = [&](int i) {
-    Tile t;
-    int m, n;
-    if constexpr (GROUPED) {
-      const int s = find_item_segment(tb, i), at = tb.scal[1] + s;
-      t.expert = uniform_value(tb.slot[at]);
-      t.count = uniform_value(tb.count[at]);
-      t.start = uniform_value(tb.start[at]);
-      const int from = s ? tb.item_end[s - 1] : 0;
-      place(uniform_value(i - from), (t.count + BM - 1) / BM, col_tiles, m, n);
-    } else {
-      t.expert = t.start = 0;
-      t.count = (int)a.rows;
-      place(i, (t.count + BM - 1) / BM, col_tiles, m, n);
-    }
-    t.m0 = m * BM;
-    t.n0 = n * BN;
-    return t;
-  };
+  const TileList<GROUPED, BM, BN> list(a, table, fewest, most);
+  int index = list.index;
+  if (index >= list.last) return;
 
   // ---- transfers of the tile that `aim` was called for
   rsrc_t xb, wb;                                  // from where its rows of either operand are counted
@@ -103,37 +30,24 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   // A transfer takes 8 rows, 8 (wave + kWaves q) and on.
   static_assert(kWaves % 2 == 0, "the place of a lane's piece is the same in all transfers");
   auto piece_of = [&](int lane) { return (lane % 8) ^ (4 * (wave % 2) + lane / 16); };
-  constexpr int kIds = (BM + kThreads - 1) / kThreads;
-  int32_t pending[kIds];
-  auto fetch_ids = [&](const Tile &t) {
-    if constexpr (GROUPED) {
+  int32_t row_of[XQ];                             // rows that this lane will transfer, of the tile that was looked up
+  auto look_up = [&](const Tile &t) {
 #pragma unroll
-      for (int q = 0; q < kIds; ++q)
-        pending[q] = a.meta.sorted[t.start + min(t.m0 + q * kThreads + (int)threadIdx.x, t.count - 1)];
+    for (int q = 0; q < XQ; ++q) {
+      const int r = min(t.m0 + (q * kWaves + wave) * 8 + lane / 8, t.count - 1);
+      if constexpr (GROUPED) row_of[q] = a.meta.sorted[t.start + r];
+      else row_of[q] = r - t.m0;
     }
   };
-  auto keep_ids = [&](int slot) {
-    if constexpr (GROUPED) {
-#pragma unroll
-      for (int q = 0; q < kIds; ++q)
-        if (q * kThreads + (int)threadIdx.x < BM) ids[slot][q * kThreads + threadIdx.x] = pending[q];
-    }
-  };
-  auto aim = [&](const Tile &t, int slot) {
-    int lane = threadIdx.x % 64;  // hidden, as in `finish` below
+  auto aim = [&](const Tile &t) {
+    int lane = threadIdx.x % 64;  // hidden, as in `store_tile`
     asm volatile("" : "+v"(lane));
     const int piece = piece_of(lane);
     xb = make_rsrc(GROUPED ? a.x : a.x + (int64_t)t.m0 * a.ldx, kNowhere - 1);
 #pragma unroll
     for (int q = 0; q < XQ; ++q) {
-      const int r = (q * kWaves + wave) * 8 + lane / 8;
-      uint32_t row;
-      if constexpr (GROUPED) {
-        row = (uint32_t)ids[slot][r];
-        if (a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
-      } else {
-        row = (uint32_t)min(r, t.count - 1 - t.m0);
-      }
+      uint32_t row = (uint32_t)row_of[q];
+      if (GROUPED && a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
       xo[q] = row * (uint32_t)a.ldx + 16 * piece;
     }
     wb = make_rsrc(a.w + t.expert * a.expert_stride + t.n0 * a.row_stride, kNowhere - 1);
@@ -223,89 +137,17 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     }
   };
 
-  // ---- y of the finished tile, through LDS so that whole lines are stored: 32 rows at a time
-  auto finish = [&](const Tile &t, int slot, u32x4 *scratch) {
-    constexpr int kRowPieces = TN * 16 * (int)sizeof(Y) / 16;
-    u32x4 *mine = scratch + wave * 32 * kRowPieces;
-    // hidden from the optimiser, which would keep what follows from it in registers all through the products
-    int lane = threadIdx.x % 64;
-    asm volatile("" : "+v"(lane));
-    const int l16 = lane % 16, quarter = lane / 16;
-    // the pieces of a row change places by its number, so that neither the writes nor the reads meet in a bank
-    auto turn = [&](int row) { return kRowPieces >= 16 ? row % kRowPieces : row * kRowPieces / 16 % kRowPieces; };
-    const int c0 = t.n0 + wn * TN * 16;
-    // the wave's columns' scales and bias: fetched once, read from LDS as they are needed
-    float *ws = columns[wave][0], *bs = columns[wave][1];
-    for (int c = lane; c < TN * 16; c += 64) {
-      const int64_t at = (int64_t)t.expert * a.d_out + min(c0 + c, a.d_out - 1);
-      ws[c] = a.w_scale[at];
-      bs[c] = a.bias ? a.bias[at] : 0.f;
-    }
-    wave_sync();
-#pragma unroll
-    for (int m = 0; m < TM; m += 2) {
-      const int r = (wm * TM + m) * 16;           // of the tile
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        uint32_t row = (uint32_t)min(t.m0 + r + 16 * b + l16, t.count - 1);
-        if constexpr (GROUPED) {
-          row = (uint32_t)ids[slot][r + 16 * b + l16];
-          if (a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
-        }
-        const float xs = a.x_scale[row];
-        u32x4 *line = mine + (16 * b + l16) * kRowPieces;
-        const int places = turn(16 * b + l16);
-#pragma unroll
-        for (int n = 0; n < TN; ++n) {
-          // columns 16 n + 4 quarter .. + 3 of the row
-          const f32x4 w4 = *reinterpret_cast<const f32x4 *>(ws + 16 * n + 4 * quarter);
-          const f32x4 b4 = *reinterpret_cast<const f32x4 *>(bs + 16 * n + 4 * quarter);
-          float v[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = (float)sum[m + b][n][e] * (xs * w4[e]) + b4[e];
-          if constexpr (sizeof(Y) == 2) {
-            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-            u32x2 *to = reinterpret_cast<u32x2 *>(line + ((2 * n + quarter / 2) ^ places));
-            to[quarter % 2] = u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
-          } else {
-            line[(4 * n + quarter) ^ places] = __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]});
-          }
-        }
-      }
-      wave_sync();
-      constexpr int kRowsAtOnce = 64 / kRowPieces;
-#pragma unroll
-      for (int q = 0; q < 32 / kRowsAtOnce; ++q) {
-        const int lr = q * kRowsAtOnce + lane / kRowPieces, p = lane % kRowPieces;
-        const u32x4 v = mine[lr * kRowPieces + (p ^ turn(lr))];
-        const int c = c0 + p * (16 / (int)sizeof(Y));
-        if (t.m0 + r + lr < t.count && c < a.d_out) {
-          int64_t to = t.m0 + r + lr;
-          if constexpr (GROUPED) to = (uint32_t)ids[slot][r + lr];
-          gstore16(a.y + (to * a.ldy + c) * (int64_t)sizeof(Y), v);
-        }
-      }
-      wave_sync();
-    }
-  };
-
-  Tile now = tile_at(index), then;
-  int slot = 0;
-  if constexpr (GROUPED) {
-    fetch_ids(now);
-    keep_ids(0);
-    __syncthreads();
-  }
-  aim(now, 0);
+  Tile now = list.at(index), then;
+  look_up(now);
+  aim(now);
   transfer_end(buf0, 0);
   while (true) {
-    const bool follows = index + per < last;
+    const bool follows = index + list.per < list.last;
     if (follows) {
-      then = tile_at(index + per);
-      fetch_ids(then);
+      then = list.at(index + list.per);
+      look_up(then);
     }
     settle();         // the first stage is there, and the last tile's scratch is free
-    if (follows) keep_ids(slot ^ 1);
     if (stages > 1) transfer_end(buf1, kDepth);
 #pragma unroll
     for (int m = 0; m < TM; ++m)
@@ -327,14 +169,15 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
     __syncthreads();  // every wave has read its last stage
     // the next tile's first stage arrives while this one's results leave
     if (follows) {
-      aim(then, slot ^ 1);
+      aim(then);
       transfer_end(buf0, 0);
     }
-    finish(now, slot, buf1);
+    constexpr int kRowPieces = TN * 16 * (int)sizeof(Y) / 16;
+    store_tile<Y, GROUPED, TM, TN>(a, now, sum, wm * TM * 16, now.n0 + wn * TN * 16, buf1 + wave * 32 * kRowPieces,
+                                   columns[wave]);
     if (!follows) return;
     now = then;
-    slot ^= 1;
-    index += per;
+    index += list.per;
   }
 }
 
@@ -347,7 +190,7 @@ hipError_t launch_as(const Int8Args &a, int fewest, hipStream_t s) {
   const int64_t cols = (a.d_out + BN - 1) / BN;
   const int64_t bound = ((a.rows + BM - 1) / BM + (GROUPED ? std::min<int64_t>(a.experts, a.rows) : 0)) * cols;
   const int grid = xcd_grid(bound, resident_groups(cache, f, 64 * WM * WN, lds));
-  tile_kernel<Y, GROUPED, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), lds, s>>>(a, fewest);
+  tile_kernel<Y, GROUPED, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), lds, s>>>(a, fewest, INT32_MAX);
   return hipGetLastError();
 }
 
