@@ -758,34 +758,34 @@ SCORES = {"softmax": 0, "sigmoid": 1}
 ACTIVATIONS = {None: 0, "silu_mul": 1}
 
 
-def _together(device, **tensors) -> None:
-    """Every tensor that is given lies on `device`."""
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+def _apart(device: int, *tensors) -> None:
+    """Refuses tensors that do not lie on the device of that index."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on {t.device} and on device {device}")
 
 
-def _at(device):
-    """The device of a call's tensors made current: launches go to the current one."""
-    if device.type != "cuda" or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+def _elsewhere(device: int) -> bool:
+    """Whether a call's tensors lie on another device than the current one, to which launches go."""
+    return device >= 0 and device != torch._C._cuda_getDevice()
 
 
-def _rows(t: torch.Tensor, name: str, dtype, rows: int | None = None, cols: int | None = None) -> tuple:
-    """Address and row stride of a matrix of `rows` rows of at least `cols` columns."""
-    if t.dim() != 2 or t.dtype != dtype or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a matrix of {dtype} with unit column stride")
-    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{name} must be {rows} x {cols}, not {tuple(t.shape)}")
+def _rows(t: torch.Tensor, name: str, dtype, rows: int, cols: int) -> tuple:
+    """Address and row stride of a matrix of rows x cols."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != rows or shape[1] != cols or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} of {rows} x {cols}, not {t.dtype} of {tuple(shape)}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
     # the stride of a single row says nothing
-    return (_dev(t, name) if t.numel() else None), (t.stride(0) if t.shape[0] > 1 else t.shape[1])
+    return (_dev(t, name) if rows and cols else None), (ld if rows > 1 else cols)
 
 
 def _vector(t: torch.Tensor, name: str, dtype, shape) -> int | None:
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} of {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
-    return _dev(t, name) if t.numel() else None
+    return _dev(t, name)
 
 
 class Routing:
@@ -810,19 +810,21 @@ def lora_moe_route(logits: torch.Tensor, routing: Routing, topk_ids: torch.Tenso
     any stride) -> topk_ids int32 [T][topk], as lora_prepare_moe_meta takes them, and
     weights float32 [T][topk]; outputs that are not given are allocated on the stream of
     the call."""
-    if logits.dim() != 2 or logits.shape[1] != routing.num_experts or (routing.num_experts > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be [T][experts] with unit column stride")
-    T, K, device = logits.shape[0], routing.topk, logits.device
-    _together(device, bias=routing.bias, topk_ids=topk_ids, weights=weights)
-    with _at(device):
-        if topk_ids is None:
-            topk_ids = _empty_for(stream, (T, K), torch.int32, device)
-        if weights is None:
-            weights = _empty_for(stream, (T, K), torch.float32, device)
-        st = _lib.lora_moe_route(routing.ref, _dev(logits, "logits") if T else None,
-                                 logits.stride(0) if T > 1 else routing.num_experts, T, _dtype(logits),
-                                 _vector(topk_ids, "topk_ids", torch.int32, (T, K)),
-                                 _vector(weights, "weights", torch.float32, (T, K)), _stream_handle(stream))
+    device = logits.get_device()
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return lora_moe_route(logits, routing, topk_ids, weights, stream)
+    if logits.dim() != 2:
+        raise ValueError("logits must be [T][experts]")
+    T, K = logits.shape[0], routing.topk
+    ptr, ld = _rows(logits, "logits", logits.dtype, T, routing.num_experts)
+    if topk_ids is None:
+        topk_ids = _empty_for(stream, (T, K), torch.int32, logits.device)
+    if weights is None:
+        weights = _empty_for(stream, (T, K), torch.float32, logits.device)
+    _apart(device, routing.bias, topk_ids, weights)
+    st = _lib.lora_moe_route(routing.ref, ptr, ld, T, _dtype(logits), _vector(topk_ids, "topk_ids", torch.int32, (T, K)),
+                             _vector(weights, "weights", torch.float32, (T, K)), _stream_handle(stream))
     _check("lora_moe_route", st)
     return topk_ids, weights
 
@@ -835,27 +837,32 @@ def lora_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.T
     act, if given, takes in x's type.  meta: only the rows that it gives a key.  q and
     scale that are not given are allocated on the stream of the call (with meta, rows
     without a key hold anything)."""
+    device = x.get_device()
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return lora_quantize(x, q, scale, activation, act, meta, stream)
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}")
-    xp, ldx = _rows(x, "x", x.dtype)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][width]")
     rows, width = x.shape
+    xp, ldx = _rows(x, "x", x.dtype, rows, width)
     if activation:
         if width % 2:
             raise ValueError("x must be gate | up, of one width")
         width //= 2
     elif act is not None:
         raise ValueError("act goes with an activation")
-    _together(x.device, q=q, scale=scale, act=act, meta=None if meta is None else meta.workspace)
-    with _at(x.device):
-        if q is None:
-            q = _empty_for(stream, (rows, width), torch.int8, x.device)
-        if scale is None:
-            scale = _empty_for(stream, (rows,), torch.float32, x.device)
-        qp, ldq = _rows(q, "q", torch.int8, rows, width)
-        ap, lda = (None, 0) if act is None else _rows(act, "act", x.dtype, rows, width)
-        st = _lib.lora_quantize(xp, ldx, rows, width, _dtype(x), ACTIVATIONS[activation],
-                                None if meta is None else C.byref(meta.c), qp, ldq,
-                                _vector(scale, "scale", torch.float32, (rows,)), ap, lda, _stream_handle(stream))
+    if q is None:
+        q = _empty_for(stream, (rows, width), torch.int8, x.device)
+    if scale is None:
+        scale = _empty_for(stream, (rows,), torch.float32, x.device)
+    _apart(device, q, scale, act, None if meta is None else meta.workspace)
+    qp, ldq = _rows(q, "q", torch.int8, rows, width)
+    ap, lda = (None, 0) if act is None else _rows(act, "act", x.dtype, rows, width)
+    st = _lib.lora_quantize(xp, ldx, rows, width, _dtype(x), ACTIVATIONS[activation],
+                            None if meta is None else C.byref(meta.c), qp, ldq,
+                            _vector(scale, "scale", torch.float32, (rows,)), ap, lda, _stream_handle(stream))
     _check("lora_quantize", st)
     return q, scale
 
@@ -869,7 +876,7 @@ class Int8Weight:
         if w.dim() not in (2, 3) or w.dtype != torch.int8 or w.stride(-1) != 1:
             raise ValueError("w must be int8 [d_out][d_in] or [experts][d_out][d_in] with contiguous rows")
         shape = w.shape[:-1]
-        _together(w.device, scale=scale, bias=bias)
+        _apart(w.get_device(), scale, bias)
         self.w, self.scale, self.bias = w, scale, bias
         self.num_experts, self.d_out, self.d_in = (w.shape[0] if w.dim() == 3 else 1), w.shape[-2], w.shape[-1]
         self.c = lora_int8_weight(_dev(w, "w"), w.stride(0) if w.dim() == 3 and len(w) > 1 else 0,
@@ -893,26 +900,30 @@ def lora_int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, weight: Int8Weight,
     lora_quantize leaves it.  meta: metadata of the output's rows, keyed by expert (row i
     of the output reads row i / x_row_div of x; rows without a key are not written).  An
     out that is not given is allocated on the stream of the call, of type dtype."""
-    xp, ldx = _rows(x, "x", torch.int8, None, weight.d_in)
-    div = 1 if meta is None else int(meta.c.x_row_div)
-    rows = x.shape[0] if meta is None else meta.num_tokens
-    if x.shape[0] != -(-rows // div):
-        raise ValueError(f"x must have {-(-rows // div)} rows, one for {div} of the metadata's")
-    device = x.device
-    _together(device, x_scale=x_scale, w=weight.w, out=out, workspace=workspace,
-              meta=None if meta is None else meta.workspace)
-    with _at(device):
-        if out is None:
-            out = _empty_for(stream, (rows, weight.d_out), dtype, device)
-        yp, ldy = _rows(out, "out", out.dtype, rows, weight.d_out)
+    device = x.get_device()
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return lora_int8_matmul(x, x_scale, weight, out, meta, dtype, workspace, stream)
+    if x.dim() != 2:
+        raise ValueError("x must be [rows][d_in]")
+    x_rows = rows = x.shape[0]
+    if meta is not None:
+        rows, div = meta.num_tokens, int(meta.c.x_row_div)
+        if x_rows != -(-rows // div):
+            raise ValueError(f"x must have {-(-rows // div)} rows, one for {div} of the metadata's")
+    xp, ldx = _rows(x, "x", torch.int8, x_rows, weight.d_in)
+    if out is None:
+        out = _empty_for(stream, (rows, weight.d_out), dtype, x.device)
+    if workspace is None:
         need = lora_int8_matmul_workspace_bytes(rows, weight)
-        if workspace is None and need:
-            workspace = _empty_for(stream, need, torch.uint8, device)
-        st = _lib.lora_int8_matmul(None if meta is None else C.byref(meta.c), xp, ldx,
-                                   _vector(x_scale, "x_scale", torch.float32, (x.shape[0],)), rows, weight.ref, yp, ldy,
-                                   _dtype(out), None if workspace is None else _dev(workspace, "workspace"),
-                                   0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                   _stream_handle(stream))
+        if need:
+            workspace = _empty_for(stream, need, torch.uint8, x.device)
+    _apart(device, x_scale, weight.w, out, workspace, None if meta is None else meta.workspace)
+    yp, ldy = _rows(out, "out", out.dtype, rows, weight.d_out)
+    st = _lib.lora_int8_matmul(None if meta is None else C.byref(meta.c), xp, ldx,
+                               _vector(x_scale, "x_scale", torch.float32, (x_rows,)), rows, weight.ref, yp, ldy,
+                               _dtype(out), None if workspace is None else _dev(workspace, "workspace"),
+                               0 if workspace is None else workspace.nbytes, _stream_handle(stream))
     _check("lora_int8_matmul", st)
     return out
 
@@ -923,11 +934,15 @@ def lora_moe_combine(y: torch.Tensor, weights: torch.Tensor, topk_ids: torch.Ten
     """out[t] = add[t] + sum of weights[t][j] * y[t * topk + j] over the choices whose
     expert is local (as in lora_prepare_moe_meta; without a map ids below
     num_local_experts, by default all).  add may be out itself."""
-    if topk_ids.dim() != 2:
-        raise ValueError("topk_ids must be [T][topk]")
+    device = y.get_device()
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return lora_moe_combine(y, weights, topk_ids, out, num_experts, num_local_experts, expert_map, add, stream)
+    if topk_ids.dim() != 2 or y.dim() != 2:
+        raise ValueError("topk_ids must be [T][topk], y [T * topk][width]")
     T, K = topk_ids.shape
-    yp, ldy = _rows(y, "y", y.dtype, T * K)
-    width, device = y.shape[1], y.device
+    width = y.shape[1]
+    yp, ldy = _rows(y, "y", y.dtype, T * K, width)
     if expert_map is not None:
         if num_local_experts is None:
             raise ValueError("an expert_map needs num_local_experts")
@@ -937,17 +952,16 @@ def lora_moe_combine(y: torch.Tensor, weights: torch.Tensor, topk_ids: torch.Ten
         num_experts = num_local_experts if num_local_experts is not None else 0x7fffffff
     if num_local_experts is None:
         num_local_experts = num_experts
-    _together(device, weights=weights, topk_ids=topk_ids, out=out, expert_map=expert_map, add=add)
-    with _at(device):
-        if out is None:
-            out = _empty_for(stream, (T, width), y.dtype, device)
-        op, ldout = _rows(out, "out", y.dtype, T, width)
-        ap, ldadd = (None, 0) if add is None else _rows(add, "add", y.dtype, T, width)
-        st = _lib.lora_moe_combine(
-            yp, ldy, width, _dtype(y), _vector(topk_ids, "topk_ids", torch.int32, (T, K)),
-            _vector(weights, "weights", torch.float32, (T, K)), T, K, num_experts, num_local_experts,
-            None if expert_map is None else _vector(expert_map, "expert_map", torch.int32, (num_experts,)), ap, ldadd,
-            op, ldout, _stream_handle(stream))
+    if out is None:
+        out = _empty_for(stream, (T, width), y.dtype, y.device)
+    _apart(device, weights, topk_ids, out, expert_map, add)
+    op, ldout = _rows(out, "out", y.dtype, T, width)
+    ap, ldadd = (None, 0) if add is None else _rows(add, "add", y.dtype, T, width)
+    st = _lib.lora_moe_combine(
+        yp, ldy, width, _dtype(y), _vector(topk_ids, "topk_ids", torch.int32, (T, K)),
+        _vector(weights, "weights", torch.float32, (T, K)), T, K, num_experts, num_local_experts,
+        None if expert_map is None else _vector(expert_map, "expert_map", torch.int32, (num_experts,)), ap, ldadd, op, ldout,
+        _stream_handle(stream))
     _check("lora_moe_combine", st)
     return out
 
