@@ -43,10 +43,31 @@ struct Int8Args {
   MetaView meta;                 // sorted == NULL: dense
 };
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s);
-// Rows in tiles of 64; with metadata, the segments of fewest .. most rows.
-hipError_t launch_int8_mid(const Int8Args &a, bool bf16, int fewest, int most, hipStream_t s);
-// Rows in tiles of 256; with metadata, the segments of at least `fewest` rows.
-hipError_t launch_int8_tile(const Int8Args &a, bool bf16, int fewest, hipStream_t s);
+// A dense batch in tiles of 64 rows.
+hipError_t launch_int8_mid(const Int8Args &a, bool bf16, hipStream_t s);
+// A dense batch in tiles of 256 rows; by expert, the segments that are not few_kernel's.
+hipError_t launch_int8_tile(const Int8Args &a, bool bf16, hipStream_t s);
+
+// By expert, rows decide who takes a segment, and only the device knows them.  Every kernel
+// that may be the one asks the same rule, whose answers follow from the metadata's counts:
+//   few   most rows of a segment that few_kernel takes: 64 in a decode step (16 rows a
+//         segment or fewer on average), and where tiles would not fill the chip: it splits
+//         d_in over a workgroup's waves, which answers soonest; else 16
+//   large whether the others take tiles of 256, else of 128: from 160 rows a segment on.
+//         (Long and short segments in tiles of their own, one kernel after the other, are
+//         slower than either for all: 113 rows a segment on average 178 us for 165, all in
+//         tiles of 256: 169; 226 rows 240 us for 207.)
+constexpr int kFewRows = 64;
+struct ExpertRule {
+  int few;
+  bool large;
+  __device__ __forceinline__ ExpertRule(const MetaView &m, int d_out) {
+    const int none = m.info[3];                   // rows without a key come first, as a segment of their own
+    const int64_t segments = m.info[0] - (none > 0), rows = m.T - none;
+    few = rows > 16 * segments && segments * ((d_out + 127) / 128) >= 512 ? 16 : kFewRows;
+    large = rows > 160 * segments;
+  }
+};
 
 struct CombineArgs {
   const char *y, *add;           // add: NULL or rows

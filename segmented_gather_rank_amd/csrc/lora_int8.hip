@@ -18,8 +18,7 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kFewRows = 64;  // most rows of a segment (or a dense batch) that few_kernel takes
-constexpr int kMidRows = 512; // most rows that take tiles of 64
+constexpr int kMidRows = 512; // most rows of a dense batch that take tiles of 64
 constexpr int kStep = 128;  // bytes of d_in a step takes: two matrix instructions
 
 // The rows that a workgroup works on: a segment of the metadata, or all.
@@ -179,14 +178,14 @@ __device__ __forceinline__ void few_block(const Int8Args &a, const Rows &rows, i
 }
 
 template <typename Y, bool WIDE, int NT, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Int8Args a, int group0, int most) {
+__global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Int8Args a, int group0, bool all) {
   __shared__ i32x4 lds[4 * NT * WAVES * 64];
   const int n0 = blockIdx.x * 16 * NT;
   Rows rows{nullptr, (int)a.rows, 0, 1};
   int r0 = 0, end = rows.count;
   if (a.meta.sorted) {
     rows = segment(a, group0 + blockIdx.y);
-    end = rows.count <= most ? rows.count : 0;
+    end = all || rows.count <= ExpertRule(a.meta, a.d_out).few ? rows.count : 0;
   } else {
     r0 = (group0 + blockIdx.y) * 64;
     end = min(end, r0 + 64);
@@ -198,9 +197,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void few_kernel(Int8Args a, int grou
   }
 }
 
-// With metadata, the segments of at most `most` rows.
+// With metadata, all segments or those of few rows.
 template <typename Y, bool WIDE, int NT>
-hipError_t launch_few(const Int8Args &a, int most, hipStream_t s) {
+hipError_t launch_few(const Int8Args &a, bool all, hipStream_t s) {
   constexpr int kWaves = 8;
   const int64_t groups = a.meta.sorted ? std::min<int64_t>(a.rows, a.experts) + 1 : (a.rows + 63) / 64;
   const int64_t cols = (a.d_out + 16 * NT - 1) / (16 * NT);
@@ -208,7 +207,7 @@ hipError_t launch_few(const Int8Args &a, int most, hipStream_t s) {
   const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(32768, ((int64_t)1 << 22) / cols));
   for (int64_t g0 = 0; g0 < groups; g0 += rows) {
     const dim3 grid((unsigned)cols, (unsigned)std::min(groups - g0, rows));
-    few_kernel<Y, WIDE, NT, kWaves><<<grid, dim3(64 * kWaves), 0, s>>>(a, (int)g0, most);
+    few_kernel<Y, WIDE, NT, kWaves><<<grid, dim3(64 * kWaves), 0, s>>>(a, (int)g0, all);
     const hipError_t err = hipGetLastError();
     if (err != hipSuccess) return err;
   }
@@ -216,12 +215,12 @@ hipError_t launch_few(const Int8Args &a, int most, hipStream_t s) {
 }
 
 template <typename Y>
-hipError_t launch_few(const Int8Args &a, int most, bool wide, hipStream_t s) {
-  if (wide) return launch_few<Y, true, 2>(a, most, s);
+hipError_t launch_few(const Int8Args &a, bool all, bool wide, hipStream_t s) {
+  if (wide) return launch_few<Y, true, 2>(a, all, s);
   // 16 columns a workgroup where 32 would leave CUs without one
   const int64_t groups = a.meta.sorted ? std::min<int64_t>(a.rows, a.experts) : (a.rows + 63) / 64;
-  if (groups * a.d_out < 512 * 32) return launch_few<Y, false, 1>(a, most, s);
-  return launch_few<Y, false, 2>(a, most, s);
+  if (groups * a.d_out < 512 * 32) return launch_few<Y, false, 1>(a, all, s);
+  return launch_few<Y, false, 2>(a, all, s);
 }
 
 }  // namespace
@@ -231,17 +230,12 @@ hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s) {
   const int64_t x_rows = a.meta.sorted ? (a.rows - 1) / a.meta.x_row_div + 1 : a.rows;
   const bool wide = x_rows * a.ldx >= ((int64_t)1 << 32) - 256;
   const bool tiles = a.meta.sorted ? !wide : 256 * a.ldx < ((int64_t)1 << 32) - 256;
-  hipError_t err = hipSuccess;
-  if (!tiles) return bf16 ? launch_few<uint16_t>(a, INT32_MAX, wide, s) : launch_few<float>(a, INT32_MAX, wide, s);
-  if (!a.meta.sorted) {
-    if (a.rows <= kFewRows) return bf16 ? launch_few<uint16_t>(a, kFewRows, wide, s) : launch_few<float>(a, kFewRows, wide, s);
-    return a.rows <= kMidRows ? launch_int8_mid(a, bf16, 1, INT32_MAX, s) : launch_int8_tile(a, bf16, 1, s);
+  if (!tiles || a.meta.sorted || a.rows <= kFewRows) {
+    const hipError_t err = bf16 ? launch_few<uint16_t>(a, !tiles, wide, s) : launch_few<float>(a, !tiles, wide, s);
+    if (err != hipSuccess || !tiles || a.rows <= 16 || (!a.meta.sorted && a.rows <= kFewRows)) return err;
   }
-  // by expert: who takes a segment goes by its rows, which only the device knows
-  err = bf16 ? launch_few<uint16_t>(a, kFewRows, wide, s) : launch_few<float>(a, kFewRows, wide, s);
-  if (err == hipSuccess && a.rows > kFewRows) err = launch_int8_mid(a, bf16, kFewRows + 1, kMidRows, s);
-  if (err == hipSuccess && a.rows > kMidRows) err = launch_int8_tile(a, bf16, kMidRows + 1, s);
-  return err;
+  if (!a.meta.sorted && a.rows <= kMidRows) return launch_int8_mid(a, bf16, s);
+  return launch_int8_tile(a, bf16, s);
 }
 
 }  // namespace lora

@@ -14,45 +14,31 @@ namespace lora {
 
 namespace {
 
-template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN, 2) void mid_kernel(Int8Args a, int fewest, int most) {
+template <typename Y, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN, 2) void mid_kernel(Int8Args a) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;          // blocks of 16 of a wave
   constexpr int XQ = BM / 8 / kWaves, WQ = BN / 8 / kWaves;    // transfers of 8 rows of a wave and stage
   static_assert(kWaves % 2 == 0, "a lane's piece is the same in all transfers");
   __shared__ u32x4 buf0[(BM + BN) * kPieces], buf1[(BM + BN) * kPieces];
   __shared__ __align__(16) float columns[kWaves][2 * TN * 16];
-  extern __shared__ __align__(16) char table[];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane % 16, quarter = lane / 16;
-  const TileList<GROUPED, BM, BN> list(a, table, fewest, most);
+  const TileList<false, BM, BN> list(a, nullptr);
   if (list.index >= list.last) return;
 
   // ---- what is loaded: a tile at byte `lk` of d_in, then the next one of the list
   int loads = list.index, lk = 0;
-  Tile next;                                  // the tile after it, if there is one
-  int32_t row_of[XQ];                         // and the rows of it that this lane will load, on their way
   rsrc_t xb, wb;                              // from where the loaded tile's rows of either operand are counted
   uint32_t xo[XQ], wo[WQ];                    // bytes from there to the piece of its row that a lane loads
   const int piece = (lane % 8) ^ (4 * (wave % 2) + lane / 16);
-  auto look_up = [&](const Tile &t) {
-#pragma unroll
-    for (int q = 0; q < XQ; ++q) {
-      const int r = min(t.m0 + (q * kWaves + wave) * 8 + lane / 8, t.count - 1);
-      if constexpr (GROUPED) row_of[q] = a.meta.sorted[t.start + r];
-      else row_of[q] = r - t.m0;
-    }
-  };
   auto aim = [&](const Tile &t) {
-    xb = make_rsrc(GROUPED ? a.x : a.x + (int64_t)t.m0 * a.ldx, kNowhere - 1);
+    xb = make_rsrc(a.x + (int64_t)t.m0 * a.ldx, kNowhere - 1);
 #pragma unroll
-    for (int q = 0; q < XQ; ++q) {
-      uint32_t row = (uint32_t)row_of[q];
-      if (GROUPED && a.meta.x_row_div != 1) row /= (uint32_t)a.meta.x_row_div;
-      xo[q] = row * (uint32_t)a.ldx + 16 * piece;
-    }
-    wb = make_rsrc(a.w + t.expert * a.expert_stride + t.n0 * a.row_stride, kNowhere - 1);
+    for (int q = 0; q < XQ; ++q)
+      xo[q] = (uint32_t)min((q * kWaves + wave) * 8 + lane / 8, t.count - 1 - t.m0) * (uint32_t)a.ldx + 16 * piece;
+    wb = make_rsrc(a.w + t.n0 * a.row_stride, kNowhere - 1);
 #pragma unroll
     for (int q = 0; q < WQ; ++q)
       wo[q] = (uint32_t)min((q * kWaves + wave) * 8 + lane / 8, a.d_out - 1 - t.n0) * (uint32_t)a.row_stride + 16 * piece;
@@ -81,11 +67,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mid_kernel(Int8Args a, int fe
     if (lk < a.d_in || loads >= list.last) return;
     lk = 0;
     loads += list.per;
-    if (loads >= list.last) return;
-    aim(next);
-    if (loads + list.per >= list.last) return;
-    next = list.at(loads + list.per);
-    look_up(next);
+    if (loads < list.last) aim(list.at(loads));
   };
 
   // ---- products, as in the large tiles
@@ -132,7 +114,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mid_kernel(Int8Args a, int fe
     if (left > 0 || index >= list.last) return;
     constexpr int kRowPieces = TN * 16 * (int)sizeof(Y) / 16;
     static_assert(kWaves * 32 * kRowPieces <= (BM + BN) * kPieces, "the waves' rows fit the stage");
-    store_tile<Y, GROUPED, TM, TN>(a, now, sum, wm * TM * 16, now.n0 + wn * TN * 16, here + wave * 32 * kRowPieces,
+    store_tile<Y, false, TM, TN>(a, now, sum, wm * TM * 16, now.n0 + wn * TN * 16, here + wave * 32 * kRowPieces,
                                    columns[wave]);
     __syncthreads();  // the waves' scratch is free
     index += list.per;
@@ -142,12 +124,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mid_kernel(Int8Args a, int fe
     left = a.d_in;
   };
 
-  look_up(now);
   aim(now);
-  if (loads + list.per < list.last) {
-    next = list.at(loads + list.per);
-    look_up(next);
-  }
   fetch(0);
   advance();
   fetch(1);
@@ -168,29 +145,21 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void mid_kernel(Int8Args a, int fe
   }
 }
 
-template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
-hipError_t launch_as(const Int8Args &a, int fewest, int most, hipStream_t s) {
-  static std::atomic<int> cache[2][kMaxDevices];
-  const size_t lds = GROUPED ? seg_table_bytes(a.experts) : 0;
-  const void *f = reinterpret_cast<const void *>(&mid_kernel<Y, GROUPED, BM, BN, WM, WN>);
-  const int64_t cols = (a.d_out + BN - 1) / BN;
-  const int64_t bound = ((a.rows + BM - 1) / BM + (GROUPED ? std::min<int64_t>(a.experts, a.rows) : 0)) * cols;
-  // (a long table leaves a CU room for one workgroup)
-  const int grid = xcd_grid(bound, resident_groups(cache[a.experts > 256], f, 64 * WM * WN, GROUPED ? seg_table_bytes(a.experts > 256 ? kMaxSlots : 256) : 0));
-  mid_kernel<Y, GROUPED, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), lds, s>>>(a, fewest, most);
-  return hipGetLastError();
-}
-
 template <typename Y>
-hipError_t launch_for(const Int8Args &a, int fewest, int most, hipStream_t s) {
-  if (a.meta.sorted) return launch_as<Y, true, 64, 128, 1, 4>(a, fewest, most, s);
-  return launch_as<Y, false, 64, 128, 1, 4>(a, fewest, most, s);
+hipError_t launch_for(const Int8Args &a, hipStream_t s) {
+  constexpr int BM = 64, BN = 64, WM = 2, WN = 4 / WM;
+  static std::atomic<int> cache[kMaxDevices];
+  const void *f = reinterpret_cast<const void *>(&mid_kernel<Y, BM, BN, WM, WN>);
+  const int64_t tiles = ((a.rows + BM - 1) / BM) * ((a.d_out + BN - 1) / BN);
+  const int grid = xcd_grid(tiles, resident_groups(cache, f, 64 * WM * WN, 0));
+  mid_kernel<Y, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_int8_mid(const Int8Args &a, bool bf16, int fewest, int most, hipStream_t s) {
-  return bf16 ? launch_for<uint16_t>(a, fewest, most, s) : launch_for<float>(a, fewest, most, s);
+hipError_t launch_int8_mid(const Int8Args &a, bool bf16, hipStream_t s) {
+  return bf16 ? launch_for<uint16_t>(a, s) : launch_for<float>(a, s);
 }
 
 }  // namespace lora

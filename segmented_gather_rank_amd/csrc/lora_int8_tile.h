@@ -48,18 +48,22 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // The list of tiles of BM rows and BN columns that a persistent grid walks: all of a dense
-// batch, or of the segments of fewest .. most rows.  Every XCD takes a run of neighbours.
+// batch, or of the segments that are not few_kernel's where the rule says tiles of BM.  Every
+// XCD takes a run of neighbours.
 template <bool GROUPED, int BM, int BN>
 struct TileList {
   SegTable tb;
   int col_tiles, rows, index, last, per;  // this workgroup's tiles: index, index + per, ... below last
-  __device__ __forceinline__ TileList(const Int8Args &a, char *table, int fewest, int most)
+  __device__ __forceinline__ TileList(const Int8Args &a, char *table)
       : tb(seg_table_at(table, a.experts)), col_tiles((a.d_out + BN - 1) / BN), rows((int)a.rows) {
     int tiles;
     if constexpr (GROUPED) {
-      build_items(a.meta, tb, true,
-                  [&](int count, int) { return count >= fewest && count <= most ? (count + BM - 1) / BM * col_tiles : 0; });
-      tiles = uniform_value(tb.scal[2]);
+      const ExpertRule rule(a.meta, a.d_out);
+      tiles = 0;
+      if (rule.large == (BM > 128)) {
+        build_items(a.meta, tb, true, [&](int count, int) { return count > rule.few ? (count + BM - 1) / BM * col_tiles : 0; });
+        tiles = uniform_value(tb.scal[2]);
+      }
     } else {
       tiles = (rows + BM - 1) / BM * col_tiles;
     }

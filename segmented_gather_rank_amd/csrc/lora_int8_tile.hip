@@ -9,7 +9,7 @@ namespace lora {
 namespace {
 
 template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
-__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewest, int most) {
+__global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a) {
   constexpr int kWaves = WM * WN;
   constexpr int TM = BM / WM / 16, TN = BN / WN / 16;          // blocks of 16 of a wave
   constexpr int XQ = BM / 8 / kWaves, WQ = BN / 8 / kWaves;    // transfers of 8 rows of a wave and stage
@@ -19,7 +19,7 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wm = wave / WN, wn = wave % WN;
   const int l16 = lane % 16, quarter = lane / 16;
-  const TileList<GROUPED, BM, BN> list(a, table, fewest, most);
+  const TileList<GROUPED, BM, BN> list(a, table);
   int index = list.index;
   if (index >= list.last) return;
 
@@ -182,28 +182,31 @@ __global__ __launch_bounds__(64 * WM * WN) void tile_kernel(Int8Args a, int fewe
 }
 
 template <typename Y, bool GROUPED, int BM, int BN, int WM, int WN>
-hipError_t launch_as(const Int8Args &a, int fewest, hipStream_t s) {
-  static std::atomic<int> cache[kMaxDevices];
-  // the table's size only matters where it costs a workgroup its place: sized for the most
-  const size_t lds = GROUPED ? seg_table_bytes(a.experts) : 0;
+hipError_t launch_as(const Int8Args &a, hipStream_t s) {
+  static std::atomic<int> cache[2][kMaxDevices];
+  // workgroups that fit a CU go by the length of the table of segments
+  const bool wide = a.experts > 256;
+  const size_t lds = GROUPED ? seg_table_bytes(wide ? kMaxSlots : 256) : 0;
   const void *f = reinterpret_cast<const void *>(&tile_kernel<Y, GROUPED, BM, BN, WM, WN>);
   const int64_t cols = (a.d_out + BN - 1) / BN;
   const int64_t bound = ((a.rows + BM - 1) / BM + (GROUPED ? std::min<int64_t>(a.experts, a.rows) : 0)) * cols;
-  const int grid = xcd_grid(bound, resident_groups(cache, f, 64 * WM * WN, lds));
-  tile_kernel<Y, GROUPED, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), lds, s>>>(a, fewest, INT32_MAX);
+  const int grid = xcd_grid(bound, resident_groups(cache[wide], f, 64 * WM * WN, lds));
+  tile_kernel<Y, GROUPED, BM, BN, WM, WN><<<dim3((unsigned)grid), dim3(64 * WM * WN), lds, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename Y>
-hipError_t launch_for(const Int8Args &a, int fewest, hipStream_t s) {
-  if (a.meta.sorted) return launch_as<Y, true, 256, 256, 2, 4>(a, fewest, s);
-  return launch_as<Y, false, 256, 256, 2, 4>(a, fewest, s);
+hipError_t launch_for(const Int8Args &a, hipStream_t s) {
+  if (!a.meta.sorted) return launch_as<Y, false, 256, 256, 2, 4>(a, s);
+  const hipError_t err = launch_as<Y, true, 128, 128, 2, 2>(a, s);
+  // (no average reaches 160 rows where there are fewer)
+  return err != hipSuccess || a.rows <= 160 ? err : launch_as<Y, true, 256, 256, 2, 4>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_int8_tile(const Int8Args &a, bool bf16, int fewest, hipStream_t s) {
-  return bf16 ? launch_for<uint16_t>(a, fewest, s) : launch_for<float>(a, fewest, s);
+hipError_t launch_int8_tile(const Int8Args &a, bool bf16, hipStream_t s) {
+  return bf16 ? launch_for<uint16_t>(a, s) : launch_for<float>(a, s);
 }
 
 }  // namespace lora
