@@ -51,7 +51,7 @@ hipError_t launch_int8_tile(const Int8Args &a, bool bf16, hipStream_t s);
 // By expert, rows decide who takes a segment, and only the device knows them.  Every kernel
 // that may be the one asks the same rule, whose answers follow from the metadata's counts:
 //   few   most rows of a segment that few_kernel takes: 64 in a decode step (16 rows a
-//         segment or fewer on average), and where tiles would not fill the chip: it splits
+//         segment or fewer on average), 128 where tiles would not fill the chip: it splits
 //         d_in over a workgroup's waves, which answers soonest; else 16
 //   large whether the others take tiles of 256, else of 128: from 160 rows a segment on.
 //         (Long and short segments in tiles of their own, one kernel after the other, are
@@ -64,7 +64,7 @@ struct ExpertRule {
   __device__ __forceinline__ ExpertRule(const MetaView &m, int d_out) {
     const int none = m.info[3];                   // rows without a key come first, as a segment of their own
     const int64_t segments = m.info[0] - (none > 0), rows = m.T - none;
-    few = rows > 16 * segments && segments * ((d_out + 127) / 128) >= 512 ? 16 : kFewRows;
+    few = rows <= 16 * segments ? kFewRows : segments * ((d_out + 127) / 128) >= 512 ? 16 : 2 * kFewRows;
     large = rows > 160 * segments;
   }
 };

@@ -18,7 +18,6 @@ namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kMidRows = 512; // most rows of a dense batch that take tiles of 64
 constexpr int kStep = 128;  // bytes of d_in a step takes: two matrix instructions
 
 // The rows that a workgroup works on: a segment of the metadata, or all.
@@ -234,8 +233,9 @@ hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s) {
     const hipError_t err = bf16 ? launch_few<uint16_t>(a, !tiles, wide, s) : launch_few<float>(a, !tiles, wide, s);
     if (err != hipSuccess || !tiles || a.rows <= 16 || (!a.meta.sorted && a.rows <= kFewRows)) return err;
   }
-  if (!a.meta.sorted && a.rows <= kMidRows) return launch_int8_mid(a, bf16, s);
-  return launch_int8_tile(a, bf16, s);
+  // a dense batch of up to three workgroups a CU takes tiles of 64 x 64
+  const int64_t tiles64 = (a.rows + 63) / 64 * ((a.d_out + 63) / 64);
+  return !a.meta.sorted && tiles64 <= 768 ? launch_int8_mid(a, bf16, s) : launch_int8_tile(a, bf16, s);
 }
 
 }  // namespace lora
