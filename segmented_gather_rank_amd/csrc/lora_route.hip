@@ -4,9 +4,10 @@
 // integers that order like them, PER consecutive experts a lane, so that equal values go
 // to the lowest id by going to the lowest lane.
 //
-// 16 lanes: the topk-th largest of the lanes' maxima bounds the choices from below, and
-// few values reach it (8 choices of 256: 12 or so).  They are laid out one a lane, and
-// each counts how many come before it.  A wave, or a token of whose values more than 16
+// 16 lanes: the topk-th largest of the maxima of the lanes' halves bounds the choices from
+// below, and few values reach it (8 choices of 256: 10 or so; of whole lanes' maxima a
+// grouped choice leaves too few: 17705 tokens took 29 us, now 25).  They are
+// laid out one a lane, and each counts how many come before it.  A wave, or a token of whose values more than 16
 // reach the bound: topk rounds, each of which takes the largest that is left.
 //
 // What decides a choice is compared exactly.  Without bias (and where a group's rank is
@@ -314,6 +315,17 @@ __device__ __forceinline__ int before_me(int32_t v, int lane) {
   }
 }
 
+// How many of 16 lanes' pairs of values are larger than this lane's two.
+template <int N = 1>
+__device__ __forceinline__ void larger_pairs(int32_t high, int32_t low, int &over_high, int &over_low) {
+  if constexpr (N < 16) {
+    const int32_t h = turned<0x120 + N>(high), l = turned<0x120 + N>(low);
+    over_high += (int)(h > high) + (int)(l > high);
+    over_low += (int)(h > low) + (int)(l > low);
+    larger_pairs<N + 1>(high, low, over_high, over_low);
+  }
+}
+
 // A value that reached the bound.
 struct Reached {
   int32_t key, id;
@@ -326,11 +338,17 @@ __device__ __forceinline__ bool by_bound(const RouteArgs &a, const Token<PER> &t
                                          bool &unsure) {
   typedef Ordered<float> O;
   const bool margins = a.bias != nullptr;
-  int32_t m = k[0];
+  // the bound: of the maxima of every lane's two halves (groups may have left few lanes), the topk-th largest
+  int32_t high = k[0], low = PER > 1 ? k[PER / 2] : O::kGone;
 #pragma unroll
-  for (int i = 1; i < PER; ++i) m = larger(m, k[i]);
-  int32_t bound = most<16>(before_me(m, t.lane) == a.topk - 1 ? m : INT32_MIN);
-  // fewer lanes than choices hold any value: all that are left
+  for (int i = 1; i < PER; ++i) {
+    int32_t &m = i < (PER + 1) / 2 ? high : low;
+    m = larger(m, k[i]);
+  }
+  int over_high = low > high, over_low = high > low;
+  larger_pairs(high, low, over_high, over_low);
+  int32_t bound = least<16>(smaller(over_high < a.topk ? high : INT32_MAX, over_low < a.topk ? low : INT32_MAX));
+  // fewer halves than choices hold any value: all that are left
   bound = larger(bound, O::kGone + 1);
   if (margins) {
     // what 64 bits might put before the last choice reaches it too
@@ -408,7 +426,7 @@ __device__ __forceinline__ Token<PER> token_at(const RouteArgs &a, const char *r
 }
 
 template <typename X, int LANES, int PER>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
   constexpr int kTokens = 64 / LANES;             // a wave's
   constexpr int kExactPer = LANES * PER / 64 < 1 ? 1 : LANES * PER / 64;
   __shared__ Reached boxes[LANES == 16 ? 256 : 1];
