@@ -139,9 +139,18 @@ template <typename S> __device__ __forceinline__ void two_largest(S v, S &first,
   first = larger(first, v);
 }
 
+// Whether 64 bits may have a rank of at most `out` in the place of one of at least `in`
+// (each the farthest of the token's lanes).
+template <int LANES, typename S> __device__ __forceinline__ bool may_change(S in, S out) {
+  in = least<LANES>(in);
+  out = most<LANES>(out);
+  return out >= in && fabs(out) < INFINITY;
+}
+
 // The values' own order where nothing is added to them, and c where it is; kGone for
 // experts past the last and in groups that do not stay.  `unsure`: 32 bits could not
-// tell which groups stay.  lds: LANES * PER values and kMaxGroups ranks.
+// tell which groups stay.  lds: LANES * PER values and kMaxGroups ranks, in 32 bits also
+// how far off each may be.
 template <typename S, int LANES, int PER>
 __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t, S *lds, typename Ordered<S>::key k[PER],
                                         bool &unsure) {
@@ -185,10 +194,24 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
   if (a.groups == 1) return;
 
   const int size = a.experts / a.groups;
-  // ranks this near may stand the other way round in 64 bits; only those around the border matter, but such pairs are rare
-  auto too_near = [&](S v, S mine) {
-    if constexpr (kExact) return false;
-    else return (biased || by_rank) && v > -INFINITY && fabsf(v - mine) <= 2.f * near(mine, biased);
+  // The group's rank; in 32 bits the 64-bit one is within `off` of it (c's own rounding
+  // goes by the sizes of the two, which may cancel).
+  S off = 0;
+  auto rank_of = [&](S first, S second) {
+    const S v = a.group_top > 1 ? first + second : first;
+    if constexpr (!kExact) {
+      const S of = fabsf(first) + (a.group_top > 1 ? fabsf(second) : 0.f);
+      off = (biased || by_rank) && of < INFINITY ? near(of, biased) : 0.f;
+    }
+    return v;
+  };
+  // What the lowest rank that stays may be, and the highest that does not.
+  S in = INFINITY, out = -INFINITY;
+  auto border = [&](bool stays, S v) {
+    if constexpr (!kExact) {
+      if (stays) in = smaller(in, v - off);
+      else out = larger(out, v + off);
+    }
   };
   if (LANES == 16 && a.group_lanes) {
     // a group is `group_lanes` neighbouring lanes, a power of two
@@ -202,13 +225,10 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
     if (a.group_lanes > 1) join(turned<0xB1>(first), turned<0xB1>(second));    // lane ^ 1
     if (a.group_lanes > 2) join(turned<0x4E>(first), turned<0x4E>(second));    // lane ^ 2
     if (a.group_lanes > 4) join(turned<0x141>(first), turned<0x141>(second));  // 7 - lane: the other four
-    const S mine = a.group_top > 1 ? first + second : first;
+    const S mine = rank_of(first, second);
     int before = 0;
     // lane l reads lane l - n of its 16: a group before its own where l >= n, n whole groups
-    auto against = [&](S v, int n) {
-      before += v > mine || (v == mine && t.lane >= n);
-      if (too_near(v, mine)) unsure = true;
-    };
+    auto against = [&](S v, int n) { before += v > mine || (v == mine && t.lane >= n); };
     if (a.group_lanes == 1) {
       against(turned<0x121>(mine), 1);
       against(turned<0x123>(mine), 3);
@@ -230,6 +250,8 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
       against(turned<0x12C>(mine), 12);
     }
     against(turned<0x128>(mine), 8);
+    border(before < a.kept, mine);
+    if (!kExact && (biased || by_rank)) unsure = may_change<LANES>(in, out);
     if (before >= a.kept) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) k[i] = O::kGone;
@@ -237,14 +259,15 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
     return;
   }
   // groups of any size: the token's values in LDS, a group a lane
-  S *rank = lds + LANES * PER;
+  S *rank = lds + LANES * PER, *spread = rank + kMaxGroups;
 #pragma unroll
   for (int i = 0; i < PER; ++i) lds[t.base + i] = c[i];
   wave_sync();
   for (int g = t.lane; g < a.groups; g += LANES) {
     S first = -(S)INFINITY, second = -(S)INFINITY;
     for (int i = 0; i < size; ++i) two_largest(lds[g * size + i], first, second);
-    rank[g] = a.group_top > 1 ? first + second : first;
+    rank[g] = rank_of(first, second);
+    if (!kExact) spread[g] = off;
   }
   wave_sync();
   uint64_t stays = 0;
@@ -254,10 +277,12 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
     for (int f = 0; f < a.groups; ++f) {
       const S v = rank[f];
       before += v > mine || (v == mine && f < g);
-      if (f != g && too_near(v, mine)) unsure = true;
     }
+    if (!kExact) off = spread[g];
+    border(before < a.kept, mine);
     if (before < a.kept) stays |= 1ull << g;
   }
+  if (!kExact && (biased || by_rank)) unsure = may_change<LANES>(in, out);
   wave_sync();
   stays = fold<LANES>((int64_t)stays, [](int64_t p, int64_t q) { return p | q; });
   int g = t.base / size, left = (g + 1) * size - t.base;  // experts of group g from this one on
@@ -305,12 +330,12 @@ __device__ __forceinline__ void by_rounds(const RouteArgs &a, const Token<PER> &
 
 // How many of the 16 lanes' values come before this lane's: larger ones, and equal ones
 // of lower lanes.
-template <int N = 1>
-__device__ __forceinline__ int before_me(int32_t v, int lane) {
+template <int N = 1, typename T>
+__device__ __forceinline__ int before_me(T v, int lane) {
   if constexpr (N == 16) {
     return 0;
   } else {
-    const int32_t o = turned<0x120 + N>(v);  // lane - N's
+    const T o = turned<0x120 + N>(v);  // lane - N's
     return (int)(lane >= N ? o >= v : o > v) + before_me<N + 1>(v, lane);
   }
 }
@@ -331,11 +356,33 @@ struct Reached {
   int32_t key, id;
 };
 
+// c of one expert a lane, in 64 bits.
+template <typename X, int PER>
+__device__ __forceinline__ double exact(const RouteArgs &a, const char *row, const Token<PER> &t, int e) {
+  const double top = (double)t.top;
+  auto term = [&](double x) { return x == top ? 1. : exp(x - top); };
+  const double x = (double)logit_at<X>(row, e);
+  double c;
+  if (a.sigmoid) {
+    c = 1. / (1. + exp(-x));
+  } else {
+    double sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < PER && t.base + i < a.experts; ++i) {
+      const double of = (double)logit_at<X>(row, t.base + i);
+      if (of == of) sum += term(of);
+    }
+    c = term(x) / __shfl(total<16>(sum), 0, 16);
+  }
+  c += (double)a.bias[e];
+  return x > -INFINITY && c == c ? c : -(double)INFINITY;
+}
+
 // The topk (at most 16) largest of 16 lanes' values; false where more than 16 reach the
 // bound.  `box`: 16 places of this token's in LDS.
-template <int PER>
-__device__ __forceinline__ bool by_bound(const RouteArgs &a, const Token<PER> &t, const int32_t k[PER], Reached *box, int &id,
-                                         bool &unsure) {
+template <typename X, int PER>
+__device__ __forceinline__ bool by_bound(const RouteArgs &a, const char *row, const Token<PER> &t, const int32_t k[PER], Reached *box,
+                                         int &id) {
   typedef Ordered<float> O;
   const bool margins = a.bias != nullptr;
   // the bound: of the maxima of every lane's two halves (groups may have left few lanes), the topk-th largest
@@ -382,8 +429,15 @@ __device__ __forceinline__ bool by_bound(const RouteArgs &a, const Token<PER> &t
   if (margins) {
     const int32_t prior = __builtin_amdgcn_update_dpp(O::kGone, it.key, 0x111, 0xf, 0xf, false);
     const float v = O::value(it.key), p = O::value(prior);
-    if (t.lane > 0 && t.lane <= a.topk && t.lane < all && v > -INFINITY && p - v <= near(p, true)) unsure = true;
+    const bool near_by = t.lane > 0 && t.lane <= a.topk && t.lane < all && v > -INFINITY && p - v <= near(p, true);
     // 16 choices: the next one has no lane, and did not reach the bound, or there would be more than 16
+    if (__any(near_by)) {
+      const double c = exact<X>(a, row, t, mine.id);
+      const int at64 = before_me(t.lane < all ? Ordered<double>::of(c) : Ordered<double>::kGone, t.lane);
+      if (t.lane < all) box[at64].id = mine.id;
+      wave_sync();
+      if (t.lane < all) id = box[t.lane].id;
+    }
   }
   wave_sync();
   return true;
@@ -426,12 +480,12 @@ __device__ __forceinline__ Token<PER> token_at(const RouteArgs &a, const char *r
 }
 
 template <typename X, int LANES, int PER>
-__global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
+__global__ __launch_bounds__(256, LANES == 64 && PER > 8 ? 2 : 4) void route_kernel(RouteArgs a) {
   constexpr int kTokens = 64 / LANES;             // a wave's
   constexpr int kExactPer = LANES * PER / 64 < 1 ? 1 : LANES * PER / 64;
   __shared__ Reached boxes[LANES == 16 ? 256 : 1];
   // a wave's: values and ranks of its tokens, or of one token in 64 bits
-  constexpr int kShort = kTokens * (LANES * PER + kMaxGroups) * (int)sizeof(float);
+  constexpr int kShort = kTokens * (LANES * PER + 2 * kMaxGroups) * (int)sizeof(float);
   constexpr int kExact = (64 * kExactPer + kMaxGroups) * (int)sizeof(double);
   __shared__ __align__(16) char values[4][kShort > kExact ? kShort : kExact];
   const int wave = threadIdx.x / 64, lane = threadIdx.x % 64;
@@ -450,8 +504,8 @@ __global__ __launch_bounds__(256, 4) void route_kernel(RouteArgs a) {
   int id = 0;
   bool unsure = false, done = false;
   int32_t k[PER];
-  keys_of<float, LANES, PER>(a, t, reinterpret_cast<float *>(values[wave]) + lane / LANES * (LANES * PER + kMaxGroups), k, unsure);
-  if constexpr (LANES == 16) done = by_bound<PER>(a, t, k, boxes + threadIdx.x / 16 * 16, id, unsure);
+  keys_of<float, LANES, PER>(a, t, reinterpret_cast<float *>(values[wave]) + lane / LANES * (LANES * PER + 2 * kMaxGroups), k, unsure);
+  if constexpr (LANES == 16) done = by_bound<X, PER>(a, row, t, k, boxes + threadIdx.x / 16 * 16, id);
   if (!done) by_rounds<float, LANES, PER>(a, t, k, id, unsure);
   // in 64 bits, the whole wave a token
   for (uint64_t left = __ballot(unsure); left;) {
