@@ -12,10 +12,18 @@
 //
 // What decides a choice is compared exactly.  Without bias (and where a group's rank is
 // its largest value) the logits themselves are ordered.  With it c = s + bias is
-// rounded, and two values that differ in 64 bits may agree or change places in 32: a
-// token whose neighbours in the chosen order (or whose groups' ranks) come within the
-// error bound of each other is done again in 64 bits.  That is one token in some
-// hundred; where all biases are equal and logits repeat (bf16), up to all of them.
+// rounded, and two values that differ in 64 bits may agree or change places in 32: what
+// comes within the error bound of its neighbour is compared again in 64 bits.  Choices
+// that reached the bound, one a lane: 1 token in 100, a microsecond of all.  Groups whose
+// ranks leave the border open, the whole wave a token: 1 in 1000.  Rounds, too; where all
+// biases are equal and logits repeat (bf16) that may be all tokens.
+//
+// What bounds it is arithmetic: some 1400 vector operations a wave (of 4 tokens of 256
+// experts: 16 scores a lane, their keys, the groups' two largest, the bound), not the
+// 1 KB a token.  17705 tokens x 256 experts fp32, 8 of 4 of 8 groups, with bias: 19.5 us,
+// of which 3 are the wave's that decides a border again; 4609 x 60 bf16, 4 of them:
+// 4.7; one token of 256: 4.6.  Four waves a SIMD (128 registers): five
+// spill, 29 us.
 #include <algorithm>
 #include <cmath>
 
@@ -148,12 +156,12 @@ template <int LANES, typename S> __device__ __forceinline__ bool may_change(S in
 }
 
 // The values' own order where nothing is added to them, and c where it is; kGone for
-// experts past the last and in groups that do not stay.  `unsure`: 32 bits could not
-// tell which groups stay.  lds: LANES * PER values and kMaxGroups ranks, in 32 bits also
+// experts past the last.  `stays`: a bit a group, of its own group at least in each lane.
+// `unsure`: 32 bits could not tell which.  lds: LANES * PER values and kMaxGroups ranks, in 32 bits also
 // how far off each may be.
 template <typename S, int LANES, int PER>
 __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t, S *lds, typename Ordered<S>::key k[PER],
-                                        bool &unsure) {
+                                        uint64_t &stays, bool &unsure) {
   typedef Ordered<S> O;
   constexpr bool kExact = std::is_same<S, double>::value;
   const bool by_rank = a.groups > 1 && a.group_top > 1, biased = a.bias != nullptr;
@@ -191,6 +199,7 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
 #pragma unroll
   for (int i = 0; i < PER; ++i)
     if (t.base + i >= a.experts) k[i] = O::kGone;
+  stays = ~0ull;
   if (a.groups == 1) return;
 
   const int size = a.experts / a.groups;
@@ -252,10 +261,7 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
     against(turned<0x128>(mine), 8);
     border(before < a.kept, mine);
     if (!kExact && (biased || by_rank)) unsure = may_change<LANES>(in, out);
-    if (before >= a.kept) {
-#pragma unroll
-      for (int i = 0; i < PER; ++i) k[i] = O::kGone;
-    }
+    stays = before < a.kept ? ~0ull : 0;
     return;
   }
   // groups of any size: the token's values in LDS, a group a lane
@@ -265,12 +271,13 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
   wave_sync();
   for (int g = t.lane; g < a.groups; g += LANES) {
     S first = -(S)INFINITY, second = -(S)INFINITY;
+#pragma unroll 4
     for (int i = 0; i < size; ++i) two_largest(lds[g * size + i], first, second);
     rank[g] = rank_of(first, second);
     if (!kExact) spread[g] = off;
   }
   wave_sync();
-  uint64_t stays = 0;
+  stays = 0;
   for (int g = t.lane; g < a.groups; g += LANES) {
     const S mine = rank[g];
     int before = 0;
@@ -284,11 +291,26 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
   }
   if (!kExact && (biased || by_rank)) unsure = may_change<LANES>(in, out);
   wave_sync();
-  stays = fold<LANES>((int64_t)stays, [](int64_t p, int64_t q) { return p | q; });
-  int g = t.base / size, left = (g + 1) * size - t.base;  // experts of group g from this one on
+  stays = (uint64_t)fold<LANES>((int64_t)stays, [](int64_t p, int64_t q) { return p | q; });
+}
+
+// kGone for the experts of groups that do not stay.
+template <int PER, typename K>
+__device__ __forceinline__ void drop(const RouteArgs &a, int base, uint64_t stays, K gone, K k[PER]) {
+  if (a.groups == 1) return;
+  const int size = a.experts / a.groups;
+  int g = base / size;
+  if (a.group_lanes) {           // a lane's are of one group
+    if (!(stays >> g % 64 & 1)) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) k[i] = gone;
+    }
+    return;
+  }
+  int left = (g + 1) * size - base;  // experts of group g from this one on
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    if (g < a.groups && !((uint64_t)stays >> g & 1)) k[i] = O::kGone;
+    if (g < a.groups && !(stays >> g & 1)) k[i] = gone;
     if (--left == 0) {
       ++g;
       left = size;
@@ -504,22 +526,39 @@ __global__ __launch_bounds__(256, LANES == 64 && PER > 8 ? 2 : 4) void route_ker
   int id = 0;
   bool unsure = false, done = false;
   int32_t k[PER];
-  keys_of<float, LANES, PER>(a, t, reinterpret_cast<float *>(values[wave]) + lane / LANES * (LANES * PER + 2 * kMaxGroups), k, unsure);
+  uint64_t stays;
+  keys_of<float, LANES, PER>(a, t, reinterpret_cast<float *>(values[wave]) + lane / LANES * (LANES * PER + 2 * kMaxGroups), k, stays,
+                             unsure);
+  // what 32 bits left open, in 64: the whole wave a token
+  auto again = [&](uint64_t tokens, auto &&f) {
+    while (tokens) {
+      const int q = __builtin_ctzll(tokens) / LANES;
+      tokens &= LANES == 64 ? 0 : ~(((1ull << LANES % 64) - 1) << q * LANES);
+      const Token<kExactPer> u = token_at<X, 64, kExactPer>(a, row_of(first + q));
+      int64_t v[kExactPer];
+      uint64_t in;
+      bool never = false;
+      wave_sync();
+      keys_of<double, 64, kExactPer>(a, u, reinterpret_cast<double *>(values[wave]), v, in, never);
+      f(lane / LANES == q, u, v, in);
+    }
+  };
+  again(__ballot(unsure), [&](bool own, const Token<kExactPer> &, const int64_t *, uint64_t in) {
+    if (own) stays = in;
+  });
+  drop<PER>(a, t.base, stays, Ordered<float>::kGone, k);
+  unsure = false;
   if constexpr (LANES == 16) done = by_bound<X, PER>(a, row, t, k, boxes + threadIdx.x / 16 * 16, id);
-  if (!done) by_rounds<float, LANES, PER>(a, t, k, id, unsure);
-  // in 64 bits, the whole wave a token
-  for (uint64_t left = __ballot(unsure); left;) {
-    const int q = __builtin_ctzll(left) / LANES;
-    left &= LANES == 64 ? 0 : ~(((1ull << LANES % 64) - 1) << q * LANES);
-    const Token<kExactPer> u = token_at<X, 64, kExactPer>(a, row_of(first + q));
-    int64_t v[kExactPer];
-    int e = 0;
-    bool never = false;
-    wave_sync();
-    keys_of<double, 64, kExactPer>(a, u, reinterpret_cast<double *>(values[wave]), v, never);
-    by_rounds<double, 64, kExactPer>(a, u, v, e, never);
-    e = __shfl(e, lane % LANES, 64);
-    if (lane / LANES == q) id = e;
+  if (!done) {
+    by_rounds<float, LANES, PER>(a, t, k, id, unsure);
+    again(__ballot(unsure), [&](bool own, const Token<kExactPer> &u, int64_t *v, uint64_t in) {
+      int e = 0;
+      bool never = false;
+      drop<kExactPer>(a, u.base, in, Ordered<double>::kGone, v);
+      by_rounds<double, 64, kExactPer>(a, u, v, e, never);
+      e = __shfl(e, lane % LANES, 64);
+      if (own) id = e;
+    });
   }
 
   // the chosen one's score, in 64 bits
