@@ -646,7 +646,8 @@ lora_status lora_int8_matmul_workspace_bytes(int64_t num_rows, const lora_int8_w
                                              size_t *bytes);
 
 /* y[i][n] = x_scale[r] * scale[e][n] * sum_k x[r][k] * w[e][n][k] (+ bias[e][n]): the sum
- * exact, its scaling in fp32, y rounded once.
+ * exact, rounded to fp32 and multiplied by the fp32 product of the two scales, y rounded
+ * once.
  *   meta          NULL: a dense layer (num_experts = 1): r = i, e = 0.  Else metadata of
  *                 num_rows rows and num_experts keys: e is row i's key, r = i /
  *                 x_row_div, and rows without a key are not read or written.

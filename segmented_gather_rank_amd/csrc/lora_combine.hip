@@ -26,8 +26,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     }
   }
   const uint64_t all = __ballot(here);
-  const int c = 8 * (blockIdx.y * 256 + threadIdx.x);
-  if (c >= a.width) return;
+  // past the last column the last ones again, not stored: lanes hold weights that others read
+  const int at = 8 * (blockIdx.y * 256 + threadIdx.x), c = min(at, a.width - 8);
   const X *y = reinterpret_cast<const X *>(a.y) + t * a.topk * a.ldy + c;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
   if (a.add) load8(reinterpret_cast<const X *>(a.add) + t * a.ldadd + c, sum);
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += by[q] * v[q][e];
   }
-  store8(reinterpret_cast<X *>(a.out) + t * a.ldout + c, sum);
+  if (at < a.width) store8(reinterpret_cast<X *>(a.out) + t * a.ldout + c, sum);
 }
 
 }  // namespace

@@ -33,8 +33,6 @@ namespace lora {
 
 namespace {
 
-typedef unsigned int u32x2r __attribute__((ext_vector_type(2)));
-
 // ---------------------------------------------------------------- values as ordered integers
 
 template <typename S> struct Ordered;

@@ -155,3 +155,31 @@ def test_outputs_end_where_they_should(L):
     L.lora_moe_route(logits, L.Routing(60, 4), topk_ids=ids[5:42], weights=w[5:42])
     assert (ids[:5] == -7).all() and (ids[42:] == -7).all() and (w[:5] == -7).all() and (w[42:] == -7).all()
     assert (ids[5:42] >= 0).all()
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(16, 8, 3), (64, 8, 3), (66, 11, 4), (512, 16, 5)])
+def test_group_ranks_that_cancel(L, score, E, groups, kept):
+    """The two largest of a group are far larger than their sum: c's rounding goes by their sizes, the rank does not."""
+    g = torch.Generator("cuda").manual_seed(E)
+    size = E // groups
+    bias = torch.full((groups, size), -3000.0, device="cuda")
+    bias[:, 0], bias[:, 1] = 1000.0, -1000.0
+    bias = bias.reshape(-1).contiguous()
+    logits = 0.02 * torch.randn((3000, E), generator=g, device="cuda")
+    ids, _ = check(L, logits, bias, topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=2)
+    assert len(torch.unique(ids[:, 0] // size)) == groups
+
+
+def test_many_launches(L):
+    """More tokens than one launch takes: as the same tokens in two calls."""
+    T, cut = (1 << 26) + 37, (1 << 26) - 5
+    g = torch.Generator("cuda").manual_seed(1)
+    logits = torch.randn((T, 3), generator=g, device="cuda").bfloat16()
+    r = L.Routing(3, 1)
+    ids, w = L.lora_moe_route(logits, r)
+    for part in (slice(0, cut), slice(cut, T)):
+        i, v = L.lora_moe_route(logits[part], r)
+        assert torch.equal(i, ids[part]) and torch.equal(v, w[part])
+    best = logits.float().argmax(1).int()  # (equal logits: any of them)
+    assert bool((logits.gather(1, best.long()[:, None]) == logits.gather(1, ids.long())).all())

@@ -142,3 +142,21 @@ def test_metadata(L, T, topk, local, dtype):
     assert (q[away] == 99).all() and (s[away] == 7).all() and (act[away] == 7).all()
     if here.any():
         check_act(q, s, act, x, np.nonzero(here)[0])
+
+
+def test_many_launches(L):
+    """More rows than one launch takes: as the same rows in two calls; with metadata, only its rows."""
+    rows, cut = (1 << 23) + 37, (1 << 23) - 5
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn((rows, 16), generator=g, device="cuda").bfloat16()
+    q, s = L.lora_quantize(x)
+    for part in (slice(0, cut), slice(cut, rows)):
+        a, b = L.lora_quantize(x[part])
+        assert torch.equal(a, q[part]) and torch.equal(b, s[part])
+    check_plain(L, x[-50:])
+    slots = torch.randint(-1, 2, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    some, scale = torch.full_like(q, 5), torch.full_like(s, 5.0)
+    L.lora_quantize(x, q=some, scale=scale, meta=L.lora_prepare_meta(slots, 2))
+    here = slots >= 0
+    assert torch.equal(some[here], q[here]) and torch.equal(scale[here], s[here])
+    assert bool((some[~here] == 5).all()) and bool((scale[~here] == 5).all())

@@ -219,3 +219,38 @@ def test_two_graphs_and_a_stream(L, T):
         call(sets[0], stream=stream)
         side.synchronize()
         assert torch.equal(sets[0][3], want[0])
+
+
+@pytest.mark.parametrize("T,used", [(1500, 3), (2000, 300), (4000, 9)])
+def test_keys_beyond_256(L, T, used):
+    """Several hundred keys, of which few hold many rows or many hold few."""
+    g = torch.Generator("cuda").manual_seed(T)
+    keys = 300 if used != 9 else 1023
+    x, xs, w, ws, b = made(g, T, 272, 264, keys, True)
+    of = torch.randperm(keys, generator=g, device="cuda")[:used].int()
+    slots = of[torch.randint(0, used, (T,), generator=g, device="cuda")]
+    slots[::7] = -1
+    expert = slots.cpu().numpy()
+    here = expert >= 0
+    for dtype in DTYPES:
+        y = torch.full((T, 264), 7.0, dtype=dtype, device="cuda")
+        L.lora_int8_matmul(x, xs, L.Int8Weight(w, ws, bias=b), out=y, meta=L.lora_prepare_meta(slots, keys))
+        want, bound = R.int8_matmul(x, xs, w, ws, b, expert, np.arange(T), dtype)
+        R.near(y[slots >= 0], want[here], bound[here])
+        assert (y[slots < 0] == 7).all()
+
+
+def test_many_launches(L):
+    """So many columns that a launch takes some experts only: each expert as a dense call of its own."""
+    g = torch.Generator("cuda").manual_seed(3)
+    experts, d_out = 11, 1 << 24
+    x, xs, w, ws, _ = made(g, experts, 16, d_out, experts)
+    slots = torch.arange(experts, device="cuda", dtype=torch.int32).flip(0).contiguous()
+    y = L.lora_int8_matmul(x, xs, L.Int8Weight(w, ws), meta=L.lora_prepare_meta(slots, experts))
+    for i in range(experts):
+        e = experts - 1 - i
+        assert torch.equal(y[i:i + 1], L.lora_int8_matmul(x[i:i + 1], xs[i:i + 1], L.Int8Weight(w[e], ws[e])))
+    part = slice(d_out - 64, d_out)
+    want, bound = R.int8_matmul(x, xs, w[:, part].contiguous(), ws[:, part].contiguous(), None, slots.cpu().numpy(), np.arange(experts),
+                                torch.bfloat16)
+    R.near(y[:, part], want, bound)

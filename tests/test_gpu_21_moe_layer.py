@@ -199,3 +199,17 @@ def test_layer_captured(L):
         torch.cuda.synchronize()
         layer.check(x, logits, slot, b)
         other.check(x, logits, slot, mine)
+
+
+def test_combine_many_launches(L):
+    """More tokens than one launch takes: as the same tokens in two calls."""
+    T, cut = (1 << 23) + 37, (1 << 23) - 5
+    g = torch.Generator("cuda").manual_seed(2)
+    y = torch.randn((2 * T, 8), generator=g, device="cuda").bfloat16()
+    w = torch.rand((T, 2), generator=g, device="cuda")
+    ids = torch.randint(0, 6, (T, 2), generator=g, device="cuda", dtype=torch.int32)
+    out = L.lora_moe_combine(y, w, ids, num_experts=6, num_local_experts=4)
+    for part, pairs in ((slice(0, cut), slice(0, 2 * cut)), (slice(cut, T), slice(2 * cut, 2 * T))):
+        assert torch.equal(out[part], L.lora_moe_combine(y[pairs], w[part], ids[part], num_experts=6, num_local_experts=4))
+    want, bound = R.combine(y[-100:], w[-50:], ids[-50:], (ids[-50:] < 4).cpu().numpy().reshape(-1, 2), None, torch.bfloat16)
+    R.near(out[-50:], want, bound)
