@@ -1,11 +1,14 @@
-// lora_int8_mid.hip -- 8-bit products of some rows: tiles of 64 rows, whose operands wait
-// in registers for their place in LDS.
+// lora_int8_mid.hip -- 8-bit products of dense batches that large tiles would not spread
+// over the chip: tiles of 64 x 64, whose operands wait in registers for their place in LDS.
 //
-// With tens to hundreds of rows the weights' bytes and the time that memory takes to
-// answer bound the product, not the matrix cores.  Tiles are small, so that every CU has
-// some, two workgroups share a CU, and a workgroup keeps two stages of its operands on
-// their way at all times, across the ends of its tiles.  (They go through registers: the
-// compiler waits for those one by one, while it cannot tell transfers to a ring in LDS apart.)
+// Neither bytes nor the matrix cores (busy a sixth of the time) bound such a product, but
+// the way of a stage: from memory, to LDS, past a barrier, to the products.  Tiles are
+// small, so that every CU has some, two workgroups share a CU, and a workgroup keeps two
+// stages of its operands on their way at all times, across the ends of its tiles.  (They
+// go through registers: the compiler waits for those one by one, while it cannot tell
+// transfers to a ring in LDS apart.)  256 rows x 4096 x 6144: 16.4 us, 790 TOP/s; in
+// tiles of 64 x 128 17.7, of 128 x 128 25, with four stages on their way 17, six 19, with
+// stages of 256 bytes 18.
 #include <algorithm>
 
 #include "lora_int8_tile.h"

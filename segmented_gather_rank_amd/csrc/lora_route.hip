@@ -5,25 +5,25 @@
 // to the lowest id by going to the lowest lane.
 //
 // 16 lanes: the topk-th largest of the maxima of the lanes' halves bounds the choices from
-// below, and few values reach it (8 choices of 256: 10 or so; of whole lanes' maxima a
-// grouped choice leaves too few: 17705 tokens took 29 us, now 25).  They are
-// laid out one a lane, and each counts how many come before it.  A wave, or a token of whose values more than 16
-// reach the bound: topk rounds, each of which takes the largest that is left.
+// below, and few values reach it (8 choices of 256: 10 or so).  They are laid out one a
+// lane, and each counts how many come before it.  (Of whole lanes' maxima a grouped choice
+// leaves too few: 17705 tokens 29 us for 25 then.)  A wave, or a token of whose values
+// more than 16 reach the bound: topk rounds, each of which takes the largest that is left.
 //
 // What decides a choice is compared exactly.  Without bias (and where a group's rank is
 // its largest value) the logits themselves are ordered.  With it c = s + bias is
 // rounded, and two values that differ in 64 bits may agree or change places in 32: what
 // comes within the error bound of its neighbour is compared again in 64 bits.  Choices
-// that reached the bound, one a lane: 1 token in 100, a microsecond of all.  Groups whose
-// ranks leave the border open, the whole wave a token: 1 in 1000.  Rounds, too; where all
+// that reached the bound are, one a lane; groups whose ranks leave the border open, the
+// whole wave a token (all of it that way: 26.5 us for 20.8), and so are rounds.  Where all
 // biases are equal and logits repeat (bf16) that may be all tokens.
 //
-// What bounds it is arithmetic: some 1400 vector operations a wave (of 4 tokens of 256
-// experts: 16 scores a lane, their keys, the groups' two largest, the bound), not the
-// 1 KB a token.  17705 tokens x 256 experts fp32, 8 of 4 of 8 groups, with bias: 19.5 us,
-// of which 3 are the wave's that decides a border again; 4609 x 60 bf16, 4 of them:
-// 4.7; one token of 256: 4.6.  Four waves a SIMD (128 registers): five
-// spill, 29 us.
+// Bound: vector instructions, some 350 a token of 256 experts (scores and keys of 16 a
+// lane, the groups' two largest, the bound), not its 1 KB.  17705 tokens x 256 experts
+// fp32, 8 choices in 4 of 8 groups, with bias: 20.8 us a call, of which the tokens that are
+// done again take 4; 4609 x 60 bf16, 4 choices: 4.7; one token of 256: 6.5, four dependent
+// loads and the way through.  Four waves a SIMD (128 registers) measure as three do
+// (24.1 and 24.0 us then; 60 experts 6.1 and 6.4); five spill, 29 us.
 #include <algorithm>
 #include <cmath>
 
