@@ -13,10 +13,11 @@
 //
 // By expert, tiles are 128 x 128 unless segments are long (lora_base_host.h): 4609 tokens
 // x 8 choices, an eighth of the experts here, x 2048 x 7168: 137 us of the call's 156, 3.9
-// TB/s.  Neither bytes nor products bound it (and a third of the tiles' rows are past
-// their segments), but the 1.8 us in which a stage arrives from HBM, one at a time in each
-// of a CU's two workgroups.  Tiles of 128 x 256: 159 us, 128 x 192: 173, 64 x 256: 194,
-// 64 x 128: 211.
+// TB/s, with the matrix cores busy 28 %.  Neither bytes nor products bound it alone (a third
+// of the tiles' rows are past their segments; with nothing to load it still takes 100),
+// but a tile's 16 stages with a barrier each, its start and its results' way out, beside
+// the weights' stream.  Tiles of 128 x 256: 159 us, 128 x 192: 173, 64 x 256: 194,
+// 64 x 128: 211; two stages on their way, through registers: 154.
 #include <algorithm>
 
 #include "lora_int8_tile.h"
