@@ -21,9 +21,9 @@
 // Bound: vector instructions, some 350 a token of 256 experts (scores and keys of 16 a
 // lane, the groups' two largest, the bound), not its 1 KB.  17705 tokens x 256 experts
 // fp32, 8 choices in 4 of 8 groups, with bias: 20.8 us a call, of which the tokens that are
-// done again take 4; 4609 x 60 bf16, 4 choices: 4.7; one token of 256: 6.5, four dependent
+// done again take 2; 4609 x 60 bf16, 4 choices: 4.7; one token of 256: 6.5, four dependent
 // loads and the way through.  Four waves a SIMD (128 registers) measure as three do
-// (24.1 and 24.0 us then; 60 experts 6.1 and 6.4); five spill, 29 us.
+// (21.1 us both; 60 experts 6.1 and 6.4 then); five spill, 29 us.
 #include <algorithm>
 #include <cmath>
 

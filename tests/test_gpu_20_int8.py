@@ -254,3 +254,33 @@ def test_many_launches(L):
     want, bound = R.int8_matmul(x, xs, w[:, part].contiguous(), ws[:, part].contiguous(), None, slots.cpu().numpy(), np.arange(experts),
                                 torch.bfloat16)
     R.near(y[:, part], want, bound)
+
+
+def test_two_threads(L):
+    """Calls of every kernel at once from two threads, each on a stream of its own."""
+    import threading
+    g = torch.Generator("cuda").manual_seed(12)
+    cases = []
+    for rows, d_in, d_out in ((3, 256, 64), (200, 256, 640), (900, 256, 2048), (5000, 256, 4096)):
+        x, xs, w, ws, b = made(g, rows, d_in, d_out, bias=True)
+        weight = L.Int8Weight(w, ws, bias=b)
+        cases.append((x, xs, weight, L.lora_int8_matmul(x, xs, weight)))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(10):
+                for x, xs, weight, want in cases:
+                    y = L.lora_int8_matmul(x, xs, weight)
+                    stream.synchronize()
+                    if not torch.equal(y, want):
+                        wrong.append(tuple(y.shape))
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
