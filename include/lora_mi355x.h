@@ -614,8 +614,8 @@ typedef enum lora_activation {
  *                 expert is local)
  *   d_q           device int8 [num_rows][ldq]
  *   d_scale       device fp32 [num_rows]
- *   d_act         device [num_rows][ldact] of dtype, or NULL: v itself, rounded once
- *                 (the x of the down projection's lora_apply)
+ *   d_act         device [num_rows][ldact] of dtype, or NULL: the activation itself, rounded
+ *                 once (the x of the down projection's lora_apply); NULL without one
  * width is a multiple of 16, at most 2^24; ldx and ldact are multiples of 8, ldq of 16;
  * the matrices are 16-byte aligned and do not overlap. */
 lora_status lora_quantize(const void *d_x, int64_t ldx, int64_t num_rows, int64_t width,

@@ -87,7 +87,7 @@ lora_status lora_quantize(const void *d_x, int64_t ldx, int64_t num_rows, int64_
                           lora_activation activation, const lora_meta *meta, int8_t *d_q, int64_t ldq, float *d_scale,
                           void *d_act, int64_t ldact, void *stream) {
   if (!dtype_ok(dtype) || (activation != LORA_ACT_NONE && activation != LORA_ACT_SILU_MUL)) return LORA_ERR_UNSUPPORTED;
-  if (num_rows < 0 || width < 16 || width % 16) return LORA_ERR_INVALID_ARG;
+  if (num_rows < 0 || width < 16 || width % 16 || (d_act && activation == LORA_ACT_NONE)) return LORA_ERR_INVALID_ARG;
   if (num_rows > kMaxRows * 64 || width > kMaxWidth) return LORA_ERR_UNSUPPORTED;
   const int64_t in = activation == LORA_ACT_SILU_MUL ? 2 * width : width;
   if (ldx < in || ldx % 8 || ldq < width || ldq % 16 || (d_act && (ldact < width || ldact % 8))) return LORA_ERR_INVALID_ARG;

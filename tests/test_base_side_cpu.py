@@ -165,3 +165,10 @@ def test_reference_forms():
     assert ids.tolist() == [[2, 3]]
     q, s = R.quantize(np.array([[127.0, 0.5, 1.5, -2.5, -127.0], [0, 0, 0, 0, 0]]))
     assert q.tolist() == [[127, 0, 2, -2, -127], [0] * 5] and s.tolist() == [1.0, 0.0]
+
+
+def test_an_activation_that_is_none_is_not_written():
+    """Without an activation there is nothing that d_act could take: refused, whatever its stride."""
+    for kw in (dict(a=P, lda=64), dict(a=P, lda=64, rows=1), dict(a=P, lda=128, m=meta(0))):
+        assert quantize(**kw) == INVALID, kw
+    assert quantize(act=1, ldx=128, a=P, lda=64) == OK
