@@ -575,7 +575,8 @@ typedef enum lora_score {
  * after every other expert of the kept groups, whatever its bias (it is still chosen
  * where fewer than topk others are left).  +inf logits share the softmax's mass.  NaN
  * logits are ordered like -inf, and every weight of their token is NaN; a NaN bias masks
- * like -inf.  Ids are distinct and valid whatever the logits hold.
+ * like -inf.  A group whose two largest c are +inf (a bias) and -inf ranks as -inf.  Ids are
+ * distinct and valid whatever the logits hold.
  * Supported: num_experts in [1, 1024], num_groups in [1, 64] dividing it, group_top 1 or
  * 2 (at most a group's experts), topk in [1, 32], at most the kept groups' experts. */
 typedef struct lora_routing {

@@ -205,7 +205,8 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
   // goes by the sizes of the two, which may cancel).
   S off = 0;
   auto rank_of = [&](S first, S second) {
-    const S v = a.group_top > 1 ? first + second : first;
+    S v = a.group_top > 1 ? first + second : first;
+    if (v != v) v = -(S)INFINITY;  // a bias of +inf beside masked experts alone
     if constexpr (!kExact) {
       const S of = fabsf(first) + (a.group_top > 1 ? fabsf(second) : 0.f);
       off = (biased || by_rank) && of < INFINITY ? near(of, biased) : 0.f;

@@ -183,3 +183,22 @@ def test_many_launches(L):
         assert torch.equal(i, ids[part]) and torch.equal(v, w[part])
     best = logits.float().argmax(1).int()  # (equal logits: any of them)
     assert bool((logits.gather(1, best.long()[:, None]) == logits.gather(1, ids.long())).all())
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,kept", [(16, 8, 3), (64, 8, 3), (66, 11, 4), (256, 8, 1), (512, 16, 5)])
+def test_infinite_bias_beside_masked_experts(L, score, E, groups, kept):
+    """A group of one +inf and masked experts has no rank (inf - inf is no number): it counts as -inf, like a masked group."""
+    g = torch.Generator("cuda").manual_seed(E + 1)
+    size = E // groups
+    logits = torch.randn((60, E), generator=g, device="cuda")
+    bias = 0.1 * torch.randn(E, generator=g, device="cuda")
+    bias[size], bias[3 * size + 1] = torch.inf, torch.inf          # groups 1 and 3
+    logits[:20, size + 1:2 * size] = -torch.inf
+    logits[10:40, 3 * size] = -torch.inf
+    logits[10:40, 3 * size + 2:4 * size] = -torch.inf
+    logits[30:40, 4 * size:] = -torch.inf                          # what is left may be masked groups alone
+    logits[50:60, :] = -torch.inf
+    logits[50:60, size] = 0
+    with np.errstate(invalid="ignore"):
+        check(L, logits, bias, topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=2)
