@@ -135,9 +135,9 @@ struct Token {
 // the quotient) and, by the exponent's argument z and the logarithm's own step, 1.5 |z| *
 // 2^-24, up to |z| = 104 where the exponential ends (below 1e-38 it is 0).  With a bias,
 // whose sum adds half a step, the argument's part is at most |z| e^-|z| < 0.4 steps of 1,
-// and s at most 1.
-__device__ __forceinline__ float near(float v, bool biased) {
-  return biased ? 64.f * 0x1p-24f * (1.f + fabsf(v)) : 400.f * 0x1p-24f * fabsf(v) + 1e-36f;
+// and s at most 1.  `unit`: what v counts 1 as.
+__device__ __forceinline__ float near(float v, bool biased, float unit = 1.f) {
+  return biased ? 64.f * 0x1p-24f * (unit + fabsf(v)) : 400.f * 0x1p-24f * fabsf(v) + 1e-36f * unit;
 }
 
 template <typename S> __device__ __forceinline__ void two_largest(S v, S &first, S &second) {
@@ -202,14 +202,18 @@ __device__ __forceinline__ void keys_of(const RouteArgs &a, const Token<PER> &t,
 
   const int size = a.experts / a.groups;
   // The group's rank; in 32 bits the 64-bit one is within `off` of it (c's own rounding
-  // goes by the sizes of the two, which may cancel).
+  // goes by the sizes of the two, which may cancel), and of scores a quarter is taken, so
+  // that neither the sum nor the bounds leave float32 where c does not.
   S off = 0;
+  const S unit = !kExact && (biased || by_rank) ? (S)0.25 : (S)1;
   auto rank_of = [&](S first, S second) {
+    first *= unit;
+    second *= unit;
     S v = a.group_top > 1 ? first + second : first;
     if (v != v) v = -(S)INFINITY;  // a bias of +inf beside masked experts alone
     if constexpr (!kExact) {
       const S of = fabsf(first) + (a.group_top > 1 ? fabsf(second) : 0.f);
-      off = (biased || by_rank) && of < INFINITY ? near(of, biased) : 0.f;
+      off = (biased || by_rank) && of < INFINITY ? near(of, biased, 0.25f) : 0.f;
     }
     return v;
   };

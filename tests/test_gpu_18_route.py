@@ -202,3 +202,21 @@ def test_infinite_bias_beside_masked_experts(L, score, E, groups, kept):
     logits[50:60, size] = 0
     with np.errstate(invalid="ignore"):
         check(L, logits, bias, topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("top", [1, 2])
+@pytest.mark.parametrize("E,groups,kept", [(16, 8, 3), (64, 8, 3), (66, 11, 4), (512, 16, 5)])
+def test_group_ranks_beyond_32_bits(L, score, top, E, groups, kept):
+    """Biases whose sum of two is past the largest float32: the ranks are those of 64 bits."""
+    g = torch.Generator("cuda").manual_seed(E + 2)
+    size = E // groups
+    logits = torch.randn((40, E), generator=g, device="cuda")
+    largest = torch.finfo(torch.float32).max
+    for sign in (1, -1):
+        bias = sign * largest * (0.6 + 0.4 * torch.rand((groups, size), generator=g, device="cuda"))
+        some = logits.clone().view(40, groups, size)
+        some[20:, ::2, 1:] = -torch.inf                            # -inf is below every sum
+        check(L, some.view(40, E), bias.view(-1), topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=top)
+        bias[...] = sign * largest                                 # equal in 64 bits too
+        check(L, logits, bias.view(-1), topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=top)
