@@ -109,7 +109,7 @@ __device__ __forceinline__ void wave_sync() {
 }
 
 // In 32 bits the exponential and the quotient are the hardware's, a step off each: the
-// choice allows for it, and the weights are taken in 64.
+// choice allows for it, and the weights' quotients are taken in 64.
 __device__ __forceinline__ float exp_of(float v) { return __builtin_amdgcn_exp2f(v * 1.44269504f); }
 __device__ __forceinline__ double exp_of(double v) { return exp(v); }
 __device__ __forceinline__ float inverse(float v) { return __builtin_amdgcn_rcpf(v); }
@@ -573,12 +573,12 @@ __global__ __launch_bounds__(256, LANES == 64 && PER > 8 ? 2 : 4) void route_ker
   if (a.renorm) {
     sum = total<LANES>(s);
   } else if (!a.sigmoid) {
-    // the sum of all: 32 bits a lane (at most 16 of them), 64 across
-    float part = 0;
+    // the sum of all: its terms in 32 bits (a step, and |z| 2^-24 of an argument z that e^z makes small), added in 64
+    double part = 0;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
-      if (t.x[i] > -INFINITY) part += t.x[i] == t.top ? 1.f : expf(t.x[i] - t.top);
-    sum = total<LANES>((double)part);
+      if (t.x[i] > -INFINITY) part += (double)(t.x[i] == t.top ? 1.f : expf(t.x[i] - t.top));
+    sum = total<LANES>(part);
   }
   if (real && t.lane < a.topk) {
     float w = sum > 0 ? (float)(s / sum * (double)a.scale) : 0.f;

@@ -220,3 +220,18 @@ def test_group_ranks_beyond_32_bits(L, score, top, E, groups, kept):
         check(L, some.view(40, E), bias.view(-1), topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=top)
         bias[...] = sign * largest                                 # equal in 64 bits too
         check(L, logits, bias.view(-1), topk=min(4, kept * size), score=score, groups=groups, kept=kept, group_top=top)
+
+
+@pytest.mark.parametrize("E,gap", [(256, 16), (64, 4), (1024, 16)])
+def test_softmax_sum_of_many_small_terms(L, E, gap):
+    """Without renormalising: terms of just under half a float32 step of 1 beside the 1 of the largest logit, every one of
+    which a sum in float32 drops."""
+    logits = torch.full((5, E), -16.64, device="cuda")             # exp(-16.64) = 0.9956 * 2^-24
+    logits[:, ::gap] = 0
+    topk = 4
+    ids, w = L.lora_moe_route(logits, L.Routing(E, topk, renormalize=False))
+    want, weights = R.route(logits, topk, "softmax", renorm=False)
+    assert (ids.cpu().numpy() == want).all()
+    # a small term is off by the exponential's step and the rounding of its argument, (2 + 17) * 2^-24 of itself, and they
+    # are less than 2^-19 of the sum together; the sum and the quotient are taken in 64 bits, the weight is rounded once
+    R.near(w, weights, weights * R.F32 * (1 + 19 * 2.0 ** -19) + 1e-45, "weights")
