@@ -665,7 +665,8 @@ lora_status lora_int8_matmul(const lora_meta *meta, const int8_t *d_x, int64_t l
                              void *d_ws, size_t ws_bytes, void *stream);
 
 /* out[t] = add[t] + sum_j weights[t][j] * y[t * topk + j] over the choices j whose expert is
- * local (in ascending j, in fp32, rounded once).  The others' rows are not read.
+ * local (the sum in ascending j, then add, in fp32; rounded once).  The rows of the others are
+ * not read.
  *   d_y           device [T * topk][ldy] of dtype (fp32 or bf16), width columns
  *   d_topk_ids, d_expert_map, num_experts, num_local_experts: as in lora_prepare_moe_meta;
  *                 ids that count as bad there are not local here

@@ -2,9 +2,10 @@
 //
 // Bound: HBM; the rows of a token's local choices are read once, its output written once.
 // A thread takes 8 columns of a token; its choices are read eight at a time, so that a
-// token's rows are all on their way at once.  The sum is in fp32, in ascending choice.
-// 4608 tokens x 8 choices x 4096 columns bf16 and a row to add: 69 us, 5.4 TB/s; 256
-// tokens x 7168, an eighth of the choices local: 4.2 us, a launch and three dependent loads.
+// token's rows are all on their way at once.  The sum is in fp32, in ascending choice, then
+// the row to add.  4608 tokens x 8 choices x 4096 columns bf16 and a row to add: 70 us, 5.4
+// TB/s (71 with the eight waves a SIMD that its registers would allow); 256 tokens x 7168,
+// an eighth of the choices local: 4.2 us, a launch and three dependent loads.
 #include <algorithm>
 
 #include "lora_base_host.h"
@@ -14,7 +15,7 @@ namespace lora {
 namespace {
 
 template <typename X>
-__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(1, 6))) void combine_kernel(CombineArgs a) {
   const int64_t t = blockIdx.x;
   const int lane = threadIdx.x % 64;
   // lane j of every wave looks choice j up
@@ -33,7 +34,10 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int at = 8 * (blockIdx.y * 256 + threadIdx.x), c = min(at, a.width - 8);
   const X *y = reinterpret_cast<const X *>(a.y) + t * a.topk * a.ldy + c;
   float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (a.add) load8(reinterpret_cast<const X *>(a.add) + t * a.ldadd + c, sum);
+  // read along with the choices' rows, added last: the sum is rounded at its own size, not at this row's
+  Raw8<X> base;
+  base.zero();
+  if (a.add) base.load(reinterpret_cast<const X *>(a.add) + t * a.ldadd + c);
   for (uint64_t left = all; left;) {
     Raw8<X> v[8];
     float by[8];
@@ -54,6 +58,8 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum[e] += by[q] * v[q][e];
   }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum[e] += base[e];
   if (at < a.width) store8(reinterpret_cast<X *>(a.out) + t * a.ldout + c, sum);
 }
 

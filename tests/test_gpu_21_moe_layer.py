@@ -201,6 +201,29 @@ def test_layer_captured(L):
         other.check(x, logits, slot, mine)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("K", [1, 8, 20])
+def test_combine_adds_last(L, K, in_place):
+    """A row to add that is far larger than the sum: the sum is rounded at its own size, not at that of the row."""
+    T, width = 5, 2056
+    ids = torch.arange(K, device="cuda", dtype=torch.int32).expand(T, K).contiguous()
+    w = torch.ones((T, K), device="cuda")
+    add = torch.full((T, width), 2.0 ** 24, device="cuda")           # 1 is half a step there
+    out = add.clone() if in_place else None
+    got = L.lora_moe_combine(torch.ones((T * K, width), device="cuda"), w, ids, out=out, add=out if in_place else add)
+    assert bool((got == 2.0 ** 24 + K // 2 * 2).all())               # halves go to the even neighbour
+    g = torch.Generator("cuda").manual_seed(K)
+    y, w = torch.randn((T * K, width), generator=g, device="cuda"), torch.rand((T, K), generator=g, device="cuda") - 0.3
+    add = 1000 * torch.randn((T, width), generator=g, device="cuda")
+    out = add.clone() if in_place else None
+    local = np.ones((T, K), bool)
+    want, _ = R.combine(y, w, ids, local, add, torch.float32)
+    size, _ = R.combine(y.abs(), w.abs(), ids, local, None, torch.float32)
+    got = L.lora_moe_combine(y, w, ids, out=out, add=out if in_place else add)
+    # a product and a sum for each choice, off by a rounding of at most the terms' whole size; then one of the output's
+    R.near(got, want, 2 * K * R.F32 * size * (1 + 1e-5) + R.F32 * np.abs(want) * (1 + 1e-5) + 1e-37)
+
+
 def test_combine_many_launches(L):
     """More tokens than one launch takes: as the same tokens in two calls."""
     T, cut = (1 << 23) + 37, (1 << 23) - 5
