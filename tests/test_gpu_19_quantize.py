@@ -160,3 +160,36 @@ def test_many_launches(L):
     here = slots >= 0
     assert torch.equal(some[here], q[here]) and torch.equal(scale[here], s[here])
     assert bool((some[~here] == 5).all()) and bool((scale[~here] == 5).all())
+
+
+@pytest.mark.parametrize("gate", [(-87.0, 0.0), (0.0, 87.0), (-1.0, 1.0)])
+def test_gate_in_32_bits(L, gate):
+    """The gated activation in float32, where no part of it leaves the normal numbers."""
+    g = torch.Generator("cuda").manual_seed(4)
+    width = 4096
+    both = torch.empty((32, 2 * width), device="cuda")
+    both[:, :width] = gate[0] + (gate[1] - gate[0]) * torch.rand((32, width), generator=g, device="cuda")
+    both[:, width:] = 0.5 + torch.rand((32, width), generator=g, device="cuda")
+    act = torch.empty((32, width), device="cuda")
+    q, s = L.lora_quantize(both, activation="silu_mul", act=act)
+    v = R.silu_mul(both)
+    # e = exp(-|x|) is a square of the hardware's exponential (a step, 2 * 2^-24, twice; the square's rounding), corrected
+    # by what its argument's rounding left out (another rounding): 6 * 2^-24.  1 + e is rounded, its inverse is the
+    # hardware's (a step); then three products.  Where e stands alone it is off in e / (1 + e) by 6, else by at most half
+    # of that.
+    R.near(act, v, np.abs(v) * 12 * R.F32 * (1 + 1e-5) + 1e-45, "act")
+    m = np.abs(v).max(1)
+    R.near(s, m / 127, m / 127 * 13 * R.F32 * (1 + 1e-5) + 1e-45, "scale")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gate_of_values_that_are_not_finite(L, dtype):
+    """act is the formula's value there: inf * u, and no number where the quotient is inf / inf."""
+    both = torch.ones((1, 32), dtype=dtype, device="cuda")
+    both[0, :7] = torch.tensor([torch.inf, torch.inf, torch.inf, -torch.inf, torch.nan, 3e38, -3e38])
+    both[0, 16:23] = torch.tensor([2.0, -1.0, 0.0, 1.0, 1.0, 1.0, 1.0])
+    act = torch.empty((1, 16), dtype=dtype, device="cuda")
+    q, s = L.lora_quantize(both, activation="silu_mul", act=act)
+    want = torch.tensor([torch.inf, -torch.inf, torch.nan, torch.nan, torch.nan, float(both[0, 5]), 0.0], dtype=dtype)
+    assert torch.equal(act[0, :7].cpu().nan_to_num(nan=7.0, posinf=1e3, neginf=-1e3), want.nan_to_num(nan=7.0, posinf=1e3, neginf=-1e3))
+    assert bool(s.isnan().all()) and not q.any()
