@@ -630,7 +630,8 @@ lora_status lora_quantize(const void *d_x, int64_t ldx, int64_t num_rows, int64_
  * Supported: d_in a multiple of 16, at most 131056 (the int32 sum of a row then cannot
  * overflow), d_out a multiple of 8, at most 2^24, num_experts in [1, 1023] (1 for a dense
  * layer), strides multiples of 16, (a block of 256 rows is addressed with 32-bit offsets:)
- * row_stride below 2^23, ptr 16-byte aligned. */
+ * row_stride below 2^23, ptr 16-byte aligned.  Matrices do not overlap: they lie one after the
+ * other, or side by side (expert_stride at least d_in, row_stride past the last expert's row). */
 typedef struct lora_int8_weight {
     const int8_t *ptr;
     int64_t expert_stride, row_stride;   /* bytes */

@@ -868,9 +868,10 @@ def lora_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.T
 
 
 class Int8Weight:
-    """8-bit base weights: w int8 [d_out][d_in], or [experts][d_out][d_in] (rows and
-    experts of any stride, bytes of a row contiguous), scale float32 [d_out] or
-    [experts][d_out], bias likewise or None."""
+    """8-bit base weights: w int8 [d_out][d_in], or [experts][d_out][d_in] (bytes of a row
+    contiguous; strides multiples of 16; experts one after the other or side by side, as
+    in a transposed [d_out][experts][d_in]), scale float32 [d_out] or [experts][d_out],
+    bias likewise or None."""
 
     def __init__(self, w: torch.Tensor, scale: torch.Tensor, bias: torch.Tensor | None = None):
         if w.dim() not in (2, 3) or w.dtype != torch.int8 or w.stride(-1) != 1:

@@ -31,7 +31,12 @@ lora_status check_weight(const lora_int8_weight *w) {
   if (w->row_stride % 16 || w->row_stride < w->d_in || w->expert_stride % 16) return LORA_ERR_INVALID_ARG;
   if (w->num_experts > kMaxSlots || w->d_in > kMaxDepth || w->d_out > kMaxWidth || w->row_stride >= (1 << 23))
     return LORA_ERR_UNSUPPORTED;
-  if (w->num_experts > 1 && w->expert_stride < (w->d_out - 1) * w->row_stride + w->d_in) return LORA_ERR_INVALID_ARG;
+  if (w->num_experts > 1) {
+    // matrices that do not overlap: one after the other, or side by side in longer rows
+    const bool apart = w->expert_stride >= (w->d_out - 1) * w->row_stride + w->d_in;
+    const bool beside = !apart && w->expert_stride >= w->d_in && w->row_stride >= (w->num_experts - 1) * w->expert_stride + w->d_in;
+    if (!apart && !beside) return LORA_ERR_INVALID_ARG;
+  }
   return LORA_OK;
 }
 

@@ -172,3 +172,13 @@ def test_an_activation_that_is_none_is_not_written():
     for kw in (dict(a=P, lda=64), dict(a=P, lda=64, rows=1), dict(a=P, lda=128, m=meta(0))):
         assert quantize(**kw) == INVALID, kw
     assert quantize(act=1, ldx=128, a=P, lda=64) == OK
+
+
+def test_experts_side_by_side():
+    """Matrices in each other's gaps are taken, overlapping ones refused."""
+    n = C.c_size_t(7)
+    ask = lambda **kw: L._lib.lora_int8_matmul_workspace_bytes(1, weight(num_experts=4, **kw), C.byref(n))  # noqa: E731
+    assert ask(expert_stride=64, row_stride=256) == OK and ask(expert_stride=80, row_stride=304) == OK
+    assert ask(expert_stride=2048, row_stride=64) == OK
+    for es, rs in ((48, 256), (64, 240), (80, 288), (0, 64), (0, 256), (64, 64), (-64, 256), (256, 256), (-2048, 64)):
+        assert ask(expert_stride=es, row_stride=rs) == INVALID, (es, rs)

@@ -284,3 +284,16 @@ def test_two_threads(L):
     for t in threads:
         t.join()
     assert not wrong, wrong
+
+
+def test_experts_side_by_side(L):
+    """Experts whose rows lie between each other's, as a transposed [d_out][experts][d_in] holds them."""
+    g = torch.Generator("cuda").manual_seed(13)
+    for rows, d_in, d_out, experts in ((300, 272, 200, 3), (1200, 528, 264, 4), (20, 128, 40, 5)):
+        x, xs, w, ws, _ = made(g, rows, d_in, d_out, experts)
+        slots = torch.randint(0, experts, (rows,), generator=g, device="cuda", dtype=torch.int32)
+        want, bound = R.int8_matmul(x, xs, w, ws, None, slots.cpu().numpy(), np.arange(rows), torch.float32)
+        between = w.transpose(0, 1).contiguous().transpose(0, 1)
+        assert between.stride() == (d_in, experts * d_in, 1)
+        y = L.lora_int8_matmul(x, xs, L.Int8Weight(between, ws), meta=L.lora_prepare_meta(slots, experts), dtype=torch.float32)
+        R.near(y, want, bound)
