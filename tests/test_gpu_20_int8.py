@@ -297,3 +297,80 @@ def test_experts_side_by_side(L):
         assert between.stride() == (d_in, experts * d_in, 1)
         y = L.lora_int8_matmul(x, xs, L.Int8Weight(between, ws), meta=L.lora_prepare_meta(slots, experts), dtype=torch.float32)
         R.near(y, want, bound)
+
+
+# d_in of 1, 2, 3, 4, 5, 6, 9 and 10 stages of 128 bytes, the last one whole or not
+STAGES = [16, 144, 384, 512, 528, 656, 1040, 1280]
+
+
+@pytest.mark.parametrize("d_in", STAGES)
+@pytest.mark.parametrize("rows,d_out", [(1025, 3080), (2100, 3848)])
+def test_dense_large_tiles(L, rows, d_out, d_in):
+    """More than 768 tiles of 64 x 64: tiles of 128, and beyond 128 of 256 x 256 those."""
+    g = torch.Generator("cuda").manual_seed(d_in)
+    args = made(g, rows, d_in, d_out, bias=d_in % 32 == 0)
+    for dtype in DTYPES:
+        dense(L, *args, dtype)
+
+
+def test_dense_more_tiles_than_workgroups(L):
+    """306 tiles of 256 x 256, for one workgroup on each of 256 CUs."""
+    g = torch.Generator("cuda").manual_seed(14)
+    args = made(g, 4100, 1040, 4360, bias=True)
+    for dtype in DTYPES:
+        dense(L, *args, dtype)
+
+
+@pytest.mark.parametrize("d_in", STAGES)
+def test_by_expert_large_tiles(L, d_in):
+    """More than 160 rows a segment: tiles of 256 x 256."""
+    for per_pair, dtype in ((False, torch.bfloat16), (True, torch.float32)):
+        by_expert(L, 1100, 2, 5, 4, 1, d_in, 520, per_pair, dtype, 0.2, seed=d_in, bias=True)
+
+
+@pytest.mark.parametrize("T,topk,E,local,d_in,d_out,skew", [
+    (2000, 2, 4, 4, 1040, 4360, 0.0),       # 306 tiles of 256
+    (1000, 4, 40, 32, 528, 2200, 0.0),      # 576 items of 128: segments of more than 16 rows go to tiles, and some workgroups take two
+    (1000, 4, 40, 32, 656, 2200, 0.12),     # the same with segments below 16 rows and above 128
+    (500, 4, 40, 32, 1040, 2064, 0.0)])     # half a tile each
+def test_by_expert_many_tiles(L, T, topk, E, local, d_in, d_out, skew):
+    for per_pair, dtype in ((False, torch.bfloat16), (True, torch.float32)):
+        by_expert(L, T, topk, E, local, 0, d_in, d_out, per_pair, dtype, skew, seed=T + d_in, bias=True)
+
+
+def test_two_threads_in_every_kernel(L):
+    """Two threads, each on a stream of its own, with calls that go to each kernel: dense ones of few rows, in tiles of 64, 128
+    and 256, and by expert in those of few rows, 128 and 256."""
+    import threading
+    g = torch.Generator("cuda").manual_seed(15)
+    cases = []
+    for rows, d_out, experts in ((3, 64, 0), (200, 640, 0), (900, 4096, 0), (5000, 4096, 0), (40, 256, 8), (3300, 2200, 32), (1500, 520, 4)):
+        x, xs, w, ws, b = made(g, rows, 272, d_out, experts or None, bias=True)
+        expert, meta = np.zeros(rows, np.int64), None
+        if experts:
+            slots = torch.randint(0, experts, (rows,), generator=g, device="cuda", dtype=torch.int32)
+            expert, meta = slots.cpu().numpy(), L.lora_prepare_meta(slots, experts)
+        weight = L.Int8Weight(w, ws, bias=b)
+        y = L.lora_int8_matmul(x, xs, weight, meta=meta)
+        want, bound = R.int8_matmul(x, xs, w, ws, b, expert, np.arange(rows), y.dtype)
+        R.near(y, want, bound, f"{rows} rows, {experts} experts")
+        cases.append((x, xs, weight, meta, y))
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(10):
+                for i, (x, xs, weight, meta, want) in enumerate(cases):
+                    y = L.lora_int8_matmul(x, xs, weight, meta=meta)
+                    stream.synchronize()
+                    if not torch.equal(y, want):
+                        wrong.append(i)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
