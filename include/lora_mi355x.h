@@ -550,8 +550,7 @@ lora_status lora_attention(const lora_attn_meta *meta, const void *d_q, int64_t 
  * weights are 8-bit integers, dense or by expert, and what a MoE layer needs around
  * it: the choice of experts (which lora_prepare_moe_meta takes), the rows' 8-bit
  * form, the gated activation between the two products, the weighted sum of a token's
- * choices.  None of them allocates or needs an initialised workspace; calls on one
- * stream may share one.
+ * choices.  None of them allocates or uses a workspace.
  * ------------------------------------------------------------------------- */
 
 typedef enum lora_score {
@@ -642,8 +641,8 @@ typedef struct lora_int8_weight {
     int32_t reserved;               /* must be 0 */
 } lora_int8_weight;
 
-/* Device workspace of lora_int8_matmul for num_rows rows of y (a larger call's serves a
- * smaller one). */
+/* Device workspace of lora_int8_matmul for num_rows rows of y: 0 bytes, no form needs one (its
+ * d_ws and ws_bytes are not read).  Refuses what the call refuses of these arguments. */
 lora_status lora_int8_matmul_workspace_bytes(int64_t num_rows, const lora_int8_weight *w,
                                              size_t *bytes);
 

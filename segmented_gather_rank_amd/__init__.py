@@ -889,6 +889,7 @@ class Int8Weight:
 
 
 def lora_int8_matmul_workspace_bytes(num_rows: int, weight: Int8Weight) -> int:
+    """Bytes of lora_int8_matmul's workspace: 0, no form needs one."""
     b = _sz(0)
     _check("lora_int8_matmul_workspace_bytes", _lib.lora_int8_matmul_workspace_bytes(num_rows, weight.ref, C.byref(b)))
     return int(b.value)
@@ -900,7 +901,8 @@ def lora_int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, weight: Int8Weight,
     """out[i] = (x[i] @ w.T) * x_scale[i] * w_scale (+ bias), x int8 [rows][d_in] as
     lora_quantize leaves it.  meta: metadata of the output's rows, keyed by expert (row i
     of the output reads row i / x_row_div of x; rows without a key are not written).  An
-    out that is not given is allocated on the stream of the call, of type dtype."""
+    out that is not given is allocated on the stream of the call, of type dtype.  No form
+    needs a workspace."""
     device = x.get_device()
     if _elsewhere(device):
         with torch.cuda.device(device):
@@ -915,10 +917,6 @@ def lora_int8_matmul(x: torch.Tensor, x_scale: torch.Tensor, weight: Int8Weight,
     xp, ldx = _rows(x, "x", torch.int8, x_rows, weight.d_in)
     if out is None:
         out = _empty_for(stream, (rows, weight.d_out), dtype, x.device)
-    if workspace is None:
-        need = lora_int8_matmul_workspace_bytes(rows, weight)
-        if need:
-            workspace = _empty_for(stream, need, torch.uint8, x.device)
     _apart(device, x_scale, weight.w, out, workspace, None if meta is None else meta.workspace)
     yp, ldy = _rows(out, "out", out.dtype, rows, weight.d_out)
     st = _lib.lora_int8_matmul(None if meta is None else C.byref(meta.c), xp, ldx,

@@ -133,7 +133,7 @@ lora_status lora_int8_matmul_workspace_bytes(int64_t num_rows, const lora_int8_w
 
 lora_status lora_int8_matmul(const lora_meta *meta, const int8_t *d_x, int64_t ldx, const float *d_x_scale,
                              int64_t num_rows, const lora_int8_weight *w, void *d_y, int64_t ldy, lora_dtype dtype,
-                             void *d_ws, size_t ws_bytes, void *stream) {
+                             void *, size_t, void *stream) {  // no form needs a workspace
   size_t need = 0;
   lora_status st = lora_int8_matmul_workspace_bytes(num_rows, w, &need);
   if (st != LORA_OK) return st;
@@ -149,7 +149,6 @@ lora_status lora_int8_matmul(const lora_meta *meta, const int8_t *d_x, int64_t l
   }
   if (num_rows == 0) return LORA_OK;
   if (!d_x || !d_x_scale || !d_y) return LORA_ERR_INVALID_ARG;
-  if (ws_bytes < need || (need && (!d_ws || !aligned16(d_ws)))) return LORA_ERR_WORKSPACE;
   Int8Args a{};
   a.x = d_x;
   a.w = w->ptr;
