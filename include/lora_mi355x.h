@@ -589,7 +589,7 @@ typedef struct lora_routing {
 
 /* Expert choices of every token.
  *   d_logits      device [T][ld] of dtype (fp32 or bf16), num_experts columns; any ld
- *                 and alignment of whole elements
+ *                 of at least that, any alignment of whole elements
  *   d_topk_ids    device int32 [T][topk], contiguous: as lora_prepare_moe_meta takes it
  *   d_weights     device fp32 [T][topk], contiguous */
 lora_status lora_moe_route(const lora_routing *routing, const void *d_logits, int64_t ld,
@@ -658,7 +658,8 @@ lora_status lora_int8_matmul_workspace_bytes(int64_t num_rows, const lora_int8_w
  *   d_x_scale     device fp32, one for each row of x
  *   d_y           device [num_rows][ldy] of dtype (fp32 or bf16), d_out columns
  * ldx is a multiple of 16, ldy of 8; x and y are 16-byte aligned.  num_rows is at most
- * 2^24. */
+ * 2^24.  (With metadata, an x that spans 4 GiB or more is multiplied 64 rows of a segment
+ * after the other, far slower than in tiles.) */
 lora_status lora_int8_matmul(const lora_meta *meta, const int8_t *d_x, int64_t ldx,
                              const float *d_x_scale, int64_t num_rows,
                              const lora_int8_weight *w, void *d_y, int64_t ldy, lora_dtype dtype,

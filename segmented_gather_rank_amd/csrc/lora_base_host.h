@@ -45,7 +45,7 @@ struct Int8Args {
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s);
 // A dense batch in tiles of 64 rows.
 hipError_t launch_int8_mid(const Int8Args &a, bool bf16, hipStream_t s);
-// A dense batch in tiles of 256 rows; by expert, the segments that are not few_kernel's.
+// A dense batch in tiles of 128 or 256 rows; by expert, the segments that are not few_kernel's, in either.
 hipError_t launch_int8_tile(const Int8Args &a, bool bf16, hipStream_t s);
 
 // By expert, rows decide who takes a segment, and only the device knows them.  Every kernel
@@ -56,7 +56,8 @@ hipError_t launch_int8_tile(const Int8Args &a, bool bf16, hipStream_t s);
 //   large whether the others take tiles of 256, else of 128: from 160 rows a segment on.
 //         (Long and short segments in tiles of their own, one kernel after the other, are
 //         slower than either for all: 113 rows a segment on average 178 us for 165, all in
-//         tiles of 256: 169; 226 rows 240 us for 207.)
+//         tiles of 256: 169; 226 rows 240 us for 207.  Between 113 and 226 rows, and with
+//         counts more uneven than a normal router's, nothing was timed.)
 constexpr int kFewRows = 64;
 struct ExpertRule {
   int few;

@@ -9,10 +9,11 @@
 // waves take d_in in turn, 128 bytes of every row a step, straight from memory to the
 // matrix cores' registers (few rows use a weight once, there is nothing to share); the
 // waves' sums meet in LDS.  Bound: HBM reads of the weights.  The experts of a decode step
-// (256 tokens, an eighth of their 8 choices of 256 here, 7168 x 4096 each): 158 us, 5.6 TB/s;
-// one row x 4096 x 4096: 5.4 us, 3.1 TB/s, the chain of loads, sums and barrier.  Loads by
-// buffer take 32-bit offsets, which leaves registers for two workgroups a CU (by address
-// 183 us).  Segments of a workgroup's own number that others take cost a workgroup that
+// (256 tokens, an eighth of their 8 choices of 256 here, 7168 x 4096 each): 165 us a call,
+// 5.4 TB/s; one row x 4096 x 4096: 5.4 us, 3.1 TB/s, the chain of loads, sums and barrier.
+// Dense batches x 4096 x 6144: 1 row 8 us, 16 rows 11, 32 rows 14, and 64 rows 21, as beyond
+// 32 rows registers let a wave load one step ahead only.  Loads by buffer take 32-bit
+// offsets, which leaves registers for two workgroups a CU (by address 183 us).  Segments of a workgroup's own number that others take cost a workgroup that
 // ends at once, 2 ns each; a workgroup for four segments ends them sooner, but evens the
 // load of a decode step out less (181 us for 165).
 #include <algorithm>
@@ -232,7 +233,8 @@ hipError_t launch_few(const Int8Args &a, bool all, bool wide, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_int8(const Int8Args &a, bool bf16, hipStream_t s) {
-  // x is addressed in 32 bits: all of it, or in tiles of a dense batch their 256 rows
+  // x is addressed in 32 bits: all of it, or in tiles of a dense batch their 256 rows.  Where that does not reach,
+  // few_kernel takes all, 64 rows of a segment after the other, in the time of that.
   const int64_t x_rows = a.meta.sorted ? (a.rows - 1) / a.meta.x_row_div + 1 : a.rows;
   const bool wide = x_rows * a.ldx >= ((int64_t)1 << 32) - 256;
   const bool tiles = a.meta.sorted ? !wide : 256 * a.ldx < ((int64_t)1 << 32) - 256;

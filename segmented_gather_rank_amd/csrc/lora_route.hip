@@ -20,10 +20,15 @@
 //
 // Bound: vector instructions, some 350 a token of 256 experts (scores and keys of 16 a
 // lane, the groups' two largest, the bound), not its 1 KB.  17705 tokens x 256 experts
-// fp32, 8 choices in 4 of 8 groups, with bias: 20.8 us a call, of which the tokens that are
-// done again take 2; 4609 x 60 bf16, 4 choices: 4.7; one token of 256: 6.5, four dependent
-// loads and the way through.  Four waves a SIMD (128 registers) measure as three do
-// (21.1 us both; 60 experts 6.1 and 6.4 then); five spill, 29 us.
+// fp32, 8 choices in 4 of 8 groups, with bias: 21.2 us a call, of which the tokens that are
+// done again take 2; softmax without groups or bias: 10 us, 13 where weights are not
+// renormalised; 4609 x 60 bf16, 4 choices: 4.7; one token of 256: 6.5, four dependent loads
+// and the way through.  A wave a token: 4608 x 1024, 10 choices: 22 us, 17705 x 256, 32
+// choices: 46, a chain of two folds a choice.
+//
+// Four waves a SIMD leave 128 registers, of which those of 256 experts spill 9 (bf16: 12), 40
+// and 52 bytes a lane, since the pass in 64 bits is compiled into the kernel.  (Before it was,
+// three waves measured as four, 21.1 us; five, 29.)
 #include <algorithm>
 #include <cmath>
 
@@ -132,10 +137,12 @@ struct Token {
 
 // How near two values in 32 bits may be for their order to stand: twice a value's error.
 // s is within 30 * 2^-24 of its size (the exponential, sums of 16 a lane and of the lanes,
-// the quotient) and, by the exponent's argument z and the logarithm's own step, 1.5 |z| *
-// 2^-24, up to |z| = 104 where the exponential ends (below 1e-38 it is 0).  With a bias,
-// whose sum adds half a step, the argument's part is at most |z| e^-|z| < 0.4 steps of 1,
-// and s at most 1.  `unit`: what v counts 1 as.
+// the quotient) and, by the exponent's argument z (its difference, its product with log2 e
+// and that number's own rounding), 2.3 |z| * 2^-24.  2 (30 + 2.3 |z|) is below 400 up to |z|
+// = 73; from there on s is below 2e-32, and what is missing up to |z| = 104, where the
+// exponential ends (below 1e-38 it is 0), below the 1e-36.  With a bias, whose sum adds a
+// rounding of c, the argument's part is at most 2.3 |z| e^-|z| < 0.9 steps of 1, and s at
+// most 1.  `unit`: what v counts 1 as.
 __device__ __forceinline__ float near(float v, bool biased, float unit = 1.f) {
   return biased ? 64.f * 0x1p-24f * (unit + fabsf(v)) : 400.f * 0x1p-24f * fabsf(v) + 1e-36f * unit;
 }
