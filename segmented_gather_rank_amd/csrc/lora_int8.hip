@@ -13,9 +13,10 @@
 // 5.4 TB/s; one row x 4096 x 4096: 5.4 us, 3.1 TB/s, the chain of loads, sums and barrier.
 // Dense batches x 4096 x 6144: 1 row 8 us, 16 rows 11, 32 rows 14, and 64 rows 21, as beyond
 // 32 rows registers let a wave load one step ahead only.  Loads by buffer take 32-bit
-// offsets, which leaves registers for two workgroups a CU (by address 183 us).  Segments of a workgroup's own number that others take cost a workgroup that
-// ends at once, 2 ns each; a workgroup for four segments ends them sooner, but evens the
-// load of a decode step out less (181 us for 165).
+// offsets, which leaves registers for two workgroups a CU (by address 183 us).  Segments of
+// a workgroup's own number that others take cost a workgroup that ends at once, 2 ns each;
+// a workgroup for four segments ends them sooner, but evens the load of a decode step out
+// less (181 us for 165).
 #include <algorithm>
 
 #include "lora_base_host.h"
